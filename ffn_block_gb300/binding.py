@@ -60,6 +60,15 @@ class rmx_device_io(ctypes.Structure):
                 ("dx", ctypes.c_void_p)]
 
 
+class rmx_rows(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("cols", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class rmx_layer(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("G", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
+
+
 _VP, _SZ, _I, _P = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.POINTER
 _SIGNATURES = {
     "rmx_saved_bytes": (_SZ, [_P(rmx_config)]),
@@ -83,6 +92,18 @@ _SIGNATURES = {
                               _SZ, _P(_VP)]),
     "rmx_graph_launch": (_I, [_VP, _VP]),
     "rmx_graph_destroy": (_I, [_VP]),
+    "rmx_q8_pitch": (_I, [_I]),
+    "rmx_rms_norm_q8": (_I, [_P(rmx_rows), ctypes.c_float] + [_VP] * 9),
+    "rmx_rms_norm_backward_workspace_bytes": (_SZ, [_P(rmx_rows)]),
+    "rmx_rms_norm_backward": (_I, [_P(rmx_rows)] + [_VP] * 10 + [_SZ, _VP]),
+    "rmx_quant_rows_q8": (_I, [_P(rmx_rows)] + [_VP] * 4),
+    "rmx_dequant_rows_q8": (_I, [_P(rmx_rows)] + [_VP] * 4),
+    "rmx_weight_q8": (_I, [_P(rmx_layer)] + [_VP] * 4),
+    "rmx_linear_q8": (_I, [_P(rmx_layer)] + [_VP] * 8),
+    "rmx_ckpt8_pack": (_I, [_P(rmx_rows)] + [_VP] * 4),
+    "rmx_ckpt8_unpack": (_I, [_P(rmx_rows)] + [_VP] * 4),
+    "rmx_ckpt8_wgrad_workspace_bytes": (_SZ, [_P(rmx_layer)]),
+    "rmx_ckpt8_wgrad": (_I, [_P(rmx_layer)] + [_VP] * 6 + [_SZ, _VP]),
 }
 
 _lib = None
@@ -238,3 +259,71 @@ def rmx_graph_launch(g: int, stream=None) -> int:
 
 def rmx_graph_destroy(g: int) -> int:
     return lib().rmx_graph_destroy(g)
+
+
+# ------------------------------------------------------------------ 8-bit operators
+
+def _code(dtype: str | int) -> int:
+    return DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+
+
+def make_rows(rows: int, cols: int, dtype: str | int) -> rmx_rows:
+    return rmx_rows(rows, cols, _code(dtype))
+
+
+def make_layer(M: int, G: int, K: int, N: int, dtype: str | int) -> rmx_layer:
+    return rmx_layer(M, G, K, N, _code(dtype))
+
+
+def rmx_q8_pitch(cols: int) -> int:
+    return lib().rmx_q8_pitch(cols)
+
+
+def rmx_rms_norm_q8(shape: rmx_rows, eps: float, x, r, gamma, h, y, q, scale, rstd, stream=None) -> int:
+    return lib().rmx_rms_norm_q8(ctypes.byref(shape), eps, _ptr(x), _ptr(r), _ptr(gamma), _ptr(h), _ptr(y), _ptr(q),
+                                 _ptr(scale), _ptr(rstd), _stream(stream))
+
+
+def rmx_rms_norm_backward_workspace_bytes(shape: rmx_rows) -> int:
+    return lib().rmx_rms_norm_backward_workspace_bytes(ctypes.byref(shape))
+
+
+def rmx_rms_norm_backward(shape: rmx_rows, dn, dh, h, q, exps, rstd, gamma, dx, dgamma, ws, ws_bytes: int,
+                          stream=None) -> int:
+    return lib().rmx_rms_norm_backward(ctypes.byref(shape), _ptr(dn), _ptr(dh), _ptr(h), _ptr(q), _ptr(exps),
+                                       _ptr(rstd), _ptr(gamma), _ptr(dx), _ptr(dgamma), _ptr(ws), ws_bytes,
+                                       _stream(stream))
+
+
+def rmx_quant_rows_q8(shape: rmx_rows, x, q, scale, stream=None) -> int:
+    return lib().rmx_quant_rows_q8(ctypes.byref(shape), _ptr(x), _ptr(q), _ptr(scale), _stream(stream))
+
+
+def rmx_dequant_rows_q8(shape: rmx_rows, q, scale, x, stream=None) -> int:
+    return lib().rmx_dequant_rows_q8(ctypes.byref(shape), _ptr(q), _ptr(scale), _ptr(x), _stream(stream))
+
+
+def rmx_weight_q8(layer: rmx_layer, w, q, scale, stream=None) -> int:
+    return lib().rmx_weight_q8(ctypes.byref(layer), _ptr(w), _ptr(q), _ptr(scale), _stream(stream))
+
+
+def rmx_linear_q8(layer: rmx_layer, a, a_scale, w, w_scale, bias, resid, out, stream=None) -> int:
+    return lib().rmx_linear_q8(ctypes.byref(layer), _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(bias),
+                               _ptr(resid), _ptr(out), _stream(stream))
+
+
+def rmx_ckpt8_pack(shape: rmx_rows, x, q, exps, stream=None) -> int:
+    return lib().rmx_ckpt8_pack(ctypes.byref(shape), _ptr(x), _ptr(q), _ptr(exps), _stream(stream))
+
+
+def rmx_ckpt8_unpack(shape: rmx_rows, q, exps, x, stream=None) -> int:
+    return lib().rmx_ckpt8_unpack(ctypes.byref(shape), _ptr(q), _ptr(exps), _ptr(x), _stream(stream))
+
+
+def rmx_ckpt8_wgrad_workspace_bytes(layer: rmx_layer) -> int:
+    return lib().rmx_ckpt8_wgrad_workspace_bytes(ctypes.byref(layer))
+
+
+def rmx_ckpt8_wgrad(layer: rmx_layer, q, exps, dy, dw, db, ws, ws_bytes: int, stream=None) -> int:
+    return lib().rmx_ckpt8_wgrad(ctypes.byref(layer), _ptr(q), _ptr(exps), _ptr(dy), _ptr(dw), _ptr(db), _ptr(ws),
+                                 ws_bytes, _stream(stream))

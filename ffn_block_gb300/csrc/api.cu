@@ -30,9 +30,8 @@
 #include <string>
 #include <vector>
 
-#include "../../include/rmx.h"
+#include "api.h"
 #include "common.cuh"
-#include "kernels.h"
 
 namespace rmx {
 
@@ -279,8 +278,6 @@ rmx_status kernels_support(const rmx_config& c) {
   return RMX_OK;
 }
 
-bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 rmx_status check_params(const rmx_params* p) {
   if (!p) return RMX_ERR_INVALID_ARG;
   const void* v[] = {p->w1, p->b1, p->wout, p->bout, p->gamma0, p->beta0, p->gamma1,
@@ -300,12 +297,6 @@ rmx_status check_grads(const rmx_grads* g) {
     if (!q) return RMX_ERR_INVALID_ARG;
     if (!aligned16(q)) return RMX_ERR_ALIGNMENT;
   }
-  return RMX_OK;
-}
-
-rmx_status check_ptr(const void* p) {
-  if (!p) return RMX_ERR_INVALID_ARG;
-  if (!aligned16(p)) return RMX_ERR_ALIGNMENT;
   return RMX_OK;
 }
 
@@ -338,40 +329,35 @@ bool selected(const char* name) {
   return g_prof_only.empty() || g_prof_only == name;
 }
 
-// Brackets one kernel launch: counts it and, when profiling is on (for its
-// name), records events around it on its stream.
-class Launch {
- public:
-  Launch(const char* name, cudaStream_t st) : name_(name), st_(st) {
-    if (g_prof.load() && selected(name)) {
-      a_ = pool_event();
-      if (a_) cudaEventRecord(a_, st_);
+}  // namespace
+
+Launch::Launch(const char* name, cudaStream_t st) : name_(name), st_(st) {
+  if (g_prof.load() && selected(name)) {
+    a_ = pool_event();
+    if (a_) cudaEventRecord(a_, st_);
+  }
+}
+rmx_status Launch::done(cudaError_t e) {
+  g_launches.fetch_add(1);
+  if (a_) {
+    cudaEvent_t b = pool_event();
+    if (b) {
+      cudaEventRecord(b, st_);
+      std::lock_guard<std::mutex> lk(g_mu);
+      g_recs.push_back({name_, a_, b});
     }
   }
-  rmx_status done(cudaError_t e) {
-    g_launches.fetch_add(1);
-    if (a_) {
-      cudaEvent_t b = pool_event();
-      if (b) {
-        cudaEventRecord(b, st_);
-        std::lock_guard<std::mutex> lk(g_mu);
-        g_recs.push_back({name_, a_, b});
-      }
-    }
-    return e == cudaSuccess ? RMX_OK : RMX_ERR_CUDA;
-  }
+  return e == cudaSuccess ? RMX_OK : RMX_ERR_CUDA;
+}
 
- private:
-  const char* name_;
-  cudaStream_t st_;
-  cudaEvent_t a_ = nullptr;
-};
+bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+rmx_status check_ptr(const void* p) {
+  if (!p) return RMX_ERR_INVALID_ARG;
+  if (!aligned16(p)) return RMX_ERR_ALIGNMENT;
+  return RMX_OK;
+}
 
-#define RMX_TRY(expr)                  \
-  do {                                 \
-    rmx_status s_ = (expr);            \
-    if (s_ != RMX_OK) return s_;       \
-  } while (0)
+namespace {
 
 // Profile name of a GEMM that runs on the CUDA cores (the strict fp32
 // contract, or a 16-bit shape the tensor-core engine does not take).
@@ -380,7 +366,7 @@ const char* ffma_label(const char* name) {
       {"gemm1_fwd", "gemm1_fwd.ffma"},     {"gemm2_fwd", "gemm2_fwd.ffma"},
       {"gemm1_dgrad", "gemm1_dgrad.ffma"}, {"gemm2_dgrad", "gemm2_dgrad.ffma"},
       {"gemm1_wgrad", "gemm1_wgrad.ffma"}, {"gemm2_wgrad", "gemm2_wgrad.ffma"},
-      {"test_gemm", "test_gemm.ffma"},
+      {"test_gemm", "test_gemm.ffma"},     {"ckpt8_wgrad", "ckpt8_wgrad.ffma"},
   };
   for (const auto& n : kNames)
     if (std::strcmp(n[0], name) == 0) return n[1];
@@ -392,12 +378,16 @@ const char* ffma_label(const char* name) {
 // cores.
 bool tc_engine(const GemmDesc& d) { return (d.dtype != RMX_F32 || d.tf32) && gemm_tc_supported(d); }
 
+}  // namespace
+
 rmx_status run_gemm(const char* name, const GemmDesc& d, cudaStream_t st) {
   const bool tc = tc_engine(d);
   Launch l(tc ? name : ffma_label(name), st);
   const cudaError_t e = tc ? gemm_tc_launch(d, device_error_word(), st) : gemm_simt_launch(d, st);
   return l.done(e);
 }
+
+namespace {
 
 // Copy stream of rmx_step_host, one per device, created on first use; the
 // events are shared, so a call's enqueue sequence holds g_copy_mu.

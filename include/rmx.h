@@ -252,6 +252,123 @@ rmx_status rmx_ln2_backward_noalloc(const rmx_config* cfg, const void* dy, const
                                     void* ds2, void* dgamma2, void* dbeta2, void* dbout,
                                     rmx_stream stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit operators: a per-token layer served and trained with 8-bit
+ * activations and weights.
+ *
+ *   x (+ r) -> rmx_rms_norm_q8 -> int8 rows -> rmx_linear_q8 -> out
+ *   backward: rmx_ckpt8_wgrad (from the checkpoint of the layer's input),
+ *             rmx_rms_norm_backward (from the checkpoint of x + r)
+ *
+ * Two 8-bit formats.  Both keep a row of C columns in P = rmx_q8_pitch(C)
+ * bytes (C rounded up to a multiple of 32), the columns C .. P-1 zero:
+ *   q8 rows        value = q * scale[row], one float32 scale per row,
+ *                  scale = max|row| / 127, q in [-127, 127].  A zero row has
+ *                  scale 0; a row that holds an infinity or a NaN has scale
+ *                  NaN and q 0.
+ *   checkpoint     value = q * 2^e, one int8 exponent e per 32 columns
+ *                  (exps is [rows, P / 32]): the smallest e with max|group| /
+ *                  2^e <= 127.5, clamped to [-126, 121] (float32, bfloat16)
+ *                  or [-24, 9] (float16), so that every value is exact in the
+ *                  storage type, and q = round(x / 2^e), ties to even, in
+ *                  [-127, 127].  Values are off by at most half a step, 2^(e-1)
+ *                  (one step where the upper clamp acts, and half a step of
+ *                  2^-126 or 2^-24 at the lower one).  A group that holds an
+ *                  infinity or a NaN has e = 127 and reads back as NaN.
+ *
+ * All of them follow the conventions above (caller-owned dense row-major
+ * device memory, 16-byte aligned pointers, enqueued on `stream`, arguments
+ * checked first, repeated calls bitwise identical).  dtype is RMX_F32,
+ * RMX_BF16 or RMX_F16.  Operators on the same buffers may run on any number
+ * of streams as long as no call writes what another one uses; a workspace
+ * belongs to one call at a time (two captured graphs that may run at once
+ * need one each).  Calls can be captured into CUDA graphs; make the first
+ * call on a device outside a capture. */
+
+/* Dense rows [rows, cols] of a storage type. */
+typedef struct {
+  long long rows;
+  int cols;
+  int dtype; /* RMX_F32, RMX_BF16 or RMX_F16 */
+} rmx_rows;
+
+/* A per-token linear layer: M samples, G tokens (groups), K inputs, N
+ * outputs.  Activations are [M, G, K] and [M, G, N], weights one [K, N] (or
+ * its transpose) per group. */
+typedef struct {
+  int M, G, K, N;
+  int dtype; /* storage type of out, bias, resid, dy, dw, db */
+} rmx_layer;
+
+/* Bytes of an 8-bit row of `cols` columns (a multiple of 32); 0 if cols < 1. */
+int rmx_q8_pitch(int cols);
+
+/* RMS norm with the residual's addition and an 8-bit output:
+ *   h = x + r;  rstd = 1 / sqrt(mean(h^2) + eps);  n = h * rstd * gamma
+ * x [rows, cols]; r (may be null) likewise; gamma [cols].  The sum, the
+ * statistics and n are float32; the norm is taken of the unrounded sum.
+ * Outputs: h [rows, cols] (null: not written), y = n in the storage type
+ * (null: not written), q and scale = n as q8 rows (both null: not written),
+ * rstd [rows] float32 (null: not written).  y or q must be given.
+ * h may be x or r itself; nothing else may overlap.  cols <= 16384. */
+rmx_status rmx_rms_norm_q8(const rmx_rows* shape, float eps, const void* x, const void* r, const void* gamma,
+                           void* h, void* y, int8_t* q, float* scale, float* rstd, rmx_stream stream);
+
+/* Backward of the norm for the gradient dn of its output (through an 8-bit
+ * output straight through): with xh = h * rstd,
+ *   dx = rstd * (dn * gamma - xh * mean(dn * gamma * xh)) + dh
+ *   dgamma = sum over rows of dn * xh
+ * dx is the gradient of x and of r.  dh [rows, cols] is the gradient that
+ * reaches the sum h from elsewhere (may be null).  The sum comes either as h
+ * in the storage type (q, exps null) or as its checkpoint (h null).  rstd
+ * [rows] is the forward's.  ws: rmx_rms_norm_backward_workspace_bytes.  dx may
+ * be dn or dh itself.  cols <= 16384.  rows == 0 writes a zero dgamma. */
+size_t rmx_rms_norm_backward_workspace_bytes(const rmx_rows* shape);
+rmx_status rmx_rms_norm_backward(const rmx_rows* shape, const void* dn, const void* dh, const void* h,
+                                 const int8_t* q, const int8_t* exps, const float* rstd, const void* gamma,
+                                 void* dx, void* dgamma, void* ws, size_t ws_bytes, rmx_stream stream);
+
+/* x [rows, cols] as q8 rows (cols <= 16384), and the values of q8 rows back
+ * in the storage type. */
+rmx_status rmx_quant_rows_q8(const rmx_rows* shape, const void* x, int8_t* q, float* scale, rmx_stream stream);
+rmx_status rmx_dequant_rows_q8(const rmx_rows* shape, const int8_t* q, const float* scale, void* x,
+                               rmx_stream stream);
+
+/* Weights of a layer for rmx_linear_q8: w [G, K, N] in the storage type ->
+ * q [G, N, P] (P = rmx_q8_pitch(K); transposed, so that a channel's inputs are
+ * contiguous) and scale [G, N] = max over K / 127.  Done once per weight
+ * update; zero channels and channels with an infinity or a NaN as for rows. */
+rmx_status rmx_weight_q8(const rmx_layer* layer, const void* w, int8_t* q, float* scale, rmx_stream stream);
+
+/* Product of int8 activations and weights with scales for each token and
+ * channel:
+ *   out[m,g,n] = (sum_k a[m,g,k] * w[g,n,k]) * a_scale[m,g] * w_scale[g,n]
+ *                + bias[g,n] + resid[m,g,n]
+ * a [M, G, P] and w [G, N, P] int8 in [-128, 127] with P = rmx_q8_pitch(K) and
+ * zero columns K .. P-1 (those of one operand suffice); a_scale [M, G] and
+ * w_scale [G, N] float32; bias [G, N] and resid, out [M, G, N] in the storage
+ * type (bias, resid may be null; out may be resid itself).  The integer sum
+ * is exact below 2^24 in magnitude; larger ones may round to the 24 bits of
+ * float32.  The rest is float32, rounded once. */
+rmx_status rmx_linear_q8(const rmx_layer* layer, const int8_t* a, const float* a_scale, const int8_t* w,
+                         const float* w_scale, const void* bias, const void* resid, void* out, rmx_stream stream);
+
+/* x [rows, cols] as an 8-bit checkpoint, and the checkpoint's values back in
+ * the storage type (exact: the type the checkpoint was packed from, or
+ * float32, holds every one of them). */
+rmx_status rmx_ckpt8_pack(const rmx_rows* shape, const void* x, int8_t* q, int8_t* exps, rmx_stream stream);
+rmx_status rmx_ckpt8_unpack(const rmx_rows* shape, const int8_t* q, const int8_t* exps, void* x, rmx_stream stream);
+
+/* Weight and bias gradient of a layer whose input was kept as a checkpoint:
+ *   dw[g] = X[:,g]^T @ dy[:,g],  db[g] = sum over m of dy[m,g]
+ * q [M, G, P], exps [M, G, P / 32] = X [M, G, K]; dy [M, G, N]; dw [G, K, N];
+ * db [G, N] (may be null).  Products in the storage type's arithmetic (16-bit
+ * types: tensor cores with float32 sums; RMX_F32: strict float32).  ws:
+ * rmx_ckpt8_wgrad_workspace_bytes.  M == 0 writes zeros. */
+size_t rmx_ckpt8_wgrad_workspace_bytes(const rmx_layer* layer);
+rmx_status rmx_ckpt8_wgrad(const rmx_layer* layer, const int8_t* q, const int8_t* exps, const void* dy, void* dw,
+                           void* db, void* ws, size_t ws_bytes, rmx_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
