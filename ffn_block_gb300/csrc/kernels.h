@@ -181,4 +181,9 @@ int sm_count();
 bool make_tensor_map_2d(CUtensorMap* m, const void* base, int dtype, uint64_t d0, uint64_t d1, uint64_t s1,
                         uint32_t b0, uint32_t b1);
 
+// Rank-3 tiled tensor map of bytes with 128-byte swizzle, dims innermost
+// first, box {128, b1, b2}; out-of-range bytes read as zero.
+bool make_tensor_map_rows8(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+                           uint64_t s2, uint32_t b1, uint32_t b2);
+
 }  // namespace rmx
