@@ -12,13 +12,13 @@
 // 208 tokens.  The bound is the tensor rate from about 150 tokens on, the
 // stream of the weights below.
 //
-// Roles (22 warps, one CTA per SM, persistent over tiles):
+// Roles (30 warps, one CTA per SM, persistent over tiles):
 //   warp 0       TMA producer: 128 k of the CTA's channels and tokens a stage
 //   warp 1       TMEM allocation; one thread issues the MMAs (even CTA)
-//   warps 2-17   two sets, one for each half of a stage, of four warps for
-//                the weights (one channel a thread, 64 k, int8 -> TMEM) and
-//                four for the tokens (one token a thread, 64 k, int8 -> smem)
-//   warps 18-21  epilogue: a channel a thread, 32 tokens at a time
+//   warps 2-25   three sets, taking 64 k in turn, of four warps for the
+//                weights (one channel a thread, int8 -> TMEM) and four for
+//                the tokens (one token a thread, int8 -> smem)
+//   warps 26-29  epilogue: a channel a thread, 16 tokens at a time
 // TMEM: two accumulators of NT <= 208 columns (so that the epilogue of one
 // tile overlaps the next), then the weights' stages of 32 columns.
 //
@@ -39,7 +39,7 @@
 namespace rmx {
 namespace {
 
-constexpr int kWWarps = 4, kTWarps = 4, kSets = 2, kEpiWarps = 4;
+constexpr int kWWarps = 4, kTWarps = 4, kSets = 3, kEpiWarps = 4;
 constexpr int kFirstConv = 2, kFirstEpi = kFirstConv + kSets * (kWWarps + kTWarps);
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kRawK = 128, kConvK = 64;
@@ -138,13 +138,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.raw_stages * p.raw_bytes + p.conv_stages * p.conv_bytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxRaw + 2 * kMaxConv + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  auto raw_full = [&](int s) { return smem_u32(bars + s); };
-  auto raw_empty = [&](int s) { return smem_u32(bars + kMaxRaw + s); };
-  auto conv_full = [&](int s) { return smem_u32(bars + 2 * kMaxRaw + s); };
-  auto conv_empty = [&](int s) { return smem_u32(bars + 2 * kMaxRaw + kMaxConv + s); };
-  auto d_full = [&](int a) { return smem_u32(bars + 2 * kMaxRaw + 2 * kMaxConv + a); };
-  auto d_empty = [&](int a) { return smem_u32(bars + 2 * kMaxRaw + 2 * kMaxConv + 2 + a); };
-  const uint32_t drain_bar = smem_u32(bars + 2 * kMaxRaw + 2 * kMaxConv + 4);
+  const uint32_t bar0 = smem_u32(bars);
+  auto raw_full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+  auto raw_empty = [&](int s) { return bar0 + 8u * (uint32_t)(kMaxRaw + s); };
+  auto conv_full = [&](int s) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + s); };
+  auto conv_empty = [&](int s) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + kMaxConv + s); };
+  auto d_full = [&](int a) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + 2 * kMaxConv + a); };
+  auto d_empty = [&](int a) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + 2 * kMaxConv + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (uint32_t)(2 * kMaxRaw + 2 * kMaxConv + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)cluster_rank() : 0;
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.raw_stages; ++s) {
       mbar_init(raw_full(s), 1);
-      mbar_init(raw_empty(s), kSets * (kWWarps + twarps));
+      mbar_init(raw_empty(s), 2 * (kWWarps + twarps));  // the sets of its two halves
     }
     for (int s = 0; s < p.conv_stages; ++s) {
       mbar_init(conv_full(s), (kWWarps + twarps) * CTAS);
@@ -286,54 +287,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < kFirstEpi) {
     // ------------------------------------------------------------ converters
-    // Two sets of eight warps take the two 64-column halves of every raw
-    // stage: a half's chain of waits, loads, conversion and stores is longer
-    // than its MMAs, so two are kept in flight.
+    // Three sets of eight warps take the 64-column halves of the raw stages in
+    // turn: a half's chain of waits, loads, conversion and stores is longer
+    // than its MMAs, so three are kept in flight.
     const int cw = warp - kFirstConv, set = cw >> 3;
     const bool weights = (cw & 7) < kWWarps;
     // Weights: the channel is the TMEM lane, and a warp reaches the quarter
     // warp % 4.  Tokens: rows in warp order; warps without tokens stay out.
     const int row = (weights ? (warp & 3) : (cw & 7) - kWWarps) * 32 + lane;
     const bool live = weights || row < p.ntc, one = lane == 0;
-    const uint32_t sw = (uint32_t)(row & 7);
-    // A lane without a token reads the first one's and writes nothing.
-    const uint32_t src0 = sRaw + (weights ? 0 : 128 * kRawK) + (live ? (uint32_t)row * 128u : 0u);
+    // 16-byte chunk j of a 128-byte row sits at j ^ (row & 7): rows are 128
+    // bytes aligned, so its address is (row's | swizzle) ^ (j << 4).  A lane
+    // without a token reads its place in the first row and writes nothing.
+    const uint32_t swz = (uint32_t)(row & 7) << 4;
+    const uint32_t src0 = (sRaw + (weights ? 0 : 128 * kRawK) + (live ? (uint32_t)row * 128u : 0u)) | swz;
     const uint32_t full0 = PAIR ? mapa_shared(conv_full(0), 0) : conv_full(0);
-    int rs = 0, s = set;
-    uint32_t rph = 0, ph = 1;  // parities of the next raw_full / conv_empty wait
-    // 64 k of this lane's row as fp16 pairs.
+    // Half `it` of this CTA's run is half it % 2 of raw stage it / 2, and goes
+    // to conv stage it % conv_stages.
+    int rs = set >> 1, s = set;
+    uint32_t half = (uint32_t)(set & 1) << 6;           // bit 6 of the address: the upper 64 columns
+    uint32_t src = src0 + rs * p.raw_bytes, rph = 0, ph = 1;  // parities of the next raw_full / conv_empty wait
+    // 64 k of this lane's row widened to fp16 pairs; the raw stage is handed
+    // back once it has been read.
     auto load = [&](uint32_t* o) {
-      uint4 v[4];
-      const uint32_t src = src0 + rs * p.raw_bytes;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src + (((uint32_t)(4 * set + j) ^ sw) << 4));
-      __syncwarp();
-      arrive_if(raw_empty(rs), one);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        widen(v[j].x, o[8 * j], o[8 * j + 1]);
-        widen(v[j].y, o[8 * j + 2], o[8 * j + 3]);
-        widen(v[j].z, o[8 * j + 4], o[8 * j + 5]);
-        widen(v[j].w, o[8 * j + 6], o[8 * j + 7]);
+      for (int j = 0; j < 4; j += 2) {
+        const uint4 v = ld_shared_v4((src ^ half) ^ (uint32_t)(j << 4));
+        const uint4 w = ld_shared_v4((src ^ half) ^ (uint32_t)((j + 1) << 4));
+        if (j == 2) {
+          __syncwarp();
+          arrive_if(raw_empty(rs), one);
+        }
+        uint32_t* q = o + 8 * j;
+        widen(v.x, q[0], q[1]);
+        widen(v.y, q[2], q[3]);
+        widen(v.z, q[4], q[5]);
+        widen(v.w, q[6], q[7]);
+        widen(w.x, q[8], q[9]);
+        widen(w.y, q[10], q[11]);
+        widen(w.z, q[12], q[13]);
+        widen(w.w, q[14], q[15]);
       }
+      // Three halves on: one raw stage and a half.
+      const int adv = half ? 2 : 1;
+      const bool wrap = rs + adv >= p.raw_stages;
+      rs += wrap ? adv - p.raw_stages : adv;
+      src = src0 + rs * p.raw_bytes;
+      rph ^= wrap ? 1u : 0u;
+      half ^= 64u;
     };
     auto next = [&]() {
       __syncwarp();
       arrive_if(full0 + 8u * (uint32_t)s, one);
-      const bool rwrap = rs + 1 == p.raw_stages;
-      rs = rwrap ? 0 : rs + 1;
-      rph ^= rwrap ? 1u : 0u;
-      const bool wrap = s + 2 >= p.conv_stages;
-      s += wrap ? 2 - p.conv_stages : 2;
+      const bool wrap = s + kSets >= p.conv_stages;
+      s += wrap ? kSets - p.conv_stages : kSets;
       ph ^= wrap ? 1u : 0u;
     };
-    const long long rounds = (long long)my_tiles * p.num_raw;
+    const long long halves = (long long)my_tiles * p.num_kb;
     if (weights) {
       const uint32_t a0 = tmemA + ((uint32_t)((warp & 3) * 32) << 16);
 #pragma unroll 1
-      for (long long i = 0; i < rounds; ++i) {
-        if (!wait_warp(raw_full(rs), rph, ERRBIT_WAIT_ROWS)) break;
+      for (long long i = set; i < halves; i += kSets) {
         uint32_t o[32];
+        if (!wait_warp(raw_full(rs), rph, ERRBIT_WAIT_ROWS)) break;
         load(o);
         if (!wait_warp(conv_empty(s), ph, ERRBIT_WAIT_ROWS)) break;
         tc_fence_after();
@@ -343,18 +359,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         next();
       }
     } else if (row - lane < p.ntc) {
-      const uint32_t dst0 = sConv + (uint32_t)row * 128u;
+      const uint32_t dst0 = (sConv + (uint32_t)row * 128u) | swz;
 #pragma unroll 1
-      for (long long i = 0; i < rounds; ++i) {
-        if (!wait_warp(raw_full(rs), rph, ERRBIT_WAIT_ROWS)) break;
+      for (long long i = set; i < halves; i += kSets) {
         uint32_t o[32];
+        if (!wait_warp(raw_full(rs), rph, ERRBIT_WAIT_ROWS)) break;
         load(o);
         if (!wait_warp(conv_empty(s), ph, ERRBIT_WAIT_ROWS)) break;
         if (live) {
           const uint32_t dst = dst0 + s * p.conv_bytes;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            st_shared_v4(dst + (((uint32_t)j ^ sw) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            st_shared_v4(dst ^ (uint32_t)(j << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
         fence_proxy_async_smem();
         next();
@@ -380,6 +396,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = c0 + (lane & 15);
         return c < live_cols ? p.sa[(size_t)(m0 + c) * p.G + g] : 0.f;
       };
+      // The residual's addition, the rounding and the store of up to 16 tokens
+      // of this lane's channel (inlined twice: `cols` is 16 for all but the
+      // last tokens).  out may be resid: a value is read before it is written
+      // by the same thread.
+      auto finish = [&](float* v, T* out, size_t step, int cols) {
+        if (p.resid) {
+          const T* r = static_cast<const T*>(p.resid) + (out - static_cast<T*>(p.out));
+          T rv[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) rv[c] = c < cols ? r[c * step] : from_f<T>(0.f);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] += to_f(rv[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          if (c < cols) out[c * step] = from_f<T>(v[c]);
+      };
       float next = token_scale(0);
       if (!wait_warp(d_full(acc), (uint32_t)(lt >> 1) & 1u, ERRBIT_WAIT_EPILOGUE)) {
         ok = false;
@@ -393,23 +426,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c0 = 0; c0 < live_cols; c0 += 16, o += 16 * step) {
         const float sa = next;
         next = token_scale(c0 + 16);
-        const int cols = in ? live_cols - c0 : 0;
         float v[16];
         tmem_ld_32x16(d + c0, v);
 #pragma unroll
         for (int c = 0; c < 16; ++c) v[c] = fmaf(v[c] * __shfl_sync(0xffffffffu, sa, c), sw, bias);
-        if (p.resid) {
-          const T* r = static_cast<const T*>(p.resid) + o;
-          T rv[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c, r += step) rv[c] = c < cols ? *r : from_f<T>(0.f);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) v[c] += to_f(rv[c]);
-        }
         T* out = static_cast<T*>(p.out) + o;
-#pragma unroll
-        for (int c = 0; c < 16; ++c, out += step)
-          if (c < cols) *out = from_f<T>(v[c]);
+        if (live_cols - c0 >= 16) {
+          if (in) finish(v, out, step, 16);
+        } else {
+          if (in) finish(v, out, step, live_cols - c0);
+        }
       }
       tc_fence_before();
       __syncwarp();
