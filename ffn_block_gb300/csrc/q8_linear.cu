@@ -9,24 +9,26 @@
 // (the MMA's A operand) and the tokens into swizzled shared memory (its B
 // operand).  An output tile is channels x tokens, so that few tokens are a
 // narrow tile, not a padded one: 128 channels a CTA (256 a CTA pair) by up to
-// 208 tokens.  The bound is the tensor rate from about 150 tokens on, the
+// 192 tokens.  The bound is the tensor rate from about 150 tokens on, the
 // stream of the weights below.
 //
-// Roles (30 warps, one CTA per SM, persistent over tiles):
+// Roles (31 warps, one CTA per SM, persistent over tiles):
 //   warp 0       TMA producer: 128 k of the CTA's channels and tokens a stage
 //   warp 1       TMEM allocation; one thread issues the MMAs (even CTA)
-//   warps 2-25   three sets, taking 64 k in turn, of four warps for the
-//                weights (one channel a thread, int8 -> TMEM) and four for
+//   warps 2-22   three sets, taking 64 k in turn, of four warps for the
+//                weights (one channel a thread, int8 -> TMEM) and three for
 //                the tokens (one token a thread, int8 -> smem)
-//   warps 26-29  epilogue: a channel a thread, 16 tokens at a time
-// TMEM: two accumulators of NT <= 208 columns (so that the epilogue of one
+//   warps 23-30  epilogue: a channel a thread, 16 tokens at a time
+// TMEM: two accumulators of NT <= 192 columns (so that the epilogue of one
 // tile overlaps the next), then the weights' stages of 32 columns.
 //
 // Conversion of four int8 at once: (w & 0x00ff00ff) ^ 0x64806480 is the pair
 // of fp16 1024 + 128 + q for bytes 0 and 2, the same of w >> 8 for bytes 1 and
-// 3, and subtracting 1152 is exact: five instructions for four values.  The
+// 3, and 2 * (u - 1152) is exact: five instructions for four values.  The
 // order of k within a word changes in both operands alike, which leaves the
-// sum over k what it is.
+// sum over k what it is.  These instructions bound the large products: a step
+// of 64 k takes the tensor cores 2 * NT cycles, and the SM issues about 1000
+// instructions of conversion beside it.
 
 #include <cuda.h>
 
@@ -39,13 +41,15 @@
 namespace rmx {
 namespace {
 
-constexpr int kWWarps = 4, kTWarps = 4, kSets = 3, kEpiWarps = 4;
-constexpr int kFirstConv = 2, kFirstEpi = kFirstConv + kSets * (kWWarps + kTWarps);
+constexpr int kWWarps = 4, kTWarps = 3, kSets = 3, kEpiWarps = 8;
+constexpr int kSetWarps = kWWarps + kTWarps;
+constexpr int kFirstConv = 2, kFirstEpi = kFirstConv + kSets * kSetWarps;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kRawK = 128, kConvK = 64;
-constexpr int kMaxRaw = 8, kMaxConv = 6;
-constexpr int kMaxNT = 208;
-constexpr int kTmemCols = 512;
+constexpr int kMaxRaw = 8, kConv = 2 * kSets;
+constexpr int kMaxNT = 192, kMaxAlone = 32 * kTWarps;
+constexpr int kTmemCols = 512, kAcols = kConvK / 2;
+constexpr int kScaleBytes = kEpiWarps * 1024;  // each epilogue warp's copy of a tile's token scales
 constexpr int kBarBytes = 512;
 constexpr int kSmemMax = 227 * 1024;
 constexpr uint64_t kDrainNs = 50ull * 1000ull * 1000ull;
@@ -53,8 +57,8 @@ constexpr uint64_t kDrainNs = 50ull * 1000ull * 1000ull;
 struct Params {
   int M, G, K, N;
   int nt, ntc;            // tokens of a tile, and the share of them a CTA converts
-  int raw_stages, conv_stages, raw_bytes, conv_bytes;
-  int num_kb, num_raw;    // 64- and 128-column steps of K
+  int raw_bytes, conv_bytes, raw_stages;
+  int num_raw;            // 128-column steps of K
   int tiles_m, tiles_n, num_tiles;
   uint32_t idesc;
   const float *sa, *sw;
@@ -64,51 +68,51 @@ struct Params {
   unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ uint32_t sub1152(uint32_t u) {
-  const __half2 c = __half2half2(__ushort_as_half(0x6480));  // 1152
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), c);
-  return *reinterpret_cast<const uint32_t*>(&r);
+// 2 * (u - 1152) of a pair of fp16, exact.  The factor of two keeps this a
+// fused multiply-add, which runs on another pipe than the bit operations (a
+// plain addition shares theirs); each operand carries it, and the channel
+// scale takes the four away again.
+__device__ __forceinline__ uint32_t centre(uint32_t u) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(0x40004000u), "r"(0xe880e880u));  // 2, -2304
+  return r;
 }
 // Four int8 as two fp16 pairs, bytes (0, 2) and (1, 3).
 __device__ __forceinline__ void widen(uint32_t w, uint32_t& a, uint32_t& b) {
-  a = sub1152((w & 0x00ff00ffu) ^ 0x64806480u);
-  b = sub1152(((w >> 8) & 0x00ff00ffu) ^ 0x64806480u);
+  a = centre((w & 0x00ff00ffu) ^ 0x64806480u);
+  b = centre(((w >> 8) & 0x00ff00ffu) ^ 0x64806480u);
 }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Waits for a phase in a loop of a few instructions, at most `kTries` tests.
-constexpr uint32_t kTries = 1u << 14;
-__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, %3;\n\t"
-      "SPIN:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE;\n\t"
-      "sub.u32 n, n, 1;\n\t"
-      "setp.ne.u32 q, n, 0;\n\t"
-      "@q bra SPIN;\n\t"
-      "DONE:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "n"(kTries)
-      : "memory");
-  return ok != 0;
-}
-// The rest of a bounded wait: now and then a look at the clock and at whether
-// another warp has given up.  Out of line: it is all but never reached.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit_ns, unsigned int* err,
-                                     unsigned int bit, volatile int* abort) {
+// What a wait that runs out needs.
+struct WaitCtx {
+  uint64_t limit_ns;
+  unsigned int* err;
+  volatile int* abort;
+};
+// The rest of a bounded wait, out of line: it spins, now and then looking at
+// the clock and at whether another warp has given up.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, unsigned int bit, uint64_t limit_ns,
+                                     unsigned int* err, volatile int* abort) {
   const uint64_t t0 = globaltimer_ns();
-  while (!mbar_spin(bar, parity)) {
+  while (true) {
+    for (int i = 0; i < 1024; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (globaltimer_ns() - t0 > limit_ns) {
       atomicOr(err, bit);
@@ -116,9 +120,26 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t lim
       return false;
     }
   }
-  return true;
 }
-// Arrival by the lanes with pred set (one of a converged warp).
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t ph, unsigned int bit, const WaitCtx& w) {
+#pragma unroll 1
+  for (int i = 0; i < 512; ++i)
+    if (mbar_try_wait(bar, ph)) return true;
+  return wait_on(bar, ph, bit, w.limit_ns, w.err, w.abort);
+}
+// The same by a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t ph, unsigned int bit, const WaitCtx& w) {
+#pragma unroll 1
+  for (int i = 0; i < 512; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) return true;
+  return __all_sync(0xffffffffu, wait_on(bar, ph, bit, w.limit_ns, w.err, w.abort));
+}
+// Arrival by the lanes with pred set (one of a converged warp), on this CTA's
+// barrier or another's of the cluster.  CTA scope orders nothing in another
+// CTA's memory, which a cluster-scope release would do at the price of a fence
+// (about 1000 cycles); what is handed over here is read by the tensor cores
+// of the arriving thread's own SM (its TMEM, and its shared memory behind a
+// proxy fence), the other CTA only issuing the MMA.
 __device__ __forceinline__ void arrive_if(uint32_t bar, bool pred) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
@@ -126,7 +147,89 @@ __device__ __forceinline__ void arrive_if(uint32_t bar, bool pred) {
       : "memory");
 }
 
-template <typename T, bool PAIR>
+// A converter warp's run.  Half `it` (64 k) of the CTA's run is half it % 2 of
+// raw stage it / 2.  Set x takes halves x, x + 3, x + 6, ...: conv stages x
+// and x + 3 of the six in turn.  Tokens go to conv stage it % 6 once the MMAs
+// of half it - 6 are done, weights to TMEM stage it % W once those of half
+// it - W are (W is 3 where the accumulators leave room for no more); the
+// barriers are those of the conv stages either way.
+template <int W, bool WEIGHTS>
+__device__ __forceinline__ void convert(int set, int row, bool live, int halves, uint32_t src0, uint32_t raw_bytes,
+                                        int raw_stages, uint32_t raw_bar, uint32_t conv_full, uint32_t conv_empty,
+                                        uint32_t dst0, uint32_t conv_bytes, const WaitCtx& wc) {
+  const bool one = (threadIdx.x & 31) == 0;
+  // 16-byte chunk j of a 128-byte row sits at j ^ (row & 7): rows are 128
+  // bytes aligned, so its address is (row's | swizzle) ^ (j << 4).
+  const uint32_t swz = (uint32_t)(row & 7) << 4;
+  uint32_t dst[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    dst[j] = WEIGHTS ? dst0 + (uint32_t)(W == 3 ? set : set + kSets * j) * kAcols
+                     : (dst0 + (uint32_t)(set + kSets * j) * conv_bytes) | swz;
+  const uint32_t cfull = conv_full + 8u * (uint32_t)set, cempty = conv_empty + 8u * (uint32_t)set;
+  int rs = set >> 1;
+  uint32_t src = ((src0 + (uint32_t)rs * raw_bytes) | swz) ^ ((uint32_t)(set & 1) << 6);  // bit 6: the upper half
+  uint32_t rph = 0, lap = 0;  // parities of the raw stages' and the conv stages' laps
+#pragma unroll 1
+  for (int i = set; i < halves; i += 2 * kSets) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (j && i + kSets >= halves) return;
+      const uint32_t rbar = raw_bar + 8u * (uint32_t)rs;
+      if (!wait_warp(rbar, rph, ERRBIT_WAIT_ROWS, wc)) return;
+      uint32_t o[32];
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        const uint4 v = ld_shared_v4(src ^ (uint32_t)(c << 4));
+        const uint4 w = ld_shared_v4(src ^ (uint32_t)((c + 1) << 4));
+        if (c == 2) {
+          // Read: the raw stage is handed back.
+          __syncwarp();
+          arrive_if(rbar + 8u * kMaxRaw, one);
+        }
+        uint32_t* q = o + 8 * c;
+        widen(v.x, q[0], q[1]);
+        widen(v.y, q[2], q[3]);
+        widen(v.z, q[4], q[5]);
+        widen(v.w, q[6], q[7]);
+        widen(w.x, q[8], q[9]);
+        widen(w.y, q[10], q[11]);
+        widen(w.z, q[12], q[13]);
+        widen(w.w, q[14], q[15]);
+      }
+      // The half whose MMAs free this place: six back (this conv stage, the
+      // lap before), or three (the other one of this set).
+      constexpr bool kThree = WEIGHTS && W == 3;
+      const uint32_t e = cempty + (((j & 1) != 0) != kThree ? 8u * kSets : 0u);
+      const uint32_t eph = kThree && (j & 1) ? lap : lap ^ 1u;
+      if (!wait_warp(e, eph, ERRBIT_WAIT_ROWS, wc)) return;
+      if (WEIGHTS) {
+        tc_fence_after();
+        tmem_st_32x32(dst[j], o);
+        tmem_st_wait();
+        tc_fence_before();
+      } else {
+        if (live) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            st_shared_v4(dst[j] ^ (uint32_t)(c << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      arrive_if(cfull + (j ? 8u * kSets : 0u), one);
+      if (j) lap ^= 1u;
+      // Three halves on: one raw stage and a half.
+      const int adv = ((set + j) & 1) ? 2 : 1;
+      const bool wrap = rs + adv >= raw_stages;
+      rs += wrap ? adv - raw_stages : adv;
+      src = (src ^ 64u) + (uint32_t)(wrap ? adv - raw_stages : adv) * raw_bytes;
+      rph ^= wrap ? 1u : 0u;
+    }
+  }
+}
+
+template <typename T, bool PAIR, int W>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_q8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const Params p) {
   pdl_trigger();
@@ -134,18 +237,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const uint32_t sRaw = smem_u32(smem);
-  const uint32_t sConv = sRaw + p.raw_stages * p.raw_bytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.raw_stages * p.raw_bytes + p.conv_stages * p.conv_bytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxRaw + 2 * kMaxConv + 5);
+  const uint32_t sConv = sRaw + p.raw_stages * p.raw_bytes, sScale = sConv + kConv * p.conv_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.raw_stages * p.raw_bytes + kConv * p.conv_bytes + kScaleBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxRaw + 2 * kConv + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t bar0 = smem_u32(bars);
   auto raw_full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
   auto raw_empty = [&](int s) { return bar0 + 8u * (uint32_t)(kMaxRaw + s); };
   auto conv_full = [&](int s) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + s); };
-  auto conv_empty = [&](int s) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + kMaxConv + s); };
-  auto d_full = [&](int a) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + 2 * kMaxConv + a); };
-  auto d_empty = [&](int a) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + 2 * kMaxConv + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (uint32_t)(2 * kMaxRaw + 2 * kMaxConv + 4);
+  auto conv_empty = [&](int s) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + kConv + s); };
+  auto d_full = [&](int a) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + 2 * kConv + a); };
+  auto d_empty = [&](int a) { return bar0 + 8u * (uint32_t)(2 * kMaxRaw + 2 * kConv + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (uint32_t)(2 * kMaxRaw + 2 * kConv + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)cluster_rank() : 0;
@@ -162,11 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     n0 = tn * 128 * CTAS + rank * 128;
     m0 = tm * p.nt;
   };
-  auto wait = [&](uint32_t bar, uint32_t ph, unsigned int bit) {
-    return mbar_spin(bar, ph) || wait_on(bar, ph, p.wait_ns, p.err, bit, abort_flag);
-  };
-  // The same by a whole warp, which goes on or gives up together.
-  auto wait_warp = [&](uint32_t bar, uint32_t ph, unsigned int bit) { return __all_sync(0xffffffffu, wait(bar, ph, bit)); };
+  const WaitCtx wc{p.wait_ns, p.err, abort_flag};
   // Tiles of this CTA (or pair).
   const int my_tiles = first < p.num_tiles ? (p.num_tiles - first + stride - 1) / stride : 0;
 
@@ -175,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(raw_full(s), 1);
       mbar_init(raw_empty(s), 2 * (kWWarps + twarps));  // the sets of its two halves
     }
-    for (int s = 0; s < p.conv_stages; ++s) {
+    for (int s = 0; s < kConv; ++s) {
       mbar_init(conv_full(s), (kWWarps + twarps) * CTAS);
       mbar_init(conv_empty(s), 1);
     }
@@ -208,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int g, n0, m0;
         coords(tile, g, n0, m0);
         for (int rk = 0; rk < p.num_raw; ++rk) {
-          if (!wait(raw_empty(s), ph ^ 1u, ERRBIT_WAIT_PRODUCER)) {
+          if (!wait_one(raw_empty(s), ph ^ 1u, ERRBIT_WAIT_PRODUCER, wc)) {
             ok = false;
             break;
           }
@@ -246,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t conv_step = (uint32_t)p.conv_bytes >> 4;  // descriptor addresses count 16 bytes
       for (int lt = 0; ok && lt < my_tiles; ++lt) {
         const int acc = lt & 1;
-        if (!wait(d_empty(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u, ERRBIT_WAIT_MMA)) {
+        if (!wait_one(d_empty(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u, ERRBIT_WAIT_MMA, wc)) {
           ok = false;
           break;
         }
@@ -254,24 +353,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + (uint32_t)(acc * p.nt);
         uint32_t accumulate = 0;
 #pragma unroll 1
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!wait(conv_full(s), ph, ERRBIT_WAIT_MMA)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t b = desc0 + (uint32_t)s * conv_step;
-          const uint32_t a = tmemA + s * (kConvK / 2);
+        for (int rk = 0; ok && rk < p.num_raw; ++rk) {
+          // The two halves of a raw stage.
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            umma_f16_ts<PAIR>(d, a + k * 8, b + 2 * k, p.idesc, accumulate);
-            accumulate = 1;
+          for (int h = 0; h < 2; ++h) {
+            if (!wait_one(conv_full(s), ph, ERRBIT_WAIT_MMA, wc)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t b = desc0 + (uint32_t)s * conv_step;
+            const uint32_t a = tmemA + (uint32_t)(W == 3 && s >= 3 ? s - 3 : s) * kAcols;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              umma_f16_ts<PAIR>(d, a + k * 8, b + 2 * k, p.idesc, accumulate);
+              accumulate = 1;
+            }
+            if (PAIR) umma_commit_pair(conv_empty(s));
+            else umma_commit<false>(conv_empty(s));
+            const bool wrap = s == kConv - 1;
+            s = wrap ? 0 : s + 1;
+            ph ^= wrap ? 1u : 0u;
           }
-          if (PAIR) umma_commit_pair(conv_empty(s));
-          else umma_commit<false>(conv_empty(s));
-          const bool wrap = s + 1 == p.conv_stages;
-          s = wrap ? 0 : s + 1;
-          ph ^= wrap ? 1u : 0u;
         }
         if (!ok) break;
         if (PAIR) umma_commit_pair(d_full(acc));
@@ -287,98 +390,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < kFirstEpi) {
     // ------------------------------------------------------------ converters
-    // Three sets of eight warps take the 64-column halves of the raw stages in
-    // turn: a half's chain of waits, loads, conversion and stores is longer
-    // than its MMAs, so three are kept in flight.
-    const int cw = warp - kFirstConv, set = cw >> 3;
-    const bool weights = (cw & 7) < kWWarps;
-    // Weights: the channel is the TMEM lane, and a warp reaches the quarter
-    // warp % 4.  Tokens: rows in warp order; warps without tokens stay out.
-    const int row = (weights ? (warp & 3) : (cw & 7) - kWWarps) * 32 + lane;
-    const bool live = weights || row < p.ntc, one = lane == 0;
-    // 16-byte chunk j of a 128-byte row sits at j ^ (row & 7): rows are 128
-    // bytes aligned, so its address is (row's | swizzle) ^ (j << 4).  A lane
-    // without a token reads its place in the first row and writes nothing.
-    const uint32_t swz = (uint32_t)(row & 7) << 4;
-    const uint32_t src0 = (sRaw + (weights ? 0 : 128 * kRawK) + (live ? (uint32_t)row * 128u : 0u)) | swz;
+    const int cw = warp - kFirstConv, set = cw / kSetWarps, role = cw - set * kSetWarps;
     const uint32_t full0 = PAIR ? mapa_shared(conv_full(0), 0) : conv_full(0);
-    // Half `it` of this CTA's run is half it % 2 of raw stage it / 2, and goes
-    // to conv stage it % conv_stages.
-    int rs = set >> 1, s = set;
-    uint32_t half = (uint32_t)(set & 1) << 6;           // bit 6 of the address: the upper 64 columns
-    uint32_t src = src0 + rs * p.raw_bytes, rph = 0, ph = 1;  // parities of the next raw_full / conv_empty wait
-    // 64 k of this lane's row widened to fp16 pairs; the raw stage is handed
-    // back once it has been read.
-    auto load = [&](uint32_t* o) {
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        const uint4 v = ld_shared_v4((src ^ half) ^ (uint32_t)(j << 4));
-        const uint4 w = ld_shared_v4((src ^ half) ^ (uint32_t)((j + 1) << 4));
-        if (j == 2) {
-          __syncwarp();
-          arrive_if(raw_empty(rs), one);
-        }
-        uint32_t* q = o + 8 * j;
-        widen(v.x, q[0], q[1]);
-        widen(v.y, q[2], q[3]);
-        widen(v.z, q[4], q[5]);
-        widen(v.w, q[6], q[7]);
-        widen(w.x, q[8], q[9]);
-        widen(w.y, q[10], q[11]);
-        widen(w.z, q[12], q[13]);
-        widen(w.w, q[14], q[15]);
-      }
-      // Three halves on: one raw stage and a half.
-      const int adv = half ? 2 : 1;
-      const bool wrap = rs + adv >= p.raw_stages;
-      rs += wrap ? adv - p.raw_stages : adv;
-      src = src0 + rs * p.raw_bytes;
-      rph ^= wrap ? 1u : 0u;
-      half ^= 64u;
-    };
-    auto next = [&]() {
-      __syncwarp();
-      arrive_if(full0 + 8u * (uint32_t)s, one);
-      const bool wrap = s + kSets >= p.conv_stages;
-      s += wrap ? kSets - p.conv_stages : kSets;
-      ph ^= wrap ? 1u : 0u;
-    };
-    const long long halves = (long long)my_tiles * p.num_kb;
-    if (weights) {
-      const uint32_t a0 = tmemA + ((uint32_t)((warp & 3) * 32) << 16);
-#pragma unroll 1
-      for (long long i = set; i < halves; i += kSets) {
-        uint32_t o[32];
-        if (!wait_warp(raw_full(rs), rph, ERRBIT_WAIT_ROWS)) break;
-        load(o);
-        if (!wait_warp(conv_empty(s), ph, ERRBIT_WAIT_ROWS)) break;
-        tc_fence_after();
-        tmem_st_32x32(a0 + s * (kConvK / 2), o);
-        tmem_st_wait();
-        tc_fence_before();
-        next();
-      }
-    } else if (row - lane < p.ntc) {
-      const uint32_t dst0 = (sConv + (uint32_t)row * 128u) | swz;
-#pragma unroll 1
-      for (long long i = set; i < halves; i += kSets) {
-        uint32_t o[32];
-        if (!wait_warp(raw_full(rs), rph, ERRBIT_WAIT_ROWS)) break;
-        load(o);
-        if (!wait_warp(conv_empty(s), ph, ERRBIT_WAIT_ROWS)) break;
-        if (live) {
-          const uint32_t dst = dst0 + s * p.conv_bytes;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            st_shared_v4(dst ^ (uint32_t)(j << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-        }
-        fence_proxy_async_smem();
-        next();
-      }
+    const int halves = 2 * my_tiles * p.num_raw;  // the launch keeps this below 2^31
+    if (role < kWWarps) {
+      // The channel is the TMEM lane, and a warp reaches the quarter warp % 4.
+      const int row = (warp & 3) * 32 + lane;
+      convert<W, true>(set, row, true, halves, sRaw + (uint32_t)row * 128u, p.raw_bytes, p.raw_stages, raw_full(0), full0,
+                       conv_empty(0), tmemA + ((uint32_t)((warp & 3) * 32) << 16), 0, wc);
+    } else {
+      // Warps without tokens stay out; a lane without a token reads the first
+      // token's place and writes nothing.
+      const int row = (role - kWWarps) * 32 + lane;
+      const bool live = row < p.ntc;
+      if (row - lane < p.ntc)
+        convert<W, false>(set, row, live, halves, sRaw + 128 * kRawK + (live ? (uint32_t)row * 128u : 0u),
+                          p.raw_bytes, p.raw_stages, raw_full(0), full0, conv_empty(0), sConv + (uint32_t)row * 128u,
+                               p.conv_bytes, wc);
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;
+    // Two warps a lane quarter, taking 16 tokens in turn.
+    const int q = warp & 3, odd = (warp - kFirstEpi) >> 2;
+    const uint32_t scales = sScale + (uint32_t)(warp - kFirstEpi) * 1024u;
     int lt = 0;
     bool ok = true;
     for (int tile = first; tile < p.num_tiles; tile += stride, ++lt) {
@@ -388,53 +423,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = n0 + q * 32 + lane;
       const bool in = n < p.N;
       const int live_cols = min(p.nt, p.M - m0);
-      // While the accumulator is being computed: the scales, one token a lane.
-      const float sw = in ? p.sw[(size_t)g * p.N + n] : 0.f;
+      // While the accumulator is being computed: the scales.  (0.25: the
+      // factor of two in each operand.)
+      const float sw = in ? 0.25f * p.sw[(size_t)g * p.N + n] : 0.f;
       const float bias = p.bias && in ? to_f(static_cast<const T*>(p.bias)[(size_t)g * p.N + n]) : 0.f;
-      // Token scales 16 columns ahead, one a lane.
-      auto token_scale = [&](int c0) {
-        const int c = c0 + (lane & 15);
-        return c < live_cols ? p.sa[(size_t)(m0 + c) * p.G + g] : 0.f;
-      };
-      // The residual's addition, the rounding and the store of up to 16 tokens
-      // of this lane's channel (inlined twice: `cols` is 16 for all but the
-      // last tokens).  out may be resid: a value is read before it is written
-      // by the same thread.
-      auto finish = [&](float* v, T* out, size_t step, int cols) {
-        if (p.resid) {
-          const T* r = static_cast<const T*>(p.resid) + (out - static_cast<T*>(p.out));
-          T rv[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) rv[c] = c < cols ? r[c * step] : from_f<T>(0.f);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) v[c] += to_f(rv[c]);
-        }
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c < cols) out[c * step] = from_f<T>(v[c]);
-      };
-      float next = token_scale(0);
-      if (!wait_warp(d_full(acc), (uint32_t)(lt >> 1) & 1u, ERRBIT_WAIT_EPILOGUE)) {
+      for (int c = lane; c < p.nt; c += 32)
+        st_shared_f32(scales + 4u * (uint32_t)c, c < live_cols ? p.sa[(size_t)(m0 + c) * p.G + g] : 0.f);
+      __syncwarp();
+      if (!wait_warp(d_full(acc), (uint32_t)(lt >> 1) & 1u, ERRBIT_WAIT_EPILOGUE, wc)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const size_t step = (size_t)p.G * p.N;
-      size_t o = ((size_t)m0 * p.G + g) * p.N + n;
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * p.nt);
-#pragma unroll 1
-      for (int c0 = 0; c0 < live_cols; c0 += 16, o += 16 * step) {
-        const float sa = next;
-        next = token_scale(c0 + 16);
-        float v[16];
-        tmem_ld_32x16(d + c0, v);
+      const float2 sw2 = f2(sw), bias2 = f2(bias);
+      const size_t step = (size_t)p.G * p.N;
+      size_t at = ((size_t)(m0 + 16 * odd) * p.G + g) * p.N + n;
+      // Up to 16 tokens of this lane's channel (inlined twice: `cols` is 16
+      // for all but the last).  Neighbouring lanes write neighbouring
+      // channels.  out may be resid: a value is read before the same thread
+      // writes it.
+      auto finish = [&](float2* v, int cols) {
+        if (p.resid) {
+          const T* r = static_cast<const T*>(p.resid) + at;
+          T rv[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = fmaf(v[c] * __shfl_sync(0xffffffffu, sa, c), sw, bias);
-        T* out = static_cast<T*>(p.out) + o;
+          for (int c = 0; c < 16; ++c, r += step) rv[c] = c < cols ? *r : from_f<T>(0.f);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = add2(v[c], make_float2(to_f(rv[2 * c]), to_f(rv[2 * c + 1])));
+        }
+        T* out = static_cast<T*>(p.out) + at;
+#pragma unroll
+        for (int c = 0; c < 16; ++c, out += step)
+          if (c < cols) *out = from_f<T>(c & 1 ? v[c / 2].y : v[c / 2].x);
+      };
+#pragma unroll 1
+      for (int c0 = 16 * odd; c0 < live_cols; c0 += 32, at += 32 * step) {
+        float2 v[8];
+        tmem_ld_32x16(d + c0, reinterpret_cast<float*>(v));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 sa = ld_shared_f4(scales + 4u * (uint32_t)(c0 + 4 * i));
+          v[2 * i] = fma2(mul2(v[2 * i], make_float2(sa.x, sa.y)), sw2, bias2);
+          v[2 * i + 1] = fma2(mul2(v[2 * i + 1], make_float2(sa.z, sa.w)), sw2, bias2);
+        }
         if (live_cols - c0 >= 16) {
-          if (in) finish(v, out, step, 16);
+          if (in) finish(v, 16);
         } else {
-          if (in) finish(v, out, step, live_cols - c0);
+          if (in) finish(v, live_cols - c0);
         }
       }
       tc_fence_before();
@@ -444,9 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // No commit may still be on its way to this CTA's barriers at the end:
     // wait for the last use of every stage.
     if (ok && warp == kFirstEpi) {
-      const long long its = (long long)lt * p.num_kb;
-      for (long long j = its > p.conv_stages ? its - p.conv_stages : 0; ok && j < its; ++j)
-        ok = wait_warp(conv_empty((int)(j % p.conv_stages)), (uint32_t)(j / p.conv_stages) & 1u, ERRBIT_WAIT_DRAIN);
+      const long long its = 2ll * lt * p.num_raw;
+      for (long long j = its > kConv ? its - kConv : 0; ok && j < its; ++j)
+        ok = wait_warp(conv_empty((int)(j % kConv)), (uint32_t)(j / kConv) & 1u, ERRBIT_WAIT_DRAIN, wc);
     }
   }
 
@@ -461,15 +497,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename T, bool PAIR>
+template <typename T, bool PAIR, int W>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& a, const Params& p, cudaStream_t st) {
-  auto k = k_linear_q8<T, PAIR>;
-  const int smem = 1024 + p.raw_stages * p.raw_bytes + p.conv_stages * p.conv_bytes + kBarBytes;
+  auto k = k_linear_q8<T, PAIR, W>;
+  const int smem = 1024 + p.raw_stages * p.raw_bytes + kConv * p.conv_bytes + kScaleBytes + kBarBytes;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
   const int slots = PAIR ? sm_count() / 2 : sm_count();
   const int n = p.num_tiles < slots ? p.num_tiles : slots;
   return launch_k(k, dim3(PAIR ? 2 * n : n), dim3(kThreads), smem, st, PAIR ? 2 : 1, w, a, p);
+}
+
+// The accumulators of a CTA alone (up to 96 tokens) leave TMEM room for six
+// stages of weights, those of a pair for three.
+template <typename T>
+cudaError_t dispatch(const CUtensorMap& w, const CUtensorMap& a, const Params& p, bool pair, cudaStream_t st) {
+  return pair ? launch<T, true, 3>(w, a, p, st) : launch<T, false, 6>(w, a, p, st);
 }
 
 }  // namespace
@@ -480,10 +523,10 @@ cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t 
   p.G = d.G;
   p.K = d.K;
   p.N = d.N;
-  // A CTA alone up to 128 tokens, a pair above: the pair shares the tokens'
+  // A CTA alone up to 96 tokens, a pair above: the pair shares the tokens'
   // conversion, which a CTA alone would do for all of them.
-  const bool pair = d.M > 128 && d.N > 128;
-  const int most = pair ? kMaxNT : 128;
+  const bool pair = d.M > kMaxAlone && d.N > 128;
+  const int most = pair ? kMaxNT : kMaxAlone;
   p.tiles_m = (d.M + most - 1) / most;
   const int even = (d.M + p.tiles_m - 1) / p.tiles_m;
   p.nt = (even + 15) / 16 * 16;
@@ -494,14 +537,13 @@ cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t 
   const long long tiles = (long long)d.G * p.tiles_n * p.tiles_m;
   if (tiles > (1ll << 30)) return cudaErrorInvalidValue;
   p.num_tiles = (int)tiles;
-  p.num_raw = (d.K + kRawK - 1) / kRawK;
-  p.num_kb = p.num_raw * (kRawK / kConvK);  // columns past K are zeros
-  p.conv_stages = (kTmemCols - 2 * p.nt) / (kConvK / 2);
-  if (p.conv_stages > kMaxConv) p.conv_stages = kMaxConv;
+  p.num_raw = (d.K + kRawK - 1) / kRawK;  // columns past K are zeros
   p.raw_bytes = 128 * kRawK + p.ntc * kRawK;
   p.conv_bytes = p.ntc * kConvK * 2;
-  p.raw_stages = (kSmemMax - 1024 - kBarBytes - p.conv_stages * p.conv_bytes) / p.raw_bytes;
+  p.raw_stages = (kSmemMax - 1024 - kScaleBytes - kBarBytes - kConv * p.conv_bytes) / p.raw_bytes;
   if (p.raw_stages > kMaxRaw) p.raw_stages = kMaxRaw;
+  const long long rounds = (tiles + (pair ? sm_count() / 2 : sm_count()) - 1) / (pair ? sm_count() / 2 : sm_count());
+  if (rounds * p.num_raw >= (1ll << 30)) return cudaErrorInvalidValue;  // more than 10^19 operations
   // kind::f16, fp16 operands (type 0), fp32 accumulator, both K-major.
   p.idesc = (1u << 4) | ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)((pair ? 256 : 128) >> 4) << 24);
   p.sa = d.sa;
@@ -516,14 +558,12 @@ cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t 
   if (!make_tensor_map_rows8(&w, d.w, K, N, G, P, N * P, 128, 1) ||
       !make_tensor_map_rows8(&a, d.a, K, G, M, P, G * P, 1, (uint32_t)p.ntc))
     return cudaErrorInvalidValue;
-#define RMX_LQ8(T) return pair ? launch<T, true>(w, a, p, st) : launch<T, false>(w, a, p, st)
   switch (d.dtype) {
-    case 0: RMX_LQ8(float);
-    case 1: RMX_LQ8(bf16);
-    case 2: RMX_LQ8(f16);
+    case 0: return dispatch<float>(w, a, p, pair, st);
+    case 1: return dispatch<bf16>(w, a, p, pair, st);
+    case 2: return dispatch<f16>(w, a, p, pair, st);
     default: return cudaErrorInvalidValue;
   }
-#undef RMX_LQ8
 }
 
 }  // namespace rmx
