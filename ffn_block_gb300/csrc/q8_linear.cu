@@ -79,8 +79,13 @@ __device__ __forceinline__ uint32_t centre(uint32_t u) {
 }
 // Four int8 as two fp16 pairs, bytes (0, 2) and (1, 3).
 __device__ __forceinline__ void widen(uint32_t w, uint32_t& a, uint32_t& b) {
-  a = centre((w & 0x00ff00ffu) ^ 0x64806480u);
-  b = centre(((w >> 8) & 0x00ff00ffu) ^ 0x64806480u);
+  // lop3 0x6a is (x & y) ^ z in one instruction, which the compiler does not
+  // form by itself from two constants.
+  uint32_t x, y;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x) : "r"(w), "r"(0x00ff00ffu), "r"(0x64806480u));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(w >> 8), "r"(0x00ff00ffu), "r"(0x64806480u));
+  a = centre(x);
+  b = centre(y);
 }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
