@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (elect_one()) {
       int it = 0;
       bool ok = true;
       for (int tile = first; ok && tile < count; tile += stride) {
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       constexpr uint32_t idesc = make_idesc<T, KT::A_MN, KT::B_MN, PAIR ? 2 * BM : BM>();
       int it = 0, lt = 0;
       bool ok = true;

@@ -54,7 +54,7 @@ WgradWs wgrad_ws(const rmx_layer& l) {
     o = up256(o + (size_t)l.G * w.Kp * w.Np * e);
   }
   w.part = o;
-  w.total = up256(o + (size_t)colpart_slices(l.M) * l.G * l.N * sizeof(float));
+  w.total = up256(o + (size_t)colpart_slices(l.M, (long long)l.G * l.N, (int)e) * l.G * l.N * sizeof(float));
   return w;
 }
 
@@ -231,14 +231,17 @@ rmx_status rmx_ckpt8_wgrad(const rmx_layer* layer, const int8_t* q, const int8_t
   }
   if (db) {
     const long long J = (long long)l.G * l.N;
+    const int slices = colpart_slices(l.M, J, (int)e);
     float* part = reinterpret_cast<float*>(at(ws, w.part));
     {
       Launch la("ckpt8_dbias", st);
-      RMX_TRY(la.done(launch_colpart(l.M, J, l.dtype, dy, part, st)));
+      RMX_TRY(la.done(launch_colpart(l.M, J, l.dtype, dy, part, db, st)));
     }
-    const ColsumJob job{part, db, colpart_slices(l.M), (int)J};
-    Launch la("ckpt8_dbias_sum", st);
-    RMX_TRY(la.done(launch_colsums(&job, 1, l.dtype, st)));
+    if (slices > 1) {
+      const ColsumJob job{part, db, slices, (int)J};
+      Launch la("ckpt8_dbias_sum", st);
+      RMX_TRY(la.done(launch_colsums(&job, 1, l.dtype, st)));
+    }
   }
   return RMX_OK;
 }
