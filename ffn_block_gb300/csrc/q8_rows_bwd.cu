@@ -17,154 +17,174 @@
 namespace rmx {
 namespace {
 
-template <typename T, int TPR, int NCH, bool CK, bool VEC>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 256 ? 2 : 1) k_rows_bwd(const RowsBwd a) {
+// Sum over the warps of a row, in a fixed order.  `red` holds two slots of a
+// float per warp of the row, used in turn; the row's warps meet at a barrier of
+// their own (rows of a block do not wait for one another).
+__device__ __forceinline__ float row_sum(float s, float* red, int slot, int w, int W, int barrier) {
+  s = warp_sum(s);
+  if (W == 1) return s;
+  float* r = red + slot * W;
+  if ((threadIdx.x & 31) == 0) r[w] = s;
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * W) : "memory");
+  s = 0.f;
+  for (int i = 0; i < W; ++i) s += r[i];
+  return s;
+}
+
+// Registers of a thread with one block of a row.  Many warps with one row each
+// hide the loads better than few with rows loaded ahead: 65536 rows of 1280
+// 16-bit columns take 125 us at 64 registers (30 warps a SM), 198 us with two
+// rows ahead at 96 (20 warps).
+constexpr int kRegs = 64;
+
+// What a row brings, as loaded.
+template <typename T, bool CK, bool VEC> struct RowIn {
+  Chunk<T> dn, dh;
+  Chunk<T> h;          // the stored sum
+  uint2 q;             // or its checkpoint: eight int8 and their exponents
+  uint32_t e[2];
+};
+
+// A row belongs to W warps (W = blocks of 256 columns, up to 16), each with
+// NCH blocks of it; `rpb` rows at a time to a thread block.
+template <typename T, int NCH, bool CK, bool VEC>
+__global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, const int W, const int rpb) {
   pdl_enter();
-  constexpr int TH = TPR < 256 ? 256 : TPR, RPB = TH / TPR, W = TPR / 32;
-  __shared__ uint32_t red[RPB * 4 * W];
-  extern __shared__ float cols[];  // RPB > 1: [C] partials of the block
-  const int lane = threadIdx.x & 31, w = (threadIdx.x & (TPR - 1)) >> 5, rib = threadIdx.x / TPR;
+  __shared__ float red[64];
+  extern __shared__ float cols[];  // rpb > 1: [C] partials of the block
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, rib = wid / W, w = wid - rib * W;
   const float inv_n = 1.f / (float)a.C;
   const int groups = a.P / kQ8Group;
-  int slot = 0;
+  float* my_red = red + rib * 2 * W;
+  auto c_of = [&](int j) { return col0<VEC>(w + j * W, lane); };
+  auto load = [&](RowIn<T, CK, VEC>& in, long long row, int j) {
+    const size_t at = (size_t)row * a.C;
+    const int C = a.C, P = a.P, c0 = c_of(j);
+    in.dn = load_chunk<T, VEC>(static_cast<const T*>(a.dn) + at, c0, C);
+    if (a.dh) in.dh = load_chunk<T, VEC>(static_cast<const T*>(a.dh) + at, c0, C);
+    if constexpr (CK) {
+      in.q = load_bytes<VEC>(a.q + (size_t)row * P, c0, P);
+      const int8_t* e = a.e + (size_t)row * groups;
+      if constexpr (VEC) {
+        in.e[0] = c0 < P ? (uint32_t)(int)e[c0 / kQ8Group] : 0u;
+      } else {
+        const int g0 = (w + j * W) * 8;
+        in.e[0] = in.e[1] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((g0 + i) * kQ8Group < P) in.e[i / 4] |= (uint32_t)(uint8_t)e[g0 + i] << (8 * (i & 3));
+      }
+    } else {
+      in.h = load_chunk<T, VEC>(static_cast<const T*>(a.h) + at, c0, C);
+    }
+  };
+  auto xhat = [&](const RowIn<T, CK, VEC>& in, float rstd, float2 (&xh)[4]) {
+    if constexpr (CK) {
+      biased(in.q, xh);
+      if constexpr (VEC) {
+        const float s = ckpt_step((int)in.e[0]) * rstd;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xh[i] = mul2(add2(xh[i], f2(-kBias)), f2(s));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float& t = i & 1 ? xh[i / 2].y : xh[i / 2].x;
+          t = (t - kBias) * (ckpt_step((int8_t)(in.e[i / 4] >> (8 * (i & 3)))) * rstd);
+        }
+      }
+    } else {
+      to_pairs(in.h, xh);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xh[i] = mul2(xh[i], f2(rstd));
+    }
+  };
   Chunk<T> g[NCH];
   float2 acc[NCH][4];
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
-    g[j] = load_chunk<T, VEC>(static_cast<const T*>(a.gamma), col0<VEC>(w + j * W, lane), a.C);
+    g[j] = load_chunk<T, VEC>(static_cast<const T*>(a.gamma), c_of(j), a.C);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = f2(0.f);
   }
-  for (long long base = (long long)blockIdx.x * RPB; base < a.R; base += (long long)gridDim.x * RPB) {
-    const long long row = base + rib;
-    const bool live = row < a.R;
-    const size_t rr = live ? row : 0, at = rr * a.C;
-    const int C = live ? a.C : 0, P = live ? a.P : 0;
-    Chunk<T> dn[NCH], hs[CK ? 1 : NCH], dh[NCH];
-    uint2 hq[CK ? NCH : 1];
-    uint32_t he[CK ? NCH : 1][VEC ? 1 : 2];
+  const long long step = (long long)gridDim.x * rpb;
+  int slot = 0;
+  // Every warp of a row sees the same rows, so their barriers match.
+  for (long long row = (long long)blockIdx.x * rpb + rib; row < a.R; row += step, slot ^= 1) {
+    RowIn<T, CK, VEC> in[NCH];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) load(in[j], row, j);
+    const float rstd = a.rstd[row];
+    float2 dot2 = f2(0.f), xh[NCH][4], t[NCH][4];
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int c0 = col0<VEC>(w + j * W, lane);
-      dn[j] = load_chunk<T, VEC>(static_cast<const T*>(a.dn) + at, c0, C);
-      if constexpr (CK) {
-        hq[j] = load_bytes<VEC>(a.q + rr * a.P, c0, P);
-        const int8_t* e = a.e + rr * groups;
-        if constexpr (VEC) {
-          he[j][0] = c0 < P ? (uint32_t)(int)e[c0 / kQ8Group] : 0u;
-        } else {
-          const int g0 = (w + j * W) * 8;
-          he[j][0] = he[j][1] = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if ((g0 + i) * kQ8Group < P) he[j][i / 4] |= (uint32_t)(uint8_t)e[g0 + i] << (8 * (i & 3));
-        }
-      } else {
-        hs[j] = load_chunk<T, VEC>(static_cast<const T*>(a.h) + at, c0, C);
-      }
-    }
-    if (a.dh) {
-#pragma unroll
-      for (int j = 0; j < NCH; ++j)
-        dh[j] = load_chunk<T, VEC>(static_cast<const T*>(a.dh) + at, col0<VEC>(w + j * W, lane), C);
-    }
-    const float rstd = live ? a.rstd[row] : 0.f;
-    auto xhat = [&](int j, float2 (&xh)[4]) {
-      if constexpr (CK) {
-        biased(hq[j], xh);
-        if constexpr (VEC) {
-          const float s = ckpt_step((int)he[j][0]) * rstd;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) xh[i] = mul2(add2(xh[i], f2(-kBias)), f2(s));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float& t = i & 1 ? xh[i / 2].y : xh[i / 2].x;
-            t = (t - kBias) * (ckpt_step((int8_t)(he[j][i / 4] >> (8 * (i & 3)))) * rstd);
-          }
-        }
-      } else {
-        to_pairs(hs[j], xh);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xh[i] = mul2(xh[i], f2(rstd));
-      }
-    };
-    float2 dot2 = f2(0.f);
-#pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      float2 xh[4], d[4], gm[4];
-      xhat(j, xh);
-      to_pairs(dn[j], d);
+      float2 gm[4];
+      xhat(in[j], rstd, xh[j]);
+      to_pairs(in[j].dn, t[j]);
       to_pairs(g[j], gm);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 p = mul2(d[i], xh[i]);
-        if (live) acc[j][i] = add2(acc[j][i], p);
-        dot2 = fma2(p, gm[i], dot2);
+        acc[j][i] = fma2(t[j][i], xh[j][i], acc[j][i]);
+        t[j][i] = mul2(t[j][i], gm[i]);
+        dot2 = fma2(t[j][i], xh[j][i], dot2);
       }
     }
-    float dot = dot2.x + dot2.y;
-    uint32_t unused = 0;
-    row_reduce<TPR>(dot, unused, red, slot);
-    if (!live) continue;
-    const float m = -dot * inv_n;
+    const float m = -row_sum(dot2.x + dot2.y, my_red, slot, w, W, 1 + rib) * inv_n;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      float2 xh[4], d[4], gm[4];
-      xhat(j, xh);
-      to_pairs(dn[j], d);
-      to_pairs(g[j], gm);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = mul2(fma2(xh[i], f2(m), mul2(d[i], gm[i])), f2(rstd));
+      for (int i = 0; i < 4; ++i) t[j][i] = mul2(fma2(xh[j][i], f2(m), t[j][i]), f2(rstd));
       if (a.dh) {
         float2 r[4];
-        to_pairs(dh[j], r);
+        to_pairs(in[j].dh, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = add2(d[i], r[i]);
+        for (int i = 0; i < 4; ++i) t[j][i] = add2(t[j][i], r[i]);
       }
-      store_chunk<T, VEC>(static_cast<T*>(a.dx) + at, col0<VEC>(w + j * W, lane), a.C, d);
+      store_chunk<T, VEC>(static_cast<T*>(a.dx) + (size_t)row * a.C, c_of(j), a.C, t[j]);
     }
   }
   float* pg = a.pg + (size_t)blockIdx.x * a.C;
 #pragma unroll 1
-  for (int r = 0; r < RPB; ++r) {
+  for (int r = 0; r < rpb; ++r) {
     if (rib == r) {
 #pragma unroll
       for (int j = 0; j < NCH; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int c = col<VEC>(col0<VEC>(w + j * W, lane), i);
+          const int c = col<VEC>(c_of(j), i);
           const float v = i & 1 ? acc[j][i / 2].y : acc[j][i / 2].x;
           if (c < a.C) {
-            if (RPB == 1) pg[c] = v;
+            if (rpb == 1) pg[c] = v;
             else cols[c] = r ? cols[c] + v : v;
           }
         }
     }
-    if (RPB > 1) __syncthreads();
+    if (rpb > 1) __syncthreads();
   }
-  if (RPB > 1)
-    for (int c = threadIdx.x; c < a.C; c += TH) pg[c] = cols[c];
+  if (rpb > 1)
+    for (int c = threadIdx.x; c < a.C; c += blockDim.x) pg[c] = cols[c];
 }
 
-// Threads of a row, by its 256-column blocks: a warp holds two.
-int rows_bwd_tpr(int C) {
+// How rows are spread: W warps a row, NCH blocks of 256 columns a warp, rpb
+// rows a thread block (about ten warps).
+struct Spread {
+  int W, nch, rpb, threads;
+};
+Spread spread_of(int C) {
   const int blocks = (q8_pitch(C) + 255) / 256;
-  return blocks <= 2 ? 32 : blocks <= 8 ? 128 : 512;
+  Spread s;
+  s.nch = blocks <= 16 ? 1 : blocks <= 32 ? 2 : 4;
+  s.W = (blocks + s.nch - 1) / s.nch;
+  s.rpb = s.W == 1 ? 8 : s.W < 10 ? 10 / s.W : 1;
+  s.threads = 32 * s.W * s.rpb;
+  return s;
 }
 
 template <typename T, bool CK, bool VEC>
 cudaError_t rows_bwd(const RowsBwd& a, cudaStream_t st) {
-  auto go = [&](auto k, int tpr) {
-    const int th = tpr < 256 ? 256 : tpr;
-    const size_t smem = tpr < 256 ? (size_t)a.C * sizeof(float) : 0;
-    return launch_k(k, dim3((unsigned)rows_bwd_blocks(a.R, a.C)), dim3(th), smem, st, 1, a);
-  };
-  const int tpr = rows_bwd_tpr(a.C);
-  if (tpr == 32) return go(k_rows_bwd<T, 32, 2, CK, VEC>, 32);
-  if (tpr == 128) return go(k_rows_bwd<T, 128, 2, CK, VEC>, 128);
-  if (a.P <= 8192) return go(k_rows_bwd<T, 512, 2, CK, VEC>, 512);
-  return go(k_rows_bwd<T, 512, 4, CK, VEC>, 512);
+  const Spread s = spread_of(a.C);
+  const size_t smem = s.rpb > 1 ? (size_t)a.C * sizeof(float) : 0;
+  auto k = s.nch == 1 ? k_rows_bwd<T, 1, CK, VEC> : s.nch == 2 ? k_rows_bwd<T, 2, CK, VEC> : k_rows_bwd<T, 4, CK, VEC>;
+  return launch_k(k, dim3((unsigned)rows_bwd_blocks(a.R, a.C)), dim3(s.threads), smem, st, 1, a, s.W, s.rpb);
 }
 
 template <typename T>
@@ -175,10 +195,12 @@ cudaError_t rows_bwd_t(const RowsBwd& a, cudaStream_t st) {
 
 }  // namespace
 
+// Blocks resident at once (at most three a SM, each with a partial row).
 int rows_bwd_blocks(long long R, int C) {
-  const int tpr = rows_bwd_tpr(C), rpb = tpr < 256 ? 256 / tpr : 1;
-  const long long want = (R + rpb - 1) / rpb;
-  long long most = (long long)sm_count() * (tpr < 256 ? 2 : 1);  // what is resident at once
+  const Spread s = spread_of(C);
+  const long long want = (R + s.rpb - 1) / s.rpb;
+  const int fit = 65536 / (s.threads * (s.nch > 1 ? 128 : kRegs)), per_sm = fit < 3 ? fit : 3;
+  long long most = (long long)sm_count() * per_sm;
   if (most > kRowsBwdMaxBlocks) most = kRowsBwdMaxBlocks;
   return (int)(want < most ? want : most);
 }
