@@ -69,6 +69,10 @@ class rmx_layer(ctypes.Structure):
                 ("dtype", ctypes.c_int)]
 
 
+class rmx_q8_weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "w1_scale", "wout", "wout_scale")]
+
+
 _VP, _SZ, _I, _P = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.POINTER
 _SIGNATURES = {
     "rmx_saved_bytes": (_SZ, [_P(rmx_config)]),
@@ -104,6 +108,11 @@ _SIGNATURES = {
     "rmx_ckpt8_unpack": (_I, [_P(rmx_rows)] + [_VP] * 4),
     "rmx_ckpt8_wgrad_workspace_bytes": (_SZ, [_P(rmx_layer)]),
     "rmx_ckpt8_wgrad": (_I, [_P(rmx_layer)] + [_VP] * 6 + [_SZ, _VP]),
+    "rmx_forward_q8_workspace_bytes": (_SZ, [_P(rmx_config)]),
+    "rmx_forward_q8": (_I, [_P(rmx_config), _VP, _P(rmx_params), _P(rmx_q8_weights), _VP, _SZ, _VP, _VP]),
+    "rmx_saved8_bytes": (_SZ, [_P(rmx_config)]),
+    "rmx_saved_pack8": (_I, [_P(rmx_config), _VP, _SZ, _VP, _SZ, _VP]),
+    "rmx_saved_unpack8": (_I, [_P(rmx_config), _VP, _SZ, _VP, _SZ, _VP]),
 }
 
 _lib = None
@@ -327,3 +336,30 @@ def rmx_ckpt8_wgrad_workspace_bytes(layer: rmx_layer) -> int:
 def rmx_ckpt8_wgrad(layer: rmx_layer, q, exps, dy, dw, db, ws, ws_bytes: int, stream=None) -> int:
     return lib().rmx_ckpt8_wgrad(ctypes.byref(layer), _ptr(q), _ptr(exps), _ptr(dy), _ptr(dw), _ptr(db), _ptr(ws),
                                  ws_bytes, _stream(stream))
+
+
+def make_q8_weights(w1, w1_scale, wout, wout_scale) -> rmx_q8_weights:
+    return rmx_q8_weights(_ptr(w1), _ptr(w1_scale), _ptr(wout), _ptr(wout_scale))
+
+
+def rmx_forward_q8_workspace_bytes(cfg: rmx_config) -> int:
+    return lib().rmx_forward_q8_workspace_bytes(ctypes.byref(cfg))
+
+
+def rmx_forward_q8(cfg, x, params: rmx_params, weights: rmx_q8_weights, ws, ws_bytes: int, y, stream=None) -> int:
+    return lib().rmx_forward_q8(ctypes.byref(cfg), _ptr(x), ctypes.byref(params), ctypes.byref(weights), _ptr(ws),
+                                ws_bytes, _ptr(y), _stream(stream))
+
+
+def rmx_saved8_bytes(cfg: rmx_config) -> int:
+    return lib().rmx_saved8_bytes(ctypes.byref(cfg))
+
+
+def rmx_saved_pack8(cfg, saved, saved_bytes: int, saved8, saved8_bytes: int, stream=None) -> int:
+    return lib().rmx_saved_pack8(ctypes.byref(cfg), _ptr(saved), saved_bytes, _ptr(saved8), saved8_bytes,
+                                 _stream(stream))
+
+
+def rmx_saved_unpack8(cfg, saved8, saved8_bytes: int, saved, saved_bytes: int, stream=None) -> int:
+    return lib().rmx_saved_unpack8(ctypes.byref(cfg), _ptr(saved8), saved8_bytes, _ptr(saved), saved_bytes,
+                                   _stream(stream))

@@ -32,6 +32,7 @@
 
 #include "api.h"
 #include "common.cuh"
+#include "q8.h"
 
 namespace rmx {
 
@@ -791,6 +792,135 @@ rmx_status backward_checked(const rmx_config* cfg, const void* x, const void* dy
   return backward_impl(*cfg, x, dy, saved, *params, dx, *grads, ws, st, dx_ready);
 }
 
+// ------------------------------------------------------------------ 8-bit forms
+// The 8-bit forms work on the caller's own rows: blocks whose rows need
+// padding, and the TF32 contract, are refused.
+rmx_status q8_support(const rmx_config& c, const Layout& L) {
+  if (L.padded || c.dtype == RMX_F32_TF32) return RMX_ERR_UNSUPPORTED;
+  if (c.D > kQ8MaxCols || c.H > kQ8MaxCols || c.T > 65535) return RMX_ERR_UNSUPPORTED;
+  return kernels_support(c);
+}
+
+// Workspace of the 8-bit forward.
+struct ServeWs {
+  size_t s1, out1, Z, hidden, zstats, stats, q, scale, total;
+};
+ServeWs serve_ws(const rmx_config& c, const Layout& L) {
+  ServeWs w;
+  const size_t e = esize(c.dtype), N = (size_t)c.B * c.T, D = L.D, H = L.H;
+  size_t o = 0;
+  w.s1 = o; o = up(o + N * D * e);        // norm1's input, then norm2's
+  w.out1 = o; o = up(o + N * D * e);
+  w.Z = o; o = up(o + N * 2 * H * e);
+  w.hidden = o; o = up(o + N * H * e);
+  w.zstats = o; o = up(o + N * (size_t)zstats_tiles(L.H) * 4 * sizeof(float));
+  w.stats = o; o = up(o + 10 * N * sizeof(float));
+  const size_t pd = q8_pitch(c.D), ph = q8_pitch(c.H);
+  w.q = o; o = up(o + N * (pd > ph ? pd : ph));  // out1, then hidden, as int8 rows
+  w.scale = o; o = up(o + N * sizeof(float));
+  w.total = o;
+  return w;
+}
+
+rmx_status quant_rows(const void* x, int8_t* q, float* scale, size_t rows, int cols, int dtype, cudaStream_t st) {
+  RowsFwd a{(long long)rows, cols, q8_pitch(cols), dtype, 0, 0.f, x, nullptr, nullptr, nullptr, nullptr, q, scale, nullptr};
+  Launch l("quant_rows_q8", st);
+  return l.done(launch_rows_fwd(a, st));
+}
+
+// The forward with both contractions in int8: out1 and hidden are quantised
+// row by row (one scale per sample and token), everything else is the
+// forward's own passes.
+rmx_status forward_q8_impl(const rmx_config& c, const Layout& L, const void* x, const rmx_params& p,
+                           const rmx_q8_weights& qw, void* ws, void* y, cudaStream_t st) {
+  const ServeWs w = serve_ws(c, L);
+  const size_t N = (size_t)c.B * c.T;
+  const RowArgs& ra = L.ra;
+  void *s1 = at(ws, w.s1), *out1 = at(ws, w.out1), *Z = at(ws, w.Z), *hidden = at(ws, w.hidden);
+  int8_t* q = reinterpret_cast<int8_t*>(at(ws, w.q));
+  float* scale = reinterpret_cast<float*>(at(ws, w.scale));
+  float* f = reinterpret_cast<float*>(at(ws, w.stats));
+  auto stat = [&](int i) { return f + (size_t)i * N; };
+  if (ln01_fwd_supported(ra)) {
+    Launch l("ln01_fwd", st);
+    RMX_TRY(l.done(launch_ln01_fwd(ra, x, p.gamma0, p.beta0, p.gamma1, p.beta1, s1, out1, stat(0), stat(1), stat(2),
+                                   stat(3), st)));
+  } else {
+    {
+      Launch l("ln0_fwd_mixed", st);
+      RMX_TRY(l.done(launch_ln_fwd(ra, LNF_MIXED_OUT, x, nullptr, p.gamma0, p.beta0, s1, stat(0), stat(1), nullptr, st)));
+    }
+    Launch l("ln1_fwd", st);
+    RMX_TRY(l.done(launch_ln_fwd(ra, LNF_SUM_IN, s1, x, p.gamma1, p.beta1, out1, stat(2), stat(3), s1, st)));
+  }
+  RMX_TRY(quant_rows(out1, q, scale, N, c.D, c.dtype, st));
+  {
+    const LinearQ8 d{c.B, c.T, c.D, 2 * c.H, q8_pitch(c.D), c.dtype, q, qw.w1, scale, qw.w1_scale, p.b1, nullptr, Z};
+    Launch l("linear_q8", st);
+    RMX_TRY(l.done(launch_linear_q8(d, device_error_word(), st)));
+  }
+  if (gate_fwd_rows_supported(ra)) {
+    Launch l("gate_fwd", st);
+    RMX_TRY(l.done(launch_gate_fwd_rows(ra, Z, stat(6), stat(7), stat(8), stat(9), p.lnx_w, p.lnx_b, p.lng_w, p.lng_b,
+                                        hidden, st)));
+  } else {
+    float* zstats = reinterpret_cast<float*>(at(ws, w.zstats));
+    {
+      Launch l("zstats", st);
+      RMX_TRY(l.done(launch_zstats(ra, Z, zstats, st)));
+    }
+    Launch l("gate_fwd", st);
+    RMX_TRY(l.done(launch_gate_fwd(ra, Z, zstats, stat(6), stat(7), stat(8), stat(9), p.lnx_w, p.lnx_b, p.lng_w,
+                                   p.lng_b, hidden, st)));
+  }
+  RMX_TRY(quant_rows(hidden, q, scale, N, c.H, c.dtype, st));
+  {
+    const LinearQ8 d{c.B, c.T, c.H, c.D, q8_pitch(c.H), c.dtype, q, qw.wout, scale, qw.wout_scale, p.bout, out1, s1};
+    Launch l("linear_q8", st);
+    RMX_TRY(l.done(launch_linear_q8(d, device_error_word(), st)));
+  }
+  Launch l("ln2_fwd", st);
+  return l.done(launch_ln_fwd(ra, LNF_PLAIN, s1, nullptr, p.gamma2, p.beta2, y, stat(4), stat(5), nullptr, st));
+}
+
+// The saved tensors of the forward as 8-bit checkpoints, in order: out1, Z,
+// hidden, s2, s1 (int8 rows, then exponents), then the row statistics.
+struct Saved8 {
+  struct Part {
+    size_t from;  // offset in `saved`
+    int cols;
+    size_t q, e;  // offsets in the packed buffer
+  } part[5];
+  size_t stats, total;
+};
+Saved8 saved8_of(const rmx_config& c, const Layout& L) {
+  Saved8 s;
+  const size_t N = (size_t)c.B * c.T;
+  const struct {
+    size_t from;
+    int cols;
+  } t[5] = {{L.out1, c.D}, {L.Z, 2 * c.H}, {L.hidden, c.H}, {L.s2, c.D}, {L.s1, c.D}};
+  size_t o = 0;
+  for (int i = 0; i < 5; ++i) {
+    s.part[i].from = t[i].from;
+    s.part[i].cols = t[i].cols;
+    const size_t P = q8_pitch(t[i].cols);
+    s.part[i].q = o; o = up(o + N * P);
+    s.part[i].e = o; o = up(o + N * (P / kQ8Group));
+  }
+  s.stats = o; o = up(o + 10 * N * sizeof(float));
+  s.total = o;
+  return s;
+}
+
+// params without the two weights the 8-bit forward replaces
+rmx_status check_small_params(const rmx_params* p) {
+  if (!p) return RMX_ERR_INVALID_ARG;
+  rmx_params q = *p;
+  q.w1 = q.wout = p->b1;
+  return check_params(&q);
+}
+
 }  // namespace
 }  // namespace rmx
 
@@ -872,6 +1002,86 @@ rmx_status rmx_step_host(const rmx_config* cfg, const rmx_host_io* host, const r
   if (!ok(cudaEventRecord(cs->done, cs->s))) return RMX_ERR_CUDA;
   if (!ok(cudaStreamWaitEvent(st, cs->done, 0))) return RMX_ERR_CUDA;
   return RMX_OK;
+}
+
+// ------------------------------------------------------------------ 8-bit forms
+size_t rmx_forward_q8_workspace_bytes(const rmx_config* cfg) {
+  if (!config_ok(cfg)) return 0;
+  const Layout L = layout_of(*cfg);
+  if (cfg->B > 0 && q8_support(*cfg, L) != RMX_OK) return 0;
+  return serve_ws(*cfg, L).total;
+}
+
+rmx_status rmx_forward_q8(const rmx_config* cfg, const void* x, const rmx_params* params, const rmx_q8_weights* weights,
+                          void* ws, size_t ws_bytes, void* y, rmx_stream stream) {
+  if (!config_ok(cfg) || !weights) return RMX_ERR_INVALID_ARG;
+  RMX_TRY(check_small_params(params));
+  for (const void* p : {(const void*)weights->w1, (const void*)weights->w1_scale, (const void*)weights->wout,
+                        (const void*)weights->wout_scale})
+    RMX_TRY(check_ptr(p));
+  if (cfg->B == 0) return RMX_OK;
+  RMX_TRY(check_ptr(x));
+  RMX_TRY(check_ptr(y));
+  RMX_TRY(check_ptr(ws));
+  if (x == y) return RMX_ERR_INVALID_ARG;
+  const Layout L = layout_of(*cfg);
+  RMX_TRY(q8_support(*cfg, L));
+  if (ws_bytes < serve_ws(*cfg, L).total) return RMX_ERR_WORKSPACE;
+  return forward_q8_impl(*cfg, L, x, *params, *weights, ws, y, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t rmx_saved8_bytes(const rmx_config* cfg) {
+  if (!config_ok(cfg)) return 0;
+  const Layout L = layout_of(*cfg);
+  if (cfg->B > 0 && q8_support(*cfg, L) != RMX_OK) return 0;
+  return saved8_of(*cfg, L).total;
+}
+
+rmx_status rmx_saved_pack8(const rmx_config* cfg, const void* saved, size_t saved_bytes, void* saved8,
+                           size_t saved8_bytes, rmx_stream stream) {
+  if (!config_ok(cfg)) return RMX_ERR_INVALID_ARG;
+  if (cfg->B == 0) return RMX_OK;
+  RMX_TRY(check_ptr(saved));
+  RMX_TRY(check_ptr(saved8));
+  const Layout L = layout_of(*cfg);
+  RMX_TRY(q8_support(*cfg, L));
+  const Saved8 s = saved8_of(*cfg, L);
+  if (saved_bytes < L.saved_total || saved8_bytes < s.total) return RMX_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const size_t N = (size_t)cfg->B * cfg->T;
+  for (const auto& p : s.part) {
+    Launch l("ckpt8_pack", st);
+    RMX_TRY(l.done(launch_ckpt_pack((long long)N, p.cols, cfg->dtype, at(saved, p.from),
+                                    reinterpret_cast<int8_t*>(at(saved8, p.q)),
+                                    reinterpret_cast<int8_t*>(at(saved8, p.e)), st)));
+  }
+  return cudaMemcpyAsync(at(saved8, s.stats), at(saved, L.stats), 10 * N * sizeof(float), cudaMemcpyDeviceToDevice,
+                         st) == cudaSuccess
+             ? RMX_OK
+             : RMX_ERR_CUDA;
+}
+
+rmx_status rmx_saved_unpack8(const rmx_config* cfg, const void* saved8, size_t saved8_bytes, void* saved,
+                             size_t saved_bytes, rmx_stream stream) {
+  if (!config_ok(cfg)) return RMX_ERR_INVALID_ARG;
+  if (cfg->B == 0) return RMX_OK;
+  RMX_TRY(check_ptr(saved));
+  RMX_TRY(check_ptr(saved8));
+  const Layout L = layout_of(*cfg);
+  RMX_TRY(q8_support(*cfg, L));
+  const Saved8 s = saved8_of(*cfg, L);
+  if (saved_bytes < L.saved_total || saved8_bytes < s.total) return RMX_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const size_t N = (size_t)cfg->B * cfg->T;
+  for (const auto& p : s.part) {
+    Launch l("ckpt8_unpack", st);
+    RMX_TRY(l.done(launch_ckpt_unpack((long long)N, p.cols, cfg->dtype, reinterpret_cast<const int8_t*>(at(saved8, p.q)),
+                                      reinterpret_cast<const int8_t*>(at(saved8, p.e)), at(saved, p.from), p.cols, st)));
+  }
+  return cudaMemcpyAsync(at(saved, L.stats), at(saved8, s.stats), 10 * N * sizeof(float), cudaMemcpyDeviceToDevice,
+                         st) == cudaSuccess
+             ? RMX_OK
+             : RMX_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ graph replay

@@ -59,6 +59,38 @@ class RankMixerDevice:
         self.forward(stream)
         self.backward(stream)
 
+    # ---------------------------------------------------------------- 8 bits
+
+    def quantize_weights(self, stream=None) -> None:
+        """int8 copies of w1 and wout for forward_q8 (once per weight update)."""
+        s = self.shape
+        self.q8 = {}
+        for name, K, N in (("w1", s.D, 2 * s.H), ("wout", s.H, s.D)):
+            q = torch.empty((s.T, N, B.rmx_q8_pitch(K)), dtype=torch.int8, device=self.device)
+            scale = torch.empty((s.T, N), dtype=torch.float32, device=self.device)
+            B.check(B.rmx_weight_q8(B.make_layer(max(s.B, 1), s.T, K, N, s.dtype), self.params[name], q, scale, stream),
+                    "rmx_weight_q8")
+            self.q8[name], self.q8[name + "_scale"] = q, scale
+        self.c_q8 = B.make_q8_weights(self.q8["w1"], self.q8["w1_scale"], self.q8["wout"], self.q8["wout_scale"])
+        self.ws_q8 = torch.empty(max(B.rmx_forward_q8_workspace_bytes(self.cfg), 1), dtype=torch.uint8,
+                                 device=self.device)
+
+    def forward_q8(self, stream=None) -> None:
+        """The forward for serving: int8 contractions, nothing saved."""
+        B.check(B.rmx_forward_q8(self.cfg, _ptr_or_none(self.x), self.c_params, self.c_q8, self.ws_q8,
+                                 self.ws_q8.numel(), _ptr_or_none(self.y), stream), "rmx_forward_q8")
+
+    def pack_saved(self, stream=None) -> torch.Tensor:
+        """The saved activations of the last forward as 8-bit checkpoints."""
+        out = torch.empty(max(B.rmx_saved8_bytes(self.cfg), 1), dtype=torch.uint8, device=self.device)
+        B.check(B.rmx_saved_pack8(self.cfg, self.saved, self.saved_bytes, out, out.numel(), stream), "rmx_saved_pack8")
+        return out
+
+    def unpack_saved(self, packed: torch.Tensor, stream=None) -> None:
+        """Checkpoints of pack_saved back into the saved buffer, for backward()."""
+        B.check(B.rmx_saved_unpack8(self.cfg, packed, packed.numel(), self.saved, self.saved_bytes, stream),
+                "rmx_saved_unpack8")
+
     def results(self) -> dict:
         """y, dx and every gradient as float64 numpy arrays (synchronises)."""
         torch.cuda.synchronize(self.device)

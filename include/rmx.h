@@ -369,6 +369,40 @@ size_t rmx_ckpt8_wgrad_workspace_bytes(const rmx_layer* layer);
 rmx_status rmx_ckpt8_wgrad(const rmx_layer* layer, const int8_t* q, const int8_t* exps, const void* dy, void* dw,
                            void* db, void* ws, size_t ws_bytes, rmx_stream stream);
 
+/* ------------------------------------------------------------------------
+ * The block in 8 bits.  Both forms take rmx_config's block as it is: rows that
+ * need padded copies (D or H not a multiple of 8) and RMX_F32_TF32 are refused
+ * (RMX_ERR_UNSUPPORTED; the byte counts are 0). */
+
+/* The two weights of a block for rmx_forward_q8, from rmx_weight_q8 on w1 (as a
+ * layer G = T, K = D, N = 2H) and wout (G = T, K = H, N = D). */
+typedef struct {
+  const int8_t* w1;        /* [T, 2H, rmx_q8_pitch(D)] */
+  const float* w1_scale;   /* [T, 2H] */
+  const int8_t* wout;      /* [T, D, rmx_q8_pitch(H)] */
+  const float* wout_scale; /* [T, D] */
+} rmx_q8_weights;
+
+/* Forward pass for serving: rmx_forward with both contractions in int8 (their
+ * inputs out1 and hidden quantised per sample and token) and nothing saved.
+ * params->w1 and params->wout are not read and may be null.  ws: scratch of
+ * rmx_forward_q8_workspace_bytes.  x and y may not alias. */
+size_t rmx_forward_q8_workspace_bytes(const rmx_config* cfg);
+rmx_status rmx_forward_q8(const rmx_config* cfg, const void* x, const rmx_params* params, const rmx_q8_weights* weights,
+                          void* ws, size_t ws_bytes, void* y, rmx_stream stream);
+
+/* The `saved` buffer as 8-bit checkpoints, about half its bytes (bfloat16) or a
+ * quarter (float32), for a program that keeps those of several blocks between
+ * their forward and their backward: pack after rmx_forward, and unpack into one
+ * shared `saved` buffer before rmx_backward.  Every saved tensor is off by at
+ * most half a step of its 32-column groups; the row statistics are kept as they
+ * are. */
+size_t rmx_saved8_bytes(const rmx_config* cfg);
+rmx_status rmx_saved_pack8(const rmx_config* cfg, const void* saved, size_t saved_bytes, void* saved8,
+                           size_t saved8_bytes, rmx_stream stream);
+rmx_status rmx_saved_unpack8(const rmx_config* cfg, const void* saved8, size_t saved8_bytes, void* saved,
+                             size_t saved_bytes, rmx_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

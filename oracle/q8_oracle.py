@@ -95,3 +95,25 @@ def linear_q8(a, sa, w, sw, bias, resid, K):
 def wgrad(x, dy):
     """x [M, G, K], dy [M, G, N] -> dw [G, K, N], db [G, N]."""
     return np.einsum("mgk,mgn->gkn", x, dy, optimize=True), dy.sum(0)
+
+
+def block_forward_q8(x, p, w1q, w1s, woutq, wouts):
+    """The RankMixer block's forward with int8 contractions: out1 and hidden
+    quantised per row, the weights given as int8 [T, N, pitch] and scales."""
+    from . import rmx_oracle as O
+    B, T, D = x.shape
+    H = p["lnx_w"].shape[0]
+    n0, _ = O.layer_norm(x, p["gamma0"], p["beta0"], 1e-3)
+    out1, _ = O.layer_norm(O.token_mixer(n0) + x, p["gamma1"], p["beta1"], 1e-3)
+
+    def product(a, wq, ws, bias, resid):
+        K = a.shape[-1]
+        q, s = quant_rows(a.reshape(B * T, K))
+        return linear_q8(q.reshape(B, T, -1), s.reshape(B, T), wq, ws, bias, resid, K)
+
+    Z = product(out1, w1q, w1s, p["b1"], None)
+    U, G = Z[..., :H], Z[..., H:]
+    u, _ = O.layer_norm(U, p["lnx_w"], p["lnx_b"], 1e-5)
+    g, _ = O.layer_norm(G, p["lng_w"], p["lng_b"], 1e-5)
+    s2 = product(u * O.silu(g), woutq, wouts, p["bout"], out1)
+    return O.layer_norm(s2, p["gamma2"], p["beta2"], 1e-3)[0]
