@@ -154,6 +154,106 @@ __device__ __forceinline__ void next_place(const Flat& f, Place& p) {
   p.row += wrap ? 1 : 0;
 }
 
+// Bits of the largest magnitude of a group of 32: the eight values of this lane
+// and of the three beside it.  16-bit types compare as integers two at a time,
+// without the sign; NaN comes out above infinity above every number.
+__device__ __forceinline__ uint32_t group_max(const Chunk<float>& k) {
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) am = max_abs(am, make_float2(k.v[i], k.v[i + 1]));
+  uint32_t u = __float_as_uint(am);
+  u = max(u, __shfl_xor_sync(0xffffffffu, u, 1));
+  return max(u, __shfl_xor_sync(0xffffffffu, u, 2));
+}
+template <typename T> __device__ __forceinline__ uint32_t group_max(const Chunk<T>& k) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&k);
+  uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t top = max(m >> 16, m & 0xffffu);
+  if constexpr (std::is_same<T, bf16>::value) return top << 16;
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
+}
+// Eight values of a group as int8, and the group's exponent.
+template <typename T> __device__ __forceinline__ uint2 pack_group(const Chunk<T>& k, int& ex) {
+  const uint32_t u = group_max(k);
+  ex = ckpt_exp<T>(u);
+  const float inv = pow2(-ex);  // exact, and so is the scaling: the only rounding is to the integer
+  float2 v[4];
+  to_pairs(k, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = round2(v[i], inv);
+  if (__uint_as_float(u) * inv >= 127.5f) {
+    // 128 steps: the upper clamp, and exactly 127.5.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i].x = fminf(fmaxf(v[i].x, kRound - 127.f), kRound + 127.f);
+      v[i].y = fminf(fmaxf(v[i].y, kRound - 127.f), kRound + 127.f);
+    }
+  }
+  return ex == kCkptNaN ? make_uint2(0, 0) : low_bytes(v);
+}
+
+// Rows that are a whole number of groups lie in memory as one run of groups,
+// and so do their exponents: a checkpoint of `total` blocks of 256 columns,
+// whatever the rows' length.  Addresses are one base and constants (a third of
+// the general form's instructions, which bound it: 53 -> 41 us a pass over
+// 65536 x 1280 16-bit values each way).
+template <typename T>
+__global__ void __launch_bounds__(256) k_ckpt_pack_flat(long long total, const T* x, int8_t* q, int8_t* e) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const long long b0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kBatch;
+  const T* xp = x + b0 * 256 + lane * 8;
+  int8_t* qp = q + b0 * 256 + lane * 8;
+  int8_t* ep = e + b0 * 8 + (lane >> 2);
+  auto store = [&](const Chunk<T>& k, int j) {
+    int ex;
+    *reinterpret_cast<uint2*>(qp + j * 256) = pack_group(k, ex);
+    if ((lane & 3) == 0) ep[j * 8] = (int8_t)ex;
+  };
+  if (b0 + kBatch <= total) {
+    Chunk<T> k[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) k[j] = load_chunk<T, true>(xp + j * 256, 0, 8);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) store(k[j], j);
+  } else {
+    for (int j = 0; b0 + j < total; ++j) store(load_chunk<T, true>(xp + j * 256, 0, 8), j);
+  }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) k_unpack_flat(long long total, const int8_t* q, const int8_t* e, T* x) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const long long b0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kBatch;
+  const int8_t* qp = q + b0 * 256 + lane * 8;
+  const int8_t* ep = e + b0 * 8 + (lane >> 2);
+  T* xp = x + b0 * 256 + lane * 8;
+  auto store = [&](uint2 b, int ex, int j) {
+    const float s = ckpt_step(ex);
+    float2 v[4];
+    biased(b, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(add2(v[i], f2(-kBias)), f2(s));
+    store_chunk<T, true>(xp + j * 256, 0, 8, v);
+  };
+  if (b0 + kBatch <= total) {
+    uint2 b[kBatch];
+    int ex[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) b[j] = *reinterpret_cast<const uint2*>(qp + j * 256);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) ex[j] = ep[j * 8];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) store(b[j], ex[j], j);
+  } else {
+    for (int j = 0; b0 + j < total; ++j) store(*reinterpret_cast<const uint2*>(qp + j * 256), ep[j * 8], j);
+  }
+}
+
 // The 32 columns of a group are four neighbouring lanes (VEC) or one element of
 // every lane.
 template <typename T, bool VEC>
@@ -177,30 +277,14 @@ __global__ void __launch_bounds__(256) k_ckpt_pack(const Flat f, const T* x, int
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (b0 + j >= f.total) break;
-      float2 v[4];
-      to_pairs(k[j], v);
       if constexpr (VEC) {
-        float am = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) am = max_abs(am, v[i]);
-        uint32_t u = __float_as_uint(am);
-        u = max(u, __shfl_xor_sync(0xffffffffu, u, 1));
-        u = max(u, __shfl_xor_sync(0xffffffffu, u, 2));
-        const int ex = ckpt_exp<T>(u);
-        const float inv = pow2(-ex);  // exact, and so is the scaling: the only rounding is to the integer
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = round2(v[i], inv);
-        if (__uint_as_float(u) * inv >= 127.5f) {
-          // 128 steps: the upper clamp, and exactly 127.5.
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i].x = fminf(fmaxf(v[i].x, kRound - 127.f), kRound + 127.f);
-            v[i].y = fminf(fmaxf(v[i].y, kRound - 127.f), kRound + 127.f);
-          }
-        }
-        store_bytes<VEC>(q + row[j] * f.P, c0[j], f.P, v, ex != kCkptNaN);
+        int ex;
+        const uint2 b = pack_group(k[j], ex);
+        if (c0[j] < f.P) *reinterpret_cast<uint2*>(q + row[j] * f.P + c0[j]) = b;
         if ((lane & 3) == 0 && c0[j] < f.P) e[row[j] * groups + c0[j] / kQ8Group] = (int8_t)ex;
       } else {
+        float2 v[4];
+        to_pairs(k[j], v);
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -383,7 +467,17 @@ cudaError_t launch_dequant_rows(long long R, int C, int dtype, const int8_t* q, 
                                       dim3(flat_grid(f)), dim3(256), 0, st, 1, f, q, s, static_cast<T*>(x), C))
 }
 
+// Whether a checkpoint can be taken as one run of 256-column blocks.
+static bool ckpt_flat(long long R, int C) { return C % kQ8Group == 0 && R * C % 256 == 0 && R * C / 256 < (1ll << 35); }
+static dim3 ckpt_flat_grid(long long R, int C) {
+  return dim3((unsigned)((R * C / 256 + 8 * kBatch - 1) / (8 * kBatch)));
+}
+
 cudaError_t launch_ckpt_pack(long long R, int C, int dtype, const void* x, int8_t* q, int8_t* e, cudaStream_t st) {
+  if (ckpt_flat(R, C)) {
+    RMX_BY_DTYPE(dtype, return launch_k(k_ckpt_pack_flat<T>, ckpt_flat_grid(R, C), dim3(256), 0, st, 1, R * C / 256,
+                                        static_cast<const T*>(x), q, e))
+  }
   const Flat f = flat_of(R, C);
   RMX_BY_DTYPE(dtype, return launch_k(rows_aligned(C, sizeof(T)) ? k_ckpt_pack<T, true> : k_ckpt_pack<T, false>,
                                       dim3(flat_grid(f)), dim3(256), 0, st, 1, f, static_cast<const T*>(x), q, e))
@@ -391,6 +485,10 @@ cudaError_t launch_ckpt_pack(long long R, int C, int dtype, const void* x, int8_
 
 cudaError_t launch_ckpt_unpack(long long R, int C, int dtype, const int8_t* q, const int8_t* e, void* x, int pitch,
                                cudaStream_t st) {
+  if (pitch == C && ckpt_flat(R, C)) {
+    RMX_BY_DTYPE(dtype, return launch_k(k_unpack_flat<T>, ckpt_flat_grid(R, C), dim3(256), 0, st, 1, R * C / 256, q, e,
+                                        static_cast<T*>(x)))
+  }
   const Flat f = flat_of(R, C);
   const void* s = e;
   RMX_BY_DTYPE(dtype, return launch_k(rows_aligned(pitch, sizeof(T)) ? k_unpack<T, true, true> : k_unpack<T, true, false>,
