@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(256) k_ckpt_pack_flat(long long total, const T
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const long long b0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kBatch;
+  if (b0 >= total) return;
   const T* xp = x + b0 * 256 + lane * 8;
   int8_t* qp = q + b0 * 256 + lane * 8;
   int8_t* ep = e + b0 * 8 + (lane >> 2);
@@ -224,11 +225,44 @@ __global__ void __launch_bounds__(256) k_ckpt_pack_flat(long long total, const T
     for (int j = 0; b0 + j < total; ++j) store(load_chunk<T, true>(xp + j * 256, 0, 8), j);
   }
 }
+// The same for q8 rows of a whole number of blocks (f.bpr of them), each block
+// with its row's scale.
+template <typename T>
+__global__ void __launch_bounds__(256) k_dequant_flat(const Flat f, const int8_t* q, const float* scale, T* x) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const long long b0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kBatch;
+  if (b0 >= f.total) return;
+  const int8_t* qp = q + b0 * 256 + lane * 8;
+  T* xp = x + b0 * 256 + lane * 8;
+  Place p = place_of(f, b0);
+  auto store = [&](uint2 b, float s, int j) {
+    float2 v[4];
+    biased(b, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(add2(v[i], f2(-kBias)), f2(s));
+    store_chunk<T, true>(xp + j * 256, 0, 8, v);
+  };
+  if (b0 + kBatch <= f.total) {
+    uint2 b[kBatch];
+    float s[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) b[j] = *reinterpret_cast<const uint2*>(qp + j * 256);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j, next_place(f, p)) s[j] = scale[p.row];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) store(b[j], s[j], j);
+  } else {
+    for (int j = 0; b0 + j < f.total; ++j, next_place(f, p))
+      store(*reinterpret_cast<const uint2*>(qp + j * 256), scale[p.row], j);
+  }
+}
 template <typename T>
 __global__ void __launch_bounds__(256) k_unpack_flat(long long total, const int8_t* q, const int8_t* e, T* x) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const long long b0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kBatch;
+  if (b0 >= total) return;
   const int8_t* qp = q + b0 * 256 + lane * 8;
   const int8_t* ep = e + b0 * 8 + (lane >> 2);
   T* xp = x + b0 * 256 + lane * 8;
@@ -462,6 +496,10 @@ cudaError_t launch_rows_fwd(const RowsFwd& a, cudaStream_t st) {
 cudaError_t launch_dequant_rows(long long R, int C, int dtype, const int8_t* q, const float* scale, void* x,
                                 cudaStream_t st) {
   const Flat f = flat_of(R, C);
+  if (C % 256 == 0 && f.total < (1ll << 35)) {
+    RMX_BY_DTYPE(dtype, return launch_k(k_dequant_flat<T>, dim3((unsigned)((f.total + 8 * kBatch - 1) / (8 * kBatch))),
+                                        dim3(256), 0, st, 1, f, q, scale, static_cast<T*>(x)))
+  }
   const void* s = scale;
   RMX_BY_DTYPE(dtype, return launch_k(rows_aligned(C, sizeof(T)) ? k_unpack<T, false, true> : k_unpack<T, false, false>,
                                       dim3(flat_grid(f)), dim3(256), 0, st, 1, f, q, s, static_cast<T*>(x), C))
