@@ -6,8 +6,8 @@
 // gathered into padded buffers before the passes, y, dx and the gradients are
 // gathered back afterwards.  The zeros are exact no-ops for the contractions
 // (zero rows and columns of the weights), and the LayerNorm passes take their
-// means over the real columns only.  One thread per destination element, so
-// every padded place is written (with 0) and nothing needs clearing first.
+// means over the real columns only.  Every destination element is written (a
+// padded place with 0), so nothing needs clearing first.
 
 #include "common.cuh"
 #include "kernels.h"
@@ -16,28 +16,35 @@
 namespace rmx {
 namespace {
 
+// Eight warps a CTA; a warp takes one destination row at a time (its place is
+// worked out once), neighbouring lanes neighbouring columns.
 template <typename E>
 __global__ void __launch_bounds__(256) k_pad_copy(const E* __restrict__ src, E* __restrict__ dst, PadMap m,
                                                   int pack) {
   pdl_enter();
   const int hs = m.cols / m.halves, hsp = m.cols_p / m.halves;
   const int dcols = pack ? m.cols_p : m.cols, drows = pack ? m.rows_p : m.rows;
-  const size_t total = (size_t)m.outer * drows * dcols;
-  for (size_t idx = (size_t)blockIdx.x * blockDim.x + threadIdx.x; idx < total;
-       idx += (size_t)gridDim.x * blockDim.x) {
-    const int c = (int)(idx % dcols);
-    const size_t rr = idx / dcols;
-    const int r = (int)(rr % drows);
-    const size_t o = rr / drows;
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)m.outer * drows, step = (long long)gridDim.x * 8;
+  for (long long d = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); d < rows; d += step) {
+    const long long o = d / drows;
+    const int r = (int)(d - o * drows);
+    E* out = dst + d * dcols;
     if (pack) {
-      // padded (o, r, c) <- logical (o, r, h * hs + cc) with c = h * hsp + cc
-      const int h = c / hsp, cc = c - h * hsp;
-      const bool real = r < m.rows && cc < hs;
-      dst[idx] = real ? src[(o * m.rows + r) * (size_t)m.cols + (size_t)h * hs + cc] : E(0);
+      // padded (o, r, h * hsp + cc) <- logical (o, r, h * hs + cc)
+      const E* in = src + (o * m.rows + r) * (long long)m.cols;
+      for (int h = 0; h < m.halves; ++h) {
+#pragma unroll 8
+        for (int cc = lane; cc < hsp; cc += 32)
+          out[h * hsp + cc] = r < m.rows && cc < hs ? in[h * hs + cc] : E(0);
+      }
     } else {
-      // logical (o, r, c) <- padded (o, r, h * hsp + cc) with c = h * hs + cc
-      const int h = c / hs, cc = c - h * hs;
-      dst[idx] = src[(o * m.rows_p + r) * (size_t)m.cols_p + (size_t)h * hsp + cc];
+      // logical (o, r, h * hs + cc) <- padded (o, r, h * hsp + cc)
+      const E* in = src + (o * m.rows_p + r) * (long long)m.cols_p;
+      for (int h = 0; h < m.halves; ++h) {
+#pragma unroll 8
+        for (int cc = lane; cc < hs; cc += 32) out[h * hs + cc] = in[h * hsp + cc];
+      }
     }
   }
 }
@@ -82,7 +89,7 @@ cudaError_t launch_pad_copy(const void* src, void* dst, int dtype, const PadMap&
     return cudaErrorInvalidValue;
   const size_t total = (size_t)m.outer * (pack ? (size_t)m.rows_p * m.cols_p : (size_t)m.rows * m.cols);
   if (total == 0) return cudaSuccess;
-  const size_t want = (total + 255) / 256;
+  const size_t want = ((size_t)m.outer * (pack ? m.rows_p : m.rows) + 7) / 8;
   const int grid = (int)(want < (size_t)sm_count() * 16 ? want : (size_t)sm_count() * 16);
   if (dtype == 0)
     return launch_k(k_pad_copy<uint32_t>, dim3(grid), dim3(256), 0, st, 1, static_cast<const uint32_t*>(src),

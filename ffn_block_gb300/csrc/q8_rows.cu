@@ -4,8 +4,8 @@
 //
 // All are bound by HBM traffic: each reads every input once and writes every
 // output once, a row held in registers between its reduction and its output.
-// A row belongs to one, four or sixteen warps, whichever hold it in at most
-// five blocks of 256 columns each.
+// A row belongs to 8 or 16 lanes, or to one, four or sixteen warps, whichever
+// hold it in at most five blocks of eight columns a lane.
 
 #include "common.cuh"
 #include "kernels.h"
@@ -21,19 +21,19 @@ namespace {
 // int8 scale the row's largest |n| = rstd * max|h * gamma|, so both come from
 // one reduction, and q = round(h * gamma * 127 / max|h * gamma|) needs no
 // rstd at all.
-template <typename T, int TPR, int NCH, bool VEC>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 256 ? 2 : 1) k_rows_fwd(const RowsFwd a) {
+template <typename T, int L, int W, int NCH, bool VEC>
+__global__ void __launch_bounds__(W * L < 256 ? 256 : W * L, W * L < 256 ? 2 : 1) k_rows_fwd(const RowsFwd a) {
   pdl_enter();
-  constexpr int TH = TPR < 256 ? 256 : TPR, RPB = TH / TPR, W = TPR / 32;
-  __shared__ uint32_t red[RPB * 4 * W];
-  const int lane = threadIdx.x & 31, w = (threadIdx.x & (TPR - 1)) >> 5, rib = threadIdx.x / TPR;
+  constexpr int TH = W * L < 256 ? 256 : W * L, RPB = TH / (W * L);
+  __shared__ uint32_t red[W > 1 ? RPB * 4 * W : 1];
+  const int lane = threadIdx.x & (L - 1), rib = threadIdx.x / (W * L), w = (threadIdx.x - rib * (W * L)) / L;
   const float inv_n = 1.f / (float)a.C;
   int slot = 0;
   Chunk<T> g[NCH];
   if (a.norm) {
 #pragma unroll
     for (int j = 0; j < NCH; ++j)
-      g[j] = load_chunk<T, VEC>(static_cast<const T*>(a.gamma), col0<VEC>(w + j * W, lane), a.C);
+      g[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.gamma), col0<L, VEC>(w + j * W, lane), a.C);
   }
   for (long long base = (long long)blockIdx.x * RPB; base < a.R; base += (long long)gridDim.x * RPB) {
     const long long row = base + rib;
@@ -43,11 +43,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 256 ? 2 : 1) k_ro
     float2 v[NCH][4];
     Chunk<T> cx[NCH], cr[NCH];
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) cx[j] = load_chunk<T, VEC>(static_cast<const T*>(a.x) + at, col0<VEC>(w + j * W, lane), C);
+    for (int j = 0; j < NCH; ++j) cx[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.x) + at, col0<L, VEC>(w + j * W, lane), C);
     if (a.r) {
 #pragma unroll
       for (int j = 0; j < NCH; ++j)
-        cr[j] = load_chunk<T, VEC>(static_cast<const T*>(a.r) + at, col0<VEC>(w + j * W, lane), C);
+        cr[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.r) + at, col0<L, VEC>(w + j * W, lane), C);
     }
     float2 ss = f2(0.f);
     float am = 0.f;
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 256 ? 2 : 1) k_ro
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], r[i]);
       }
-      if (a.h) store_chunk<T, VEC>(static_cast<T*>(a.h) + at, col0<VEC>(w + j * W, lane), C, v[j]);
+      if (a.h) store_chunk<T, L, VEC>(static_cast<T*>(a.h) + at, col0<L, VEC>(w + j * W, lane), C, v[j]);
       if (a.norm) {
         float2 gm[4];
         to_pairs(g[j], gm);
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 256 ? 2 : 1) k_ro
     }
     float sum = ss.x + ss.y;
     uint32_t top = __float_as_uint(am);  // NaN above infinity above every number
-    row_reduce<TPR>(sum, top, red, slot);
+    row_reduce<W, L>(sum, top, red, rib, w, slot);
     if (!live) continue;
     const float rstd = a.norm ? rsqrtf(fmaf(sum, inv_n, a.eps)) : 1.f;
     if (a.rstd && w == 0 && lane == 0) a.rstd[row] = rstd;
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 256 ? 2 : 1) k_ro
         float2 o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = mul2(v[j][i], f2(rstd));
-        store_chunk<T, VEC>(static_cast<T*>(a.y) + at, col0<VEC>(w + j * W, lane), C, o);
+        store_chunk<T, L, VEC>(static_cast<T*>(a.y) + at, col0<L, VEC>(w + j * W, lane), C, o);
       }
     }
     if (a.q) {
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 256 ? 2 : 1) k_ro
         float2 t[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = round2(v[j][i], mul);
-        store_bytes<VEC>(a.q + (size_t)row * a.P, col0<VEC>(w + j * W, lane), a.P, t, fine);
+        store_bytes<L, VEC>(a.q + (size_t)row * a.P, col0<L, VEC>(w + j * W, lane), a.P, t, fine);
       }
     }
   }
@@ -115,26 +115,29 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 256 ? 2 : 1) k_ro
 
 template <typename T, bool VEC>
 cudaError_t rows_fwd(const RowsFwd& a, cudaStream_t st) {
-  auto go = [&](auto k, int tpr) {
-    const int th = tpr < 256 ? 256 : tpr, rpb = th / tpr;
+  auto go = [&](auto k, int threads_of_row) {
+    const int th = threads_of_row < 256 ? 256 : threads_of_row, rpb = th / threads_of_row;
     const long long want = (a.R + rpb - 1) / rpb;
     const long long most = (long long)sm_count() * 16;
     return launch_k(k, dim3((unsigned)(want < most ? want : most)), dim3(th), 0, st, 1, a);
   };
-  const int blocks = (a.P + 255) / 256;  // of a padded int8 row
-  if (blocks <= 2) return go(k_rows_fwd<T, 32, 2, VEC>, 32);
-  if (blocks <= 5) return go(k_rows_fwd<T, 32, 5, VEC>, 32);
-  if (blocks <= 16) return go(k_rows_fwd<T, 128, 4, VEC>, 128);
-  return go(k_rows_fwd<T, 512, 4, VEC>, 512);
+  if (a.P <= 64) return go(k_rows_fwd<T, 8, 1, 1, VEC>, 8);
+  if (a.P <= 128) return go(k_rows_fwd<T, 16, 1, 1, VEC>, 16);
+  if (a.P <= 256) return go(k_rows_fwd<T, 32, 1, 1, VEC>, 32);
+  if (a.P <= 512) return go(k_rows_fwd<T, 32, 1, 2, VEC>, 32);
+  if (a.P <= 1280) return go(k_rows_fwd<T, 32, 1, 5, VEC>, 32);
+  if (a.P <= 4096) return go(k_rows_fwd<T, 32, 4, 4, VEC>, 128);
+  if (a.P <= 8192) return go(k_rows_fwd<T, 32, 16, 2, VEC>, 512);
+  return go(k_rows_fwd<T, 32, 16, 4, VEC>, 512);
 }
 
 // ---------------------------------------------------------------- element passes
-// A flat run over the 256-column blocks of padded int8 rows, one to a warp.
+// A flat run over the blocks of 8 * L columns of padded int8 rows.
 struct Flat {
   int C, P, bpr;         // blocks per row
   long long total;       // rows * bpr
 };
-// A warp takes kBatch neighbouring blocks at a time, all loads first.
+// L lanes take kBatch neighbouring blocks at a time, all loads first.
 constexpr int kBatch = 4;
 // Row and block of a flat position; one division for a batch.
 struct Place {
@@ -218,11 +221,11 @@ __global__ void __launch_bounds__(256) k_ckpt_pack_flat(long long total, const T
   if (b0 + kBatch <= total) {
     Chunk<T> k[kBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) k[j] = load_chunk<T, true>(xp + j * 256, 0, 8);
+    for (int j = 0; j < kBatch; ++j) k[j] = load_chunk<T, 32, true>(xp + j * 256, 0, 8);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) store(k[j], j);
   } else {
-    for (int j = 0; b0 + j < total; ++j) store(load_chunk<T, true>(xp + j * 256, 0, 8), j);
+    for (int j = 0; b0 + j < total; ++j) store(load_chunk<T, 32, true>(xp + j * 256, 0, 8), j);
   }
 }
 // The same for q8 rows of a whole number of blocks (f.bpr of them), each block
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(256) k_dequant_flat(const Flat f, const int8_t
     biased(b, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(add2(v[i], f2(-kBias)), f2(s));
-    store_chunk<T, true>(xp + j * 256, 0, 8, v);
+    store_chunk<T, 32, true>(xp + j * 256, 0, 8, v);
   };
   if (b0 + kBatch <= f.total) {
     uint2 b[kBatch];
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(256) k_unpack_flat(long long total, const int8
     biased(b, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(add2(v[i], f2(-kBias)), f2(s));
-    store_chunk<T, true>(xp + j * 256, 0, 8, v);
+    store_chunk<T, 32, true>(xp + j * 256, 0, 8, v);
   };
   if (b0 + kBatch <= total) {
     uint2 b[kBatch];
@@ -288,15 +291,18 @@ __global__ void __launch_bounds__(256) k_unpack_flat(long long total, const int8
   }
 }
 
-// The 32 columns of a group are four neighbouring lanes (VEC) or one element of
-// every lane.
-template <typename T, bool VEC>
+// The 32 columns of a group are four neighbouring lanes (VEC) or 32 / L
+// elements of each of the L lanes.
+template <typename T, int L, bool VEC>
 __global__ void __launch_bounds__(256) k_ckpt_pack(const Flat f, const T* x, int8_t* q, int8_t* e) {
   pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const long long step = (long long)gridDim.x * 8 * kBatch;
+  const int lane = threadIdx.x & (L - 1);
+  const long long step = (long long)gridDim.x * (256 / L) * kBatch;
   const int groups = f.P / kQ8Group;
-  for (long long b0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kBatch; b0 < f.total; b0 += step) {
+  // Whole warps stay in the loop together: the shuffles below take every lane.
+  for (long long w0 = ((long long)blockIdx.x * (256 / L) + (threadIdx.x >> 5) * (32 / L)) * kBatch; w0 < f.total;
+       w0 += step) {
+    const long long b0 = w0 + ((threadIdx.x & 31) / L) * kBatch;
     Chunk<T> k[kBatch];
     long long row[kBatch];
     int c0[kBatch];
@@ -305,33 +311,40 @@ __global__ void __launch_bounds__(256) k_ckpt_pack(const Flat f, const T* x, int
     for (int j = 0; j < kBatch; ++j, next_place(f, p)) {
       const bool live = b0 + j < f.total;
       row[j] = live ? p.row : 0;
-      c0[j] = col0<VEC>(p.blk, lane);
-      k[j] = load_chunk<T, VEC>(x + row[j] * f.C, c0[j], live ? f.C : 0);
+      c0[j] = col0<L, VEC>(p.blk, lane);
+      k[j] = load_chunk<T, L, VEC>(x + row[j] * f.C, c0[j], live ? f.C : 0);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      if (b0 + j >= f.total) break;
+      const bool live = b0 + j < f.total;
       if constexpr (VEC) {
         int ex;
         const uint2 b = pack_group(k[j], ex);
-        if (c0[j] < f.P) *reinterpret_cast<uint2*>(q + row[j] * f.P + c0[j]) = b;
-        if ((lane & 3) == 0 && c0[j] < f.P) e[row[j] * groups + c0[j] / kQ8Group] = (int8_t)ex;
+        if (live && c0[j] < f.P) *reinterpret_cast<uint2*>(q + row[j] * f.P + c0[j]) = b;
+        if (live && (lane & 3) == 0 && c0[j] < f.P) e[row[j] * groups + c0[j] / kQ8Group] = (int8_t)ex;
       } else {
+        constexpr int PER = 32 / L;  // elements of a lane in a group
         float2 v[4];
         to_pairs(k[j], v);
         int mine = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float& t = i & 1 ? v[i / 2].y : v[i / 2].x;
-          const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(t) & 0x7fffffffu);
-          const int ex = ckpt_exp<T>(u);
-          t = fminf(fmaxf(fmaf(t, pow2(-ex), kRound), kRound - 127.f), kRound + 127.f);
-          if (ex == kCkptNaN) t = kRound;
-          if (lane == i) mine = ex;
+        for (int g = 0; g < L / 4; ++g) {
+          uint32_t u = 0;
+#pragma unroll
+          for (int i = g * PER; i < (g + 1) * PER; ++i)
+            u = max(u, __float_as_uint(i & 1 ? v[i / 2].y : v[i / 2].x) & 0x7fffffffu);
+          const int ex = ckpt_exp<T>(lanes_max<L>(u));
+#pragma unroll
+          for (int i = g * PER; i < (g + 1) * PER; ++i) {
+            float& t = i & 1 ? v[i / 2].y : v[i / 2].x;
+            t = fminf(fmaxf(fmaf(t, pow2(-ex), kRound), kRound - 127.f), kRound + 127.f);
+            if (ex == kCkptNaN) t = kRound;
+          }
+          if (lane == g) mine = ex;
         }
-        store_bytes<VEC>(q + row[j] * f.P, c0[j], f.P, v, true);
+        store_bytes<L, VEC>(q + row[j] * f.P, c0[j], live ? f.P : 0, v, true);
         const int grp = (c0[j] - lane) / kQ8Group + lane;
-        if (lane < 8 && grp < groups) e[row[j] * groups + grp] = (int8_t)mine;
+        if (live && lane < L / 4 && grp < groups) e[row[j] * groups + grp] = (int8_t)mine;
       }
     }
   }
@@ -339,16 +352,15 @@ __global__ void __launch_bounds__(256) k_ckpt_pack(const Flat f, const T* x, int
 
 // CK: checkpoint (one exponent per group), else one scale per row.  The output
 // rows have `pitch` elements; columns C .. pitch-1 become zeros.
-template <typename T, bool CK, bool VEC>
+template <typename T, bool CK, int L, bool VEC>
 __global__ void __launch_bounds__(256) k_unpack(const Flat f, const int8_t* q, const void* s, T* x, int pitch) {
   pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const long long step = (long long)gridDim.x * 8 * kBatch;
+  const int lane = threadIdx.x & (L - 1);
+  const long long step = (long long)gridDim.x * (256 / L) * kBatch;
   const int groups = f.P / kQ8Group;
-  for (long long b0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kBatch; b0 < f.total; b0 += step) {
-    uint2 b[kBatch];
+  for (long long b0 = ((long long)blockIdx.x * (256 / L) + threadIdx.x / L) * kBatch; b0 < f.total; b0 += step) {
+    uint2 b[kBatch], ex[kBatch];
     float sc[kBatch];
-    uint2 ex[kBatch];
     long long row[kBatch];
     int c0[kBatch];
     Place p = place_of(f, b0);
@@ -356,22 +368,14 @@ __global__ void __launch_bounds__(256) k_unpack(const Flat f, const int8_t* q, c
     for (int j = 0; j < kBatch; ++j, next_place(f, p)) {
       const bool live = b0 + j < f.total;
       row[j] = live ? p.row : 0;
-      const int blk = p.blk;
-      c0[j] = col0<VEC>(blk, lane);
-      b[j] = load_bytes<VEC>(q + row[j] * f.P, c0[j], live ? f.P : 0);
+      c0[j] = col0<L, VEC>(p.blk, lane);
+      b[j] = load_bytes<L, VEC>(q + row[j] * f.P, c0[j], live ? f.P : 0);
       sc[j] = 0.f;
       ex[j] = make_uint2(0, 0);
       if (!live) continue;
-      if (!CK) {
-        sc[j] = static_cast<const float*>(s)[row[j]];
-      } else if (VEC) {
-        if (c0[j] < f.P) sc[j] = ckpt_step(static_cast<const int8_t*>(s)[row[j] * groups + c0[j] / kQ8Group]);
-      } else {
-        uint32_t w[2] = {0, 0};
-        for (int i = 0; i < 8 && blk * 8 + i < groups; ++i)
-          w[i / 4] |= (uint32_t)(uint8_t)static_cast<const int8_t*>(s)[row[j] * groups + blk * 8 + i] << (8 * (i & 3));
-        ex[j] = make_uint2(w[0], w[1]);
-      }
+      if (!CK) sc[j] = static_cast<const float*>(s)[row[j]];
+      else if (!VEC) ex[j] = load_exps<L>(static_cast<const int8_t*>(s) + row[j] * groups, p.blk, groups);
+      else if (c0[j] < f.P) sc[j] = ckpt_step(static_cast<const int8_t*>(s)[row[j] * groups + c0[j] / kQ8Group]);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -382,35 +386,50 @@ __global__ void __launch_bounds__(256) k_unpack(const Flat f, const int8_t* q, c
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float& t = i & 1 ? v[i / 2].y : v[i / 2].x;
-          t = (t - kBias) * ckpt_step((int8_t)((i < 4 ? ex[j].x : ex[j].y) >> (8 * (i & 3))));
+          t = (t - kBias) * ckpt_step(exp_of<L>(ex[j], i));
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = mul2(add2(v[i], f2(-kBias)), f2(sc[j]));
       }
-      if (pitch > f.C && c0[j] + (VEC ? 8 : 225) > f.C) {
+      if (pitch > f.C && c0[j] + (VEC ? 8 : 7 * L + 1) > f.C) {
         // Columns C .. pitch - 1: zeros whatever the padding holds (a NaN
         // scale would not leave them so).
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (col<VEC>(c0[j], i) >= f.C) (i & 1 ? v[i / 2].y : v[i / 2].x) = 0.f;
+          if (col<L, VEC>(c0[j], i) >= f.C) (i & 1 ? v[i / 2].y : v[i / 2].x) = 0.f;
       }
-      store_chunk<T, VEC>(x + row[j] * pitch, c0[j], pitch, v);
+      store_chunk<T, L, VEC>(x + row[j] * pitch, c0[j], pitch, v);
     }
   }
 }
 
-Flat flat_of(long long R, int C) {
+// Lanes for a block: as few as hold a short row.
+int lanes_of(int C) { return q8_pitch(C) <= 64 ? 8 : q8_pitch(C) <= 128 ? 16 : 32; }
+Flat flat_of(long long R, int C, int lanes) {
   Flat f;
   f.C = C;
   f.P = q8_pitch(C);
-  f.bpr = (f.P + 255) / 256;
+  f.bpr = (f.P + 8 * lanes - 1) / (8 * lanes);
   f.total = R * f.bpr;
   return f;
 }
-unsigned flat_grid(const Flat& f) {
-  const long long want = (f.total + 8 * kBatch - 1) / (8 * kBatch), most = (long long)sm_count() * 16;
-  return (unsigned)(want < most ? want : most);
+dim3 flat_grid(const Flat& f, int lanes) {
+  const long long per = (long long)(256 / lanes) * kBatch;
+  const long long want = (f.total + per - 1) / per, most = (long long)sm_count() * 16;
+  return dim3((unsigned)(want < most ? want : most));
+}
+template <typename T, int L>
+cudaError_t ckpt_pack(long long R, int C, const T* x, int8_t* q, int8_t* e, cudaStream_t st) {
+  const Flat f = flat_of(R, C, L);
+  return launch_k(rows_aligned(C, sizeof(T)) ? k_ckpt_pack<T, L, true> : k_ckpt_pack<T, L, false>, flat_grid(f, L),
+                  dim3(256), 0, st, 1, f, x, q, e);
+}
+template <typename T, bool CK, int L>
+cudaError_t unpack_rows(long long R, int C, const int8_t* q, const void* s, T* x, int pitch, cudaStream_t st) {
+  const Flat f = flat_of(R, C, L);
+  return launch_k(rows_aligned(pitch, sizeof(T)) ? k_unpack<T, CK, L, true> : k_unpack<T, CK, L, false>,
+                  flat_grid(f, L), dim3(256), 0, st, 1, f, q, s, x, pitch);
 }
 
 // ---------------------------------------------------------------- column sums
@@ -495,14 +514,18 @@ cudaError_t launch_rows_fwd(const RowsFwd& a, cudaStream_t st) {
 
 cudaError_t launch_dequant_rows(long long R, int C, int dtype, const int8_t* q, const float* scale, void* x,
                                 cudaStream_t st) {
-  const Flat f = flat_of(R, C);
-  if (C % 256 == 0 && f.total < (1ll << 35)) {
+  if (C % 256 == 0 && R * (C / 256) < (1ll << 35)) {
+    const Flat f = flat_of(R, C, 32);
     RMX_BY_DTYPE(dtype, return launch_k(k_dequant_flat<T>, dim3((unsigned)((f.total + 8 * kBatch - 1) / (8 * kBatch))),
                                         dim3(256), 0, st, 1, f, q, scale, static_cast<T*>(x)))
   }
-  const void* s = scale;
-  RMX_BY_DTYPE(dtype, return launch_k(rows_aligned(C, sizeof(T)) ? k_unpack<T, false, true> : k_unpack<T, false, false>,
-                                      dim3(flat_grid(f)), dim3(256), 0, st, 1, f, q, s, static_cast<T*>(x), C))
+  const int L = lanes_of(C);
+  RMX_BY_DTYPE(dtype, {
+    T* xt = static_cast<T*>(x);
+    return L == 8    ? unpack_rows<T, false, 8>(R, C, q, scale, xt, C, st)
+           : L == 16 ? unpack_rows<T, false, 16>(R, C, q, scale, xt, C, st)
+                     : unpack_rows<T, false, 32>(R, C, q, scale, xt, C, st);
+  })
 }
 
 // Whether a checkpoint can be taken as one run of 256-column blocks.
@@ -516,9 +539,13 @@ cudaError_t launch_ckpt_pack(long long R, int C, int dtype, const void* x, int8_
     RMX_BY_DTYPE(dtype, return launch_k(k_ckpt_pack_flat<T>, ckpt_flat_grid(R, C), dim3(256), 0, st, 1, R * C / 256,
                                         static_cast<const T*>(x), q, e))
   }
-  const Flat f = flat_of(R, C);
-  RMX_BY_DTYPE(dtype, return launch_k(rows_aligned(C, sizeof(T)) ? k_ckpt_pack<T, true> : k_ckpt_pack<T, false>,
-                                      dim3(flat_grid(f)), dim3(256), 0, st, 1, f, static_cast<const T*>(x), q, e))
+  const int L = lanes_of(C);
+  RMX_BY_DTYPE(dtype, {
+    const T* xt = static_cast<const T*>(x);
+    return L == 8    ? ckpt_pack<T, 8>(R, C, xt, q, e, st)
+           : L == 16 ? ckpt_pack<T, 16>(R, C, xt, q, e, st)
+                     : ckpt_pack<T, 32>(R, C, xt, q, e, st);
+  })
 }
 
 cudaError_t launch_ckpt_unpack(long long R, int C, int dtype, const int8_t* q, const int8_t* e, void* x, int pitch,
@@ -527,10 +554,13 @@ cudaError_t launch_ckpt_unpack(long long R, int C, int dtype, const int8_t* q, c
     RMX_BY_DTYPE(dtype, return launch_k(k_unpack_flat<T>, ckpt_flat_grid(R, C), dim3(256), 0, st, 1, R * C / 256, q, e,
                                         static_cast<T*>(x)))
   }
-  const Flat f = flat_of(R, C);
-  const void* s = e;
-  RMX_BY_DTYPE(dtype, return launch_k(rows_aligned(pitch, sizeof(T)) ? k_unpack<T, true, true> : k_unpack<T, true, false>,
-                                      dim3(flat_grid(f)), dim3(256), 0, st, 1, f, q, s, static_cast<T*>(x), pitch))
+  const int L = lanes_of(C);
+  RMX_BY_DTYPE(dtype, {
+    T* xt = static_cast<T*>(x);
+    return L == 8    ? unpack_rows<T, true, 8>(R, C, q, e, xt, pitch, st)
+           : L == 16 ? unpack_rows<T, true, 16>(R, C, q, e, xt, pitch, st)
+                     : unpack_rows<T, true, 32>(R, C, q, e, xt, pitch, st);
+  })
 }
 
 // Slices of rows: enough blocks for eight a SM, at least 16 rows each.

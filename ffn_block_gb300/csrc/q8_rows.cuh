@@ -1,11 +1,11 @@
 // Device helpers of the row passes of the 8-bit operators: which columns a
 // thread holds, int8 rounding and packing, checkpoint scales, reductions.
 //
-// A row is cut into blocks of 256 columns, one to a warp at a time, eight
-// columns to a lane.  VEC (rows start on 16-byte boundaries): a lane holds
-// eight consecutive columns, moved as 16-byte vectors.  Else (odd row
-// lengths): columns lane, lane + 32, ..., so that a warp's one-element
-// accesses are consecutive.
+// A row is cut into blocks of 8 * L columns, one to L lanes (8, 16 or 32: a
+// short row takes a part of a warp) at a time, eight columns to a lane.  VEC
+// (rows start on 16-byte boundaries): a lane holds eight consecutive columns,
+// moved as 16-byte vectors.  Else (odd row lengths): columns lane, lane + L,
+// ..., so that the lanes' one-element accesses are consecutive.
 #pragma once
 
 #include <type_traits>
@@ -24,12 +24,14 @@ inline bool rows_aligned(int C, int esize) { return ((long long)C * esize) % 16 
 template <typename T> struct alignas(16) Chunk {
   T v[8];
 };
-template <bool VEC> __device__ __forceinline__ int col0(int blk, int lane) { return blk * 256 + (VEC ? lane * 8 : lane); }
+template <int L, bool VEC> __device__ __forceinline__ int col0(int blk, int lane) {
+  return blk * (8 * L) + (VEC ? lane * 8 : lane);
+}
 // Column of element i, given that of element 0.
-template <bool VEC> __device__ __forceinline__ int col(int c0, int i) { return c0 + (VEC ? i : 32 * i); }
+template <int L, bool VEC> __device__ __forceinline__ int col(int c0, int i) { return c0 + (VEC ? i : L * i); }
 
 // Eight values of a row of C columns; columns past C read as zero.
-template <typename T, bool VEC>
+template <typename T, int L, bool VEC>
 __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int c0, int C) {
   Chunk<T> k;
   if constexpr (VEC) {
@@ -40,11 +42,11 @@ __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int c0, int C) {
     for (int i = 0; i < 8 / V; ++i) d[i] = c0 + i * V < C ? s[i] : make_uint4(0, 0, 0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) k.v[i] = col<VEC>(c0, i) < C ? row[col<VEC>(c0, i)] : from_f<T>(0.f);
+    for (int i = 0; i < 8; ++i) k.v[i] = col<L, VEC>(c0, i) < C ? row[col<L, VEC>(c0, i)] : from_f<T>(0.f);
   }
   return k;
 }
-template <typename T, bool VEC>
+template <typename T, int L, bool VEC>
 __device__ __forceinline__ void store_chunk(T* row, int c0, int C, const float2 (&f)[4]) {
   if constexpr (VEC) {
     if (sizeof(T) == 2) {
@@ -56,7 +58,7 @@ __device__ __forceinline__ void store_chunk(T* row, int c0, int C, const float2 
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (col<VEC>(c0, i) < C) row[col<VEC>(c0, i)] = from_f<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
+      if (col<L, VEC>(c0, i) < C) row[col<L, VEC>(c0, i)] = from_f<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
   }
 }
 __device__ __forceinline__ void to_pairs(const Chunk<bf16>& k, float2 (&v)[4]) {
@@ -86,7 +88,7 @@ __device__ __forceinline__ uint2 low_bytes(const float2 (&t)[4]) {
   return make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
 }
 // Eight int8 of a row whose pitch holds them; `keep` false writes zeros.
-template <bool VEC>
+template <int L, bool VEC>
 __device__ __forceinline__ void store_bytes(int8_t* row, int c0, int P, const float2 (&t)[4], bool keep) {
   const uint2 b = keep ? low_bytes(t) : make_uint2(0, 0);
   if constexpr (VEC) {
@@ -94,15 +96,15 @@ __device__ __forceinline__ void store_bytes(int8_t* row, int c0, int P, const fl
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (col<VEC>(c0, i) < P) row[col<VEC>(c0, i)] = (int8_t)((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
+      if (col<L, VEC>(c0, i) < P) row[col<L, VEC>(c0, i)] = (int8_t)((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
   }
 }
-template <bool VEC> __device__ __forceinline__ uint2 load_bytes(const int8_t* row, int c0, int P) {
+template <int L, bool VEC> __device__ __forceinline__ uint2 load_bytes(const int8_t* row, int c0, int P) {
   if constexpr (VEC) return c0 < P ? *reinterpret_cast<const uint2*>(row + c0) : make_uint2(0, 0);
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (col<VEC>(c0, i) < P) w[i / 4] |= (uint32_t)(uint8_t)row[col<VEC>(c0, i)] << (8 * (i & 3));
+    if (col<L, VEC>(c0, i) < P) w[i / 4] |= (uint32_t)(uint8_t)row[col<L, VEC>(c0, i)] << (8 * (i & 3));
   return make_uint2(w[0], w[1]);
 }
 // Eight int8 as floats 2^23 + 128 + q: byte ^ 0x80 in the low mantissa byte of
@@ -152,17 +154,43 @@ __device__ __forceinline__ float ckpt_step(int e) {
   return e == kCkptNaN ? __uint_as_float(0x7fc00000u) : pow2(min(max(e, -126), 121));
 }
 
+// Exponents of the 8 * L columns of block blk of a row, a byte each (L / 4).
+template <int L> __device__ __forceinline__ uint2 load_exps(const int8_t* e, int blk, int groups) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < L / 4; ++i)
+    if (blk * (L / 4) + i < groups) w[i / 4] |= (uint32_t)(uint8_t)e[blk * (L / 4) + i] << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+// That of element i (not VEC): columns lane + L * i, so group L * i / 32.
+template <int L> __device__ __forceinline__ int exp_of(uint2 e, int i) {
+  const int g = L * i / 32;
+  return (int8_t)((g < 4 ? e.x : e.y) >> (8 * (g & 3)));
+}
+
 // ---------------------------------------------------------------- reductions
-// Sum of s and maximum of the non-negative u over the TPR threads of a row, in
-// a fixed order.  `red` holds 4 * (TPR / 32) words per row slot; `slot`
-// alternates.
-template <int TPR>
-__device__ __forceinline__ void row_reduce(float& s, uint32_t& u, uint32_t* red, int& slot) {
-  s = warp_sum(s);
-  u = __reduce_max_sync(0xffffffffu, u);
-  if constexpr (TPR > 32) {
-    constexpr int W = TPR / 32;
-    const int w = (threadIdx.x & (TPR - 1)) >> 5, rib = threadIdx.x / TPR;
+// Over L neighbouring lanes, in a fixed order.
+template <int L> __device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int L> __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (L == 32) {
+    return __reduce_max_sync(0xffffffffu, v);
+  } else {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+// Sum of s and maximum of the non-negative u over the W x L threads of a row,
+// in a fixed order.  `red` holds 4 * W words per row slot; `slot` alternates.
+template <int W, int L>
+__device__ __forceinline__ void row_reduce(float& s, uint32_t& u, uint32_t* red, int rib, int w, int& slot) {
+  s = lanes_sum<L>(s);
+  u = lanes_max<L>(u);
+  if constexpr (W > 1) {
     uint32_t* r = red + (rib * 2 + slot) * 2 * W;
     if ((threadIdx.x & 31) == 0) {
       r[w] = __float_as_uint(s);

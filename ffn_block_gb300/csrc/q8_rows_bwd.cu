@@ -17,12 +17,13 @@
 namespace rmx {
 namespace {
 
-// Sum over the warps of a row, in a fixed order.  `red` holds two slots of a
+// Sum over the L lanes and W warps of a row, in a fixed order.  `red` holds two slots of a
 // float per warp of the row, used in turn; the row's warps meet at a barrier of
 // their own (rows of a block do not wait for one another).
+template <int L>
 __device__ __forceinline__ float row_sum(float s, float* red, int slot, int w, int W, int barrier) {
-  s = warp_sum(s);
-  if (W == 1) return s;
+  s = lanes_sum<L>(s);
+  if (L < 32 || W == 1) return s;
   float* r = red + slot * W;
   if ((threadIdx.x & 31) == 0) r[w] = s;
   asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * W) : "memory");
@@ -42,54 +43,49 @@ template <typename T, bool CK, bool VEC> struct RowIn {
   Chunk<T> dn, dh;
   Chunk<T> h;          // the stored sum
   uint2 q;             // or its checkpoint: eight int8 and their exponents
-  uint32_t e[2];
+  uint2 e;             // (VEC: the lane's own in x)
 };
 
 // A row belongs to W warps (W = blocks of 256 columns, up to 16), each with
 // NCH blocks of it; `rpb` rows at a time to a thread block.
-template <typename T, int NCH, bool CK, bool VEC>
+template <typename T, int L, int NCH, bool CK, bool VEC>
 __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, const int W, const int rpb) {
   pdl_enter();
   __shared__ float red[64];
   extern __shared__ float cols[];  // rpb > 1: [C] partials of the block
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, rib = wid / W, w = wid - rib * W;
+  const int lane = threadIdx.x & (L - 1), part = threadIdx.x / L, rib = part / W, w = part - rib * W;
   const float inv_n = 1.f / (float)a.C;
   const int groups = a.P / kQ8Group;
   float* my_red = red + rib * 2 * W;
-  auto c_of = [&](int j) { return col0<VEC>(w + j * W, lane); };
+  auto c_of = [&](int j) { return col0<L, VEC>(w + j * W, lane); };
   auto load = [&](RowIn<T, CK, VEC>& in, long long row, int j) {
-    const size_t at = (size_t)row * a.C;
-    const int C = a.C, P = a.P, c0 = c_of(j);
-    in.dn = load_chunk<T, VEC>(static_cast<const T*>(a.dn) + at, c0, C);
-    if (a.dh) in.dh = load_chunk<T, VEC>(static_cast<const T*>(a.dh) + at, c0, C);
+    const bool live = L == 32 || row < a.R;
+    const size_t at = (size_t)(live ? row : 0) * a.C;
+    const int C = live ? a.C : 0, P = live ? a.P : 0, c0 = c_of(j);
+    if (!live) row = 0;
+    in.dn = load_chunk<T, L, VEC>(static_cast<const T*>(a.dn) + at, c0, C);
+    if (a.dh) in.dh = load_chunk<T, L, VEC>(static_cast<const T*>(a.dh) + at, c0, C);
     if constexpr (CK) {
-      in.q = load_bytes<VEC>(a.q + (size_t)row * P, c0, P);
+      in.q = load_bytes<L, VEC>(a.q + (size_t)row * a.P, c0, P);
       const int8_t* e = a.e + (size_t)row * groups;
-      if constexpr (VEC) {
-        in.e[0] = c0 < P ? (uint32_t)(int)e[c0 / kQ8Group] : 0u;
-      } else {
-        const int g0 = (w + j * W) * 8;
-        in.e[0] = in.e[1] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if ((g0 + i) * kQ8Group < P) in.e[i / 4] |= (uint32_t)(uint8_t)e[g0 + i] << (8 * (i & 3));
-      }
+      if constexpr (VEC) in.e.x = c0 < P ? (uint32_t)(int)e[c0 / kQ8Group] : 0u;
+      else in.e = load_exps<L>(e, w + j * W, groups);
     } else {
-      in.h = load_chunk<T, VEC>(static_cast<const T*>(a.h) + at, c0, C);
+      in.h = load_chunk<T, L, VEC>(static_cast<const T*>(a.h) + at, c0, C);
     }
   };
   auto xhat = [&](const RowIn<T, CK, VEC>& in, float rstd, float2 (&xh)[4]) {
     if constexpr (CK) {
       biased(in.q, xh);
       if constexpr (VEC) {
-        const float s = ckpt_step((int)in.e[0]) * rstd;
+        const float s = ckpt_step((int)in.e.x) * rstd;
 #pragma unroll
         for (int i = 0; i < 4; ++i) xh[i] = mul2(add2(xh[i], f2(-kBias)), f2(s));
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float& t = i & 1 ? xh[i / 2].y : xh[i / 2].x;
-          t = (t - kBias) * (ckpt_step((int8_t)(in.e[i / 4] >> (8 * (i & 3)))) * rstd);
+          t = (t - kBias) * (ckpt_step(exp_of<L>(in.e, i)) * rstd);
         }
       }
     } else {
@@ -102,18 +98,21 @@ __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, 
   float2 acc[NCH][4];
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
-    g[j] = load_chunk<T, VEC>(static_cast<const T*>(a.gamma), c_of(j), a.C);
+    g[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.gamma), c_of(j), a.C);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = f2(0.f);
   }
   const long long step = (long long)gridDim.x * rpb;
   int slot = 0;
   // Every warp of a row sees the same rows, so their barriers match.
-  for (long long row = (long long)blockIdx.x * rpb + rib; row < a.R; row += step, slot ^= 1) {
+  // Parts of a warp stay in the loop together (their shuffles take every lane).
+  const int first_of_warp = L == 32 ? rib : (threadIdx.x >> 5) * (32 / L);
+  for (long long row = (long long)blockIdx.x * rpb + rib; row - rib + first_of_warp < a.R; row += step, slot ^= 1) {
+    const bool live = L == 32 || row < a.R;
     RowIn<T, CK, VEC> in[NCH];
 #pragma unroll
     for (int j = 0; j < NCH; ++j) load(in[j], row, j);
-    const float rstd = a.rstd[row];
+    const float rstd = live ? a.rstd[row] : 0.f;
     float2 dot2 = f2(0.f), xh[NCH][4], t[NCH][4];
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
@@ -128,7 +127,7 @@ __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, 
         dot2 = fma2(t[j][i], xh[j][i], dot2);
       }
     }
-    const float m = -row_sum(dot2.x + dot2.y, my_red, slot, w, W, 1 + rib) * inv_n;
+    const float m = -row_sum<L>(dot2.x + dot2.y, my_red, slot, w, W, 1 + rib) * inv_n;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
 #pragma unroll
@@ -139,7 +138,7 @@ __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[j][i] = add2(t[j][i], r[i]);
       }
-      store_chunk<T, VEC>(static_cast<T*>(a.dx) + (size_t)row * a.C, c_of(j), a.C, t[j]);
+      if (live) store_chunk<T, L, VEC>(static_cast<T*>(a.dx) + (size_t)row * a.C, c_of(j), a.C, t[j]);
     }
   }
   float* pg = a.pg + (size_t)blockIdx.x * a.C;
@@ -150,7 +149,7 @@ __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, 
       for (int j = 0; j < NCH; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int c = col<VEC>(c_of(j), i);
+          const int c = col<L, VEC>(c_of(j), i);
           const float v = i & 1 ? acc[j][i / 2].y : acc[j][i / 2].x;
           if (c < a.C) {
             if (rpb == 1) pg[c] = v;
@@ -164,18 +163,19 @@ __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, 
     for (int c = threadIdx.x; c < a.C; c += blockDim.x) pg[c] = cols[c];
 }
 
-// How rows are spread: W warps a row, NCH blocks of 256 columns a warp, rpb
-// rows a thread block (about ten warps).
+// How rows are spread: L lanes of W warps a row, NCH blocks of 8 * L columns
+// each, rpb rows a thread block (eight to ten warps).
 struct Spread {
-  int W, nch, rpb, threads;
+  int L, W, nch, rpb, threads;
 };
 Spread spread_of(int C) {
-  const int blocks = (q8_pitch(C) + 255) / 256;
+  const int P = q8_pitch(C), blocks = (P + 255) / 256;
   Spread s;
+  s.L = P <= 64 ? 8 : P <= 128 ? 16 : 32;
   s.nch = blocks <= 16 ? 1 : blocks <= 32 ? 2 : 4;
   s.W = (blocks + s.nch - 1) / s.nch;
-  s.rpb = s.W == 1 ? 8 : s.W < 10 ? 10 / s.W : 1;
-  s.threads = 32 * s.W * s.rpb;
+  s.rpb = s.W == 1 ? 256 / s.L : s.W < 10 ? 10 / s.W : 1;
+  s.threads = s.L * s.W * s.rpb;
   return s;
 }
 
@@ -183,7 +183,11 @@ template <typename T, bool CK, bool VEC>
 cudaError_t rows_bwd(const RowsBwd& a, cudaStream_t st) {
   const Spread s = spread_of(a.C);
   const size_t smem = s.rpb > 1 ? (size_t)a.C * sizeof(float) : 0;
-  auto k = s.nch == 1 ? k_rows_bwd<T, 1, CK, VEC> : s.nch == 2 ? k_rows_bwd<T, 2, CK, VEC> : k_rows_bwd<T, 4, CK, VEC>;
+  auto k = s.L == 8      ? k_rows_bwd<T, 8, 1, CK, VEC>
+           : s.L == 16   ? k_rows_bwd<T, 16, 1, CK, VEC>
+           : s.nch == 1  ? k_rows_bwd<T, 32, 1, CK, VEC>
+           : s.nch == 2  ? k_rows_bwd<T, 32, 2, CK, VEC>
+                         : k_rows_bwd<T, 32, 4, CK, VEC>;
   return launch_k(k, dim3((unsigned)rows_bwd_blocks(a.R, a.C)), dim3(s.threads), smem, st, 1, a, s.W, s.rpb);
 }
 
