@@ -26,9 +26,18 @@
 // of fp16 1024 + 128 + q for bytes 0 and 2, the same of w >> 8 for bytes 1 and
 // 3, and 2 * (u - 1152) is exact: five instructions for four values.  The
 // order of k within a word changes in both operands alike, which leaves the
-// sum over k what it is.  These instructions bound the large products: a step
-// of 64 k takes the tensor cores 2 * NT cycles, and the SM issues about 1000
-// instructions of conversion beside it.
+// sum over k what it is.
+//
+// Measured (GB300; us for one call among others): 1024 samples x 64 tokens
+// through 1280 -> 5120 590 us (1460 TFLOP/s, 76% of the measured cuBLAS bf16
+// rate; 640 us where the board is held at its power limit), 1000 x 40 through
+// 3600 -> 1200 240 us, one sample x 64 tokens through 1280 -> 5120 73 us
+// (5.8 TB/s, 87% of the measured copy rate).  What bounds the large products
+// is the SM's instruction issue: a step of 64 k of a 256 x 176 tile takes the
+// tensor cores 352 cycles, and about 1440 instructions (560 of them the
+// conversion itself, 260 the epilogue) at an IPC of 2.6.  With an epilogue of
+// 4 warps or tiles of 208 tokens the epilogue bounds it instead; outputs
+// through shared memory and TMA cost more instructions than they save.
 
 #include <cuda.h>
 
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (row - lane < p.ntc)
         convert<W, false>(set, row, live, halves, sRaw + 128 * kRawK + (live ? (uint32_t)row * 128u : 0u),
                           p.raw_bytes, p.raw_stages, raw_full(0), full0, conv_empty(0), sConv + (uint32_t)row * 128u,
-                               p.conv_bytes, wc);
+                          p.conv_bytes, wc);
     }
     __syncwarp();
   } else {
@@ -528,8 +537,9 @@ cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t 
   p.G = d.G;
   p.K = d.K;
   p.N = d.N;
-  // A CTA alone up to 96 tokens, a pair above: the pair shares the tokens'
-  // conversion, which a CTA alone would do for all of them.
+  // A CTA alone up to 96 tokens (what three warps convert), a pair above: the
+  // pair shares the tokens' conversion, which a CTA alone would do for all of
+  // them.
   const bool pair = d.M > kMaxAlone && d.N > 128;
   const int most = pair ? kMaxNT : kMaxAlone;
   p.tiles_m = (d.M + most - 1) / most;

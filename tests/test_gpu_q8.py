@@ -14,6 +14,9 @@ EPS = 1e-5
 
 ROW_SHAPES = [(1, 1), (1, 1280), (3, 8), (5, 31), (4, 33), (7, 100), (300, 64), (9, 513), (65, 1280), (11, 1281),
               (6, 2048), (5, 3001), (3, 4096), (2, 8192), (3, 8200), (2, 16384)]
+# both sides of every change of threads a row, odd and even
+ROW_SHAPES += [(37, 40), (37, 41), (33, 65), (33, 72), (35, 127), (35, 128), (19, 129), (19, 256), (17, 257), (17, 264),
+               (9, 512), (9, 520), (5, 1272), (5, 1288), (3, 4097), (3, 4104), (3, 8193)]
 
 
 def rms_data(R, C, dt, seed=0):
@@ -206,7 +209,9 @@ def test_rms_norm_backward_in_place_and_empty():
 # ------------------------------------------------------------------ checkpoints
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("R,C", [(1, 1), (1, 8), (3, 31), (4, 33), (17, 96), (9, 513), (33, 1280), (2, 20001)])
+@pytest.mark.parametrize("R,C", [(1, 1), (1, 8), (3, 31), (4, 33), (17, 96), (9, 513), (33, 1280), (2, 20001), (41, 40),
+                                 (41, 41), (33, 100), (33, 127), (19, 130), (7, 1000), (8, 32), (3, 256), (65, 64),
+                                 (6, 4000), (300, 1)])
 def test_checkpoint_is_the_definition(R, C, dt):
     rng = np.random.default_rng(R + C)
     x = rnd(rng.standard_normal((R, C)) * np.exp(2 * rng.standard_normal((R, C))), dt)
@@ -288,6 +293,9 @@ def check_linear(out, a, sa, w, sw, b, r, K, dt):
 LIN_SHAPES = [(1, 1, 1, 1), (1, 3, 64, 32), (2, 1, 31, 17), (5, 2, 33, 65), (8, 4, 250, 123), (17, 3, 1280, 640),
               (33, 2, 96, 300), (64, 5, 200, 129), (100, 1, 513, 257), (128, 2, 128, 256), (129, 2, 64, 520),
               (200, 3, 320, 384), (256, 1, 1000, 512), (300, 2, 72, 40), (1, 2, 4100, 1000), (700, 1, 416, 771)]
+# both sides of a CTA alone and a pair, of one token tile and two; more tiles than SMs; few k
+LIN_SHAPES += [(96, 1, 130, 129), (97, 1, 70, 128), (97, 2, 70, 129), (192, 1, 128, 256), (193, 1, 129, 257),
+               (16, 3, 127, 33), (32, 1, 257, 140), (385, 1, 64, 600), (3, 200, 40, 140), (130, 90, 33, 300)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
