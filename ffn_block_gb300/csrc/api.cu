@@ -383,6 +383,7 @@ bool tc_engine(const GemmDesc& d) { return (d.dtype != RMX_F32 || d.tf32) && gem
 
 rmx_status run_gemm(const char* name, const GemmDesc& d, cudaStream_t st) {
   const bool tc = tc_engine(d);
+  if (d.colsum && !tc) return RMX_ERR_UNSUPPORTED;  // the CUDA-core form has no column sums
   Launch l(tc ? name : ffma_label(name), st);
   const cudaError_t e = tc ? gemm_tc_launch(d, device_error_word(), st) : gemm_simt_launch(d, st);
   return l.done(e);

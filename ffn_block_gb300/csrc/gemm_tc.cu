@@ -68,6 +68,7 @@ constexpr int NUM_ACC = 2;
 constexpr int TMEM_COLS = NUM_ACC * BN;        // 512
 constexpr int EPI_WARPS = 8;                  // two per TMEM lane quarter
 constexpr int THREADS = 64 + 32 * EPI_WARPS;   // producer, MMA, epilogue
+constexpr int SUM_WARPS = 4;                   // column sums of B (weight gradients that ask for them)
 
 // Shared-memory ring.  Single CTA: the whole 256-row B tile per stage, four
 // stages.  CTA pair: each CTA holds its 128 rows of A and its half of B, so a
@@ -76,7 +77,7 @@ template <bool PAIR> struct Ring {
   static constexpr int STAGES = PAIR ? 6 : 4;
   static constexpr int B_STAGE = PAIR ? B_BYTES / 2 : B_BYTES;
   static constexpr int STAGE_BYTES = A_BYTES + B_STAGE;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * NUM_ACC + 1;
+  static constexpr int NUM_BARS = 3 * STAGES + 2 * NUM_ACC + 1;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * 4096 + 256;
   static_assert(NUM_BARS * 8 + 8 <= 256, "barrier area");
 };
@@ -100,6 +101,10 @@ struct Params {
   // [K group of 8][64-wide MN chunk][8 K rows][64 MN] (swizzle atoms of the
   // chunks of one K group adjacent), one TMA copy per operand and stage.
   int mn_il;
+  // Column sums of B over K (weight gradients): [G][colsum_n] in the storage
+  // type, colsum_n <= N.
+  void* colsum;
+  int colsum_n;
 };
 
 // Instruction descriptor, kind::f16 / kind::tf32: D fp32 (bits 4-5 = 1),
@@ -248,8 +253,13 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-template <typename T, int KIND, int EPI, bool PAIR>
-__global__ void __launch_bounds__(THREADS, 1)
+// SUMS: four more warps add up the columns of B (dy: the bias gradient) from the
+// stages of the tiles of the first row of tiles, which between them see every
+// element of B once, before those stages are loaded again.  The MMAs of a stage
+// then release it to these warps (`used`), and these to the producer.  It costs
+// the product nothing measurable, and saves a pass over B.
+template <typename T, int KIND, int EPI, bool PAIR, bool SUMS>
+__global__ void __launch_bounds__(THREADS + (SUMS ? 32 * SUM_WARPS : 0), 1)
     k_gemm_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmC, const Params p) {
   // Setup (barriers, TMEM, tensor-map prefetch) overlaps the previous
@@ -274,6 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto tfull_bar = [&](int a) { return smem_u32(bars + 2 * STAGES + a); };
   auto tempty_bar = [&](int a) { return smem_u32(bars + 2 * STAGES + NUM_ACC + a); };
   const uint32_t drain_bar = smem_u32(bars + 2 * STAGES + 2 * NUM_ACC);
+  auto used_bar = [&](int s) { return smem_u32(bars + 2 * STAGES + 2 * NUM_ACC + 1 + s); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)cluster_rank() : 0;
@@ -289,7 +300,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);    // the (even) CTA's expect_tx arrival
-      mbar_init(empty_bar(s), 1);   // one MMA commit per use
+      // One MMA commit per use, or the summing warps after it.
+      mbar_init(empty_bar(s), SUMS ? SUM_WARPS : 1);
+      if (SUMS) mbar_init(used_bar(s), 1);
     }
     for (int a = 0; a < NUM_ACC; ++a) {
       mbar_init(tfull_bar(a), 1);
@@ -463,8 +476,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                          : sw128_desc(b_base + k * 32, 16, 1024);
             umma<T, PAIR>(d_tmem, adesc, bdesc, idesc, (kb | k) != 0 ? 1u : 0u);
           }
-          if (PAIR) umma_commit_pair(empty_bar(s));
-          else umma_commit<false>(empty_bar(s));
+          const uint32_t done = SUMS ? used_bar(s) : empty_bar(s);
+          if (PAIR) umma_commit_pair(done);
+          else umma_commit<false>(done);
         }
         if (!ok) break;
         if (PAIR) umma_commit_pair(tfull_bar(acc));
@@ -478,6 +492,73 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     __syncwarp();
+  } else if (SUMS && warp >= 2 + EPI_WARPS) {
+    // ------------------------------------------------------------ column sums
+    // A lane adds one 16-byte piece (eight columns) of every eighth k row:
+    // piece lane % 4 of the warp's, k rows lane / 4, + 8, ....
+    constexpr int B_W = PAIR ? BN / 2 : BN, SETS = B_W / 8 / (4 * SUM_WARPS);
+    const int sw = warp - 2 - EPI_WARPS, kr = lane >> 2;
+    int s = 0;
+    uint32_t ph = 0;
+    for (int tile = first; tile < count; tile += stride) {
+      int g, m0, n0;
+      coords(tile, rank, g, m0, n0);
+      const bool mine = m0 - rank * BM == 0;
+      const int nb0 = n0 + (PAIR ? rank * B_W : 0);
+      float2 sum[SETS][4];
+#pragma unroll
+      for (int i = 0; i < SETS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[i][e] = f2(0.f);
+      int ok = 1;
+      for (int kb = 0; ok && kb < p.num_kb; ++kb) {
+        if (lane == 0) ok = mbar_wait_bounded(used_bar(s), ph, p.wait_limit_ns, p.err, ERRBIT_WAIT_ROWS, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (mine) {
+          const uint8_t* b = smem + STAGES * A_BYTES + s * R::B_STAGE;
+#pragma unroll
+          for (int i = 0; i < SETS; ++i) {
+            const int piece = i * 4 * SUM_WARPS + sw * 4 + (lane & 3), ch = piece >> 3;
+            const int at = kr * 128 + (((piece & 7) ^ kr) << 4);
+            const int step = p.mn_il ? (B_W / 64) * 1024 : 1024;  // from one k row to the eighth after it
+            const uint8_t* q = b + ch * (p.mn_il ? 1024 : MN_CHUNK_BYTES) + at;
+#pragma unroll
+            for (int k = 0; k < BK / 8; ++k) {
+              float2 v[4];
+              ld8(reinterpret_cast<const T*>(q + k * step), v);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum[i][e] = add2(sum[i][e], v[e]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty_bar(s));
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (!mine) continue;
+#pragma unroll
+      for (int i = 0; i < SETS; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            sum[i][e].x += __shfl_xor_sync(0xffffffffu, sum[i][e].x, o);
+            sum[i][e].y += __shfl_xor_sync(0xffffffffu, sum[i][e].y, o);
+          }
+        const int n = nb0 + (i * 4 * SUM_WARPS + sw * 4 + (lane & 3)) * 8;
+        if (kr == 0) {
+          T* out = reinterpret_cast<T*>(p.colsum) + (size_t)g * p.colsum_n;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < p.colsum_n) out[n + e] = from_f<T>(e & 1 ? sum[i][e / 2].y : sum[i][e / 2].x);
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                 // TMEM lane quarter this warp may access
@@ -654,19 +735,20 @@ bool make_map_mn5(CUtensorMap* m, const void* base, int dtype, uint64_t mn, uint
   return r == CUDA_SUCCESS;
 }
 
-template <typename T, int KIND, int EPI, bool PAIR>
+template <typename T, int KIND, int EPI, bool PAIR, bool SUMS = false>
 cudaError_t launch_tc(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const Params& p,
                       cudaStream_t st) {
-  auto k = k_gemm_tc<T, KIND, EPI, PAIR>;
+  auto k = k_gemm_tc<T, KIND, EPI, PAIR, SUMS>;
+  constexpr int THREADS_K = THREADS + (SUMS ? 32 * SUM_WARPS : 0);
   constexpr int SMEM_BYTES = Ring<PAIR>::SMEM_BYTES;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   if (!PAIR) {
     const int grid = p.num_tiles < sm_count() ? p.num_tiles : sm_count();
-    return launch_k(k, dim3(grid), dim3(THREADS), SMEM_BYTES, st, 1, a, b, c, p);
+    return launch_k(k, dim3(grid), dim3(THREADS_K), SMEM_BYTES, st, 1, a, b, c, p);
   }
   const int clusters = p.num_pair_tiles < sm_count() / 2 ? p.num_pair_tiles : sm_count() / 2;
-  return launch_k(k, dim3(2 * (clusters > 0 ? clusters : 1)), dim3(THREADS), SMEM_BYTES, st, 2, a, b, c, p);
+  return launch_k(k, dim3(2 * (clusters > 0 ? clusters : 1)), dim3(THREADS_K), SMEM_BYTES, st, 2, a, b, c, p);
 }
 
 // fp32 operands (TF32 tensor cores): both operands K-major (the dgrad
@@ -693,7 +775,9 @@ cudaError_t dispatch_tc(const GemmDesc& d, const CUtensorMap& a, const CUtensorM
     case GEMM_FWD * 8 + EPI_BIAS_ZSTATS: return launch_tc<T, GEMM_FWD, EPI_BIAS_ZSTATS, PAIR>(a, b, c, p, st);
     case GEMM_DGRAD * 8 + EPI_STORE: return launch_tc<T, GEMM_DGRAD, EPI_STORE, PAIR>(a, b, c, p, st);
     case GEMM_DGRAD * 8 + EPI_RESID: return launch_tc<T, GEMM_DGRAD, EPI_RESID, PAIR>(a, b, c, p, st);
-    case GEMM_WGRAD * 8 + EPI_STORE: return launch_tc<T, GEMM_WGRAD, EPI_STORE, PAIR>(a, b, c, p, st);
+    case GEMM_WGRAD * 8 + EPI_STORE:
+      if (d.colsum) return launch_tc<T, GEMM_WGRAD, EPI_STORE, PAIR, true>(a, b, c, p, st);
+      return launch_tc<T, GEMM_WGRAD, EPI_STORE, PAIR>(a, b, c, p, st);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -812,6 +896,8 @@ cudaError_t gemm_tc_launch(const GemmDesc& d, unsigned int* err, cudaStream_t st
   p.res_gs = p.out_gs;
   p.err = err;
   p.wait_limit_ns = kWaitLimitNs;
+  p.colsum = d.colsum;
+  p.colsum_n = d.colsum_n;
   p.zstats = d.zstats;
   p.split = d.split;
   p.zgroups = (d.N + kZStatsTile - 1) / kZStatsTile;

@@ -164,6 +164,10 @@ struct GemmDesc {
   // Optional element strides of A's (g, m) and C's (g, m) indices in the
   // FWD / DGRAD forms (0: the [M, G, K] / [M, G, N] defaults); TF32 only.
   long long a_gs = 0, a_rs = 0, c_gs = 0, c_rs = 0;
+  // WGRAD on the tensor cores only (16-bit types): also the sums of Bm's first
+  // colsum_n columns over K, [G, colsum_n] in the storage type.
+  void* colsum = nullptr;
+  int colsum_n = 0;
 };
 
 bool gemm_tc_supported(const GemmDesc& d);

@@ -32,7 +32,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspace of the weight gradient: the unpacked activation [M, G, Kp], and
 // for rows that are not a whole number of 16-byte vectors (16-bit types)
-// padded copies of dy and dw; then the bias gradient's column partials.
+// padded copies of dy and dw; float32: the bias gradient's column partials.
 struct WgradWs {
   int Kp, Np;
   bool padded;
@@ -54,7 +54,8 @@ WgradWs wgrad_ws(const rmx_layer& l) {
     o = up256(o + (size_t)l.G * w.Kp * w.Np * e);
   }
   w.part = o;
-  w.total = up256(o + (size_t)colpart_slices(l.M, (long long)l.G * l.N, (int)e) * l.G * l.N * sizeof(float));
+  if (l.dtype == RMX_F32) o += (size_t)colpart_slices(l.M, (long long)l.G * l.N, (int)e) * l.G * l.N * sizeof(float);
+  w.total = up256(o);
   return w;
 }
 
@@ -222,14 +223,21 @@ rmx_status rmx_ckpt8_wgrad(const rmx_layer* layer, const int8_t* q, const int8_t
     Launch la("pad_in", st);
     RMX_TRY(la.done(launch_pad_copy(dy, at(ws, w.dy), l.dtype, m, true, st)));
   }
-  const GemmDesc d{GEMM_WGRAD, EPI_STORE, l.dtype, w.Kp, w.Np, l.M, l.G, at(ws, w.x), dyp, dwp, nullptr, nullptr};
+  GemmDesc d{GEMM_WGRAD, EPI_STORE, l.dtype, w.Kp, w.Np, l.M, l.G, at(ws, w.x), dyp, dwp, nullptr, nullptr};
+  // The tensor-core product adds up dy's columns as they pass; the strict
+  // float32 one leaves them to a pass of their own.
+  const bool fused = l.dtype != RMX_F32;
+  if (fused) {
+    d.colsum = db;
+    d.colsum_n = l.N;
+  }
   RMX_TRY(run_gemm("ckpt8_wgrad", d, st));
   if (w.padded) {
     const PadMap m{l.G, l.K, w.Kp, l.N, w.Np, 1};
     Launch la("pad_out", st);
     RMX_TRY(la.done(launch_pad_copy(dwp, dw, l.dtype, m, false, st)));
   }
-  if (db) {
+  if (db && !fused) {
     const long long J = (long long)l.G * l.N;
     const int slices = colpart_slices(l.M, J, (int)e);
     float* part = reinterpret_cast<float*>(at(ws, w.part));
