@@ -255,9 +255,8 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 
 // SUMS: four more warps add up the columns of B (dy: the bias gradient) from the
 // stages of the tiles of the first row of tiles, which between them see every
-// element of B once, before those stages are loaded again.  The MMAs of a stage
-// then release it to these warps (`used`), and these to the producer.  It costs
-// the product nothing measurable, and saves a pass over B.
+// element of B once, before those stages are loaded again.  The MMAs of such a
+// stage release it to these warps (`used`), and these to the producer.
 template <typename T, int KIND, int EPI, bool PAIR, bool SUMS>
 __global__ void __launch_bounds__(THREADS + (SUMS ? 32 * SUM_WARPS : 0), 1)
     k_gemm_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -300,8 +299,7 @@ __global__ void __launch_bounds__(THREADS + (SUMS ? 32 * SUM_WARPS : 0), 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);    // the (even) CTA's expect_tx arrival
-      // One MMA commit per use, or the summing warps after it.
-      mbar_init(empty_bar(s), SUMS ? SUM_WARPS : 1);
+      mbar_init(empty_bar(s), 1);   // one MMA commit per use (or the summing warps after it)
       if (SUMS) mbar_init(used_bar(s), 1);
     }
     for (int a = 0; a < NUM_ACC; ++a) {
@@ -450,6 +448,12 @@ __global__ void __launch_bounds__(THREADS + (SUMS ? 32 * SUM_WARPS : 0), 1)
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+        bool summed = false;
+        if (SUMS) {
+          int g, m0, n0;
+          coords(tile, 0, g, m0, n0);
+          summed = m0 == 0;
+        }
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(THREADS + (SUMS ? 32 * SUM_WARPS : 0), 1)
                          : sw128_desc(b_base + k * 32, 16, 1024);
             umma<T, PAIR>(d_tmem, adesc, bdesc, idesc, (kb | k) != 0 ? 1u : 0u);
           }
-          const uint32_t done = SUMS ? used_bar(s) : empty_bar(s);
+          const uint32_t done = SUMS && summed ? used_bar(s) : empty_bar(s);
           if (PAIR) umma_commit_pair(done);
           else umma_commit<false>(done);
         }
@@ -498,24 +502,26 @@ __global__ void __launch_bounds__(THREADS + (SUMS ? 32 * SUM_WARPS : 0), 1)
     // piece lane % 4 of the warp's, k rows lane / 4, + 8, ....
     constexpr int B_W = PAIR ? BN / 2 : BN, SETS = B_W / 8 / (4 * SUM_WARPS);
     const int sw = warp - 2 - EPI_WARPS, kr = lane >> 2;
-    int s = 0;
-    uint32_t ph = 0;
-    for (int tile = first; tile < count; tile += stride) {
+    uint32_t phases = 0;  // bit s: parity of the next `used` wait of stage s
+    long long it = 0;     // k-blocks before this tile
+    for (int tile = first; tile < count; tile += stride, it += p.num_kb) {
       int g, m0, n0;
       coords(tile, rank, g, m0, n0);
-      const bool mine = m0 - rank * BM == 0;
+      if (m0 - rank * BM != 0) continue;
       const int nb0 = n0 + (PAIR ? rank * B_W : 0);
       float2 sum[SETS][4];
 #pragma unroll
       for (int i = 0; i < SETS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[i][e] = f2(0.f);
-      int ok = 1;
-      for (int kb = 0; ok && kb < p.num_kb; ++kb) {
-        if (lane == 0) ok = mbar_wait_bounded(used_bar(s), ph, p.wait_limit_ns, p.err, ERRBIT_WAIT_ROWS, abort_flag);
+      uint32_t ok = 1;
+      int s = (int)(it % STAGES);
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (lane == 0)
+          ok = mbar_wait_bounded(used_bar(s), (phases >> s) & 1u, p.wait_limit_ns, p.err, ERRBIT_WAIT_ROWS, abort_flag);
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if (mine) {
+        phases ^= 1u << s;
+        if (ok) {
           const uint8_t* b = smem + STAGES * A_BYTES + s * R::B_STAGE;
 #pragma unroll
           for (int i = 0; i < SETS; ++i) {
@@ -532,15 +538,20 @@ __global__ void __launch_bounds__(THREADS + (SUMS ? 32 * SUM_WARPS : 0), 1)
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty_bar(s));
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1u;
-        }
+        // The four warps meet, and go on or give up together.
+        asm volatile(
+            "{\n\t.reg .pred a, b;\n\t"
+            "setp.ne.u32 a, %0, 0;\n\t"
+            "barrier.cta.red.and.aligned.pred b, 1, %1, a;\n\t"
+            "selp.u32 %0, 1, 0, b;\n\t}"
+            : "+r"(ok)
+            : "n"(32 * SUM_WARPS)
+            : "memory");
+        if (!ok) break;
+        if (sw == 0 && lane == 0) mbar_arrive(empty_bar(s));
+        s = s + 1 == STAGES ? 0 : s + 1;
       }
       if (!ok) break;
-      if (!mine) continue;
 #pragma unroll
       for (int i = 0; i < SETS; ++i) {
 #pragma unroll
