@@ -59,13 +59,12 @@ constexpr int kRowsBwdMaxBlocks = 512;
 int rows_bwd_blocks(long long R, int C);
 cudaError_t launch_rows_bwd(const RowsBwd& a, cudaStream_t st);
 
-// Column sums of a [R][J] storage-type matrix over colpart_slices slices of
-// its rows: one slice writes out [J] itself, more write part [slices][J] for
-// launch_colsums.
+// Column sums of a float32 [R][J] matrix over colpart_slices slices of its
+// rows (the tensor-core products of the 16-bit types add up theirs): one slice
+// writes out [J] itself, more write part [slices][J] for launch_colsums.
 constexpr int kColpartMax = 64;
-int colpart_slices(long long R, long long J, int esize);
-cudaError_t launch_colpart(long long R, long long J, int dtype, const void* x, float* part, void* out,
-                           cudaStream_t st);
+int colpart_slices(long long R, long long J);
+cudaError_t launch_colpart(long long R, long long J, const float* x, float* part, float* out, cudaStream_t st);
 
 // Weights [G][K][N] (storage type) -> int8 [G][N][P] (K-major, zero padded)
 // with one scale per channel.

@@ -54,7 +54,7 @@ WgradWs wgrad_ws(const rmx_layer& l) {
     o = up256(o + (size_t)l.G * w.Kp * w.Np * e);
   }
   w.part = o;
-  if (l.dtype == RMX_F32) o += (size_t)colpart_slices(l.M, (long long)l.G * l.N, (int)e) * l.G * l.N * sizeof(float);
+  if (l.dtype == RMX_F32) o += (size_t)colpart_slices(l.M, (long long)l.G * l.N) * l.G * l.N * sizeof(float);
   w.total = up256(o);
   return w;
 }
@@ -239,11 +239,11 @@ rmx_status rmx_ckpt8_wgrad(const rmx_layer* layer, const int8_t* q, const int8_t
   }
   if (db && !fused) {
     const long long J = (long long)l.G * l.N;
-    const int slices = colpart_slices(l.M, J, (int)e);
+    const int slices = colpart_slices(l.M, J);
     float* part = reinterpret_cast<float*>(at(ws, w.part));
     {
       Launch la("ckpt8_dbias", st);
-      RMX_TRY(la.done(launch_colpart(l.M, J, l.dtype, dy, part, db, st)));
+      RMX_TRY(la.done(launch_colpart(l.M, J, static_cast<const float*>(dy), part, static_cast<float*>(db), st)));
     }
     if (slices > 1) {
       const ColsumJob job{part, db, slices, (int)J};

@@ -34,8 +34,11 @@ __device__ __forceinline__ float row_sum(float s, float* red, int slot, int w, i
 
 // Registers of a thread with one block of a row.  Many warps with one row each
 // hide the loads better than few with rows loaded ahead: 65536 rows of 1280
-// 16-bit columns take 125 us at 64 registers (30 warps a SM), 198 us with two
-// rows ahead at 96 (20 warps).
+// 16-bit columns from a checkpoint take 120 us at 64 registers (30 warps a SM;
+// 4.9 TB/s, 74% of the measured copy rate), 198 us with two rows ahead at 96 (20
+// warps); at 48, 56 or 72 registers they are slower too.  What is left is latency:
+// a warp issues about 217 instructions for a block of 256 columns and waits for
+// its loads and the row's barrier in turn, at half of the issue rate.
 constexpr int kRegs = 64;
 
 // What a row brings, as loaded.
@@ -164,7 +167,10 @@ __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, 
 }
 
 // How rows are spread: L lanes of W warps a row, NCH blocks of 8 * L columns
-// each, rpb rows a thread block (eight to ten warps).
+// each, rpb rows a thread block (eight to ten warps).  Short rows take part of a
+// warp: 1,000,000 rows of 40 columns 296 us with a warp a row, 114 with 8 lanes.
+// One block a warp where 16 warps hold the row: 65536 x 1280 in 211 us with a
+// warp a row, 124 with five.
 struct Spread {
   int L, W, nch, rpb, threads;
 };
