@@ -141,12 +141,12 @@ def tensor_peak(peaks: dict, clocks: dict) -> tuple[float, float, str]:
     return burst, sustained, "burst" if at_max else "sustained"
 
 
-# Source file of each kernel (besides the headers every kernel includes).
+# Source file of each kernel (besides the shared headers).
 KERNEL_SOURCES = {
     "gemm": "gemm_tc.cu", "gate_bwd": "gate_bwd.cu", "ln01_fwd": "ln01_fwd.cu", "ln0_bwd_gather": "ln0_bwd.cu",
     "ln1_bwd": "ln_bwd.cu", "ln2_bwd": "ln_bwd.cu", "gate_fwd": "rows.cu", "ln2_fwd": "rows.cu", "colsums": "rows.cu",
 }
-SHARED_SOURCES = ("common.cuh", "launch.cuh", "kernels.h")
+SHARED_SOURCES = ("common.cuh", "launch.cuh", "kernels.h", "tcgen05.cuh")
 
 
 def kernel_source_hash(kernel: str | None = None) -> str:
