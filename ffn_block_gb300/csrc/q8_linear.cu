@@ -19,6 +19,8 @@
 //                weights (one channel a thread, int8 -> TMEM) and three for
 //                the tokens (one token a thread, int8 -> smem)
 //   warps 23-30  epilogue: a channel a thread, 16 tokens at a time
+// Few tiles with many steps of k: a cluster of two or four CTAs shares a tile's
+// steps and adds the sums up through distributed shared memory (split_of).
 // TMEM: two accumulators of NT <= 192 columns (so that the epilogue of one
 // tile overlaps the next), then the weights' stages of 32 columns.
 //
@@ -57,6 +59,7 @@ constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kRawK = 128, kConvK = 64;
 constexpr int kMaxRaw = 8, kConv = 2 * kSets;
 constexpr int kMaxNT = 192, kMaxAlone = 32 * kTWarps;
+constexpr int kMaxSplit = 4;
 constexpr int kTmemCols = 512, kAcols = kConvK / 2;
 constexpr int kScaleBytes = kEpiWarps * 1024;  // each epilogue warp's copy of a tile's token scales
 constexpr int kBarBytes = 512;
@@ -68,6 +71,7 @@ struct Params {
   int nt, ntc;            // tokens of a tile, and the share of them a CTA converts
   int raw_bytes, conv_bytes, raw_stages;
   int num_raw;            // 128-column steps of K
+  int split;              // CTAs that share a tile's steps (SPLIT)
   int tiles_m, tiles_n, num_tiles;
   uint32_t idesc;
   const float *sa, *sw;
@@ -104,6 +108,16 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
@@ -243,7 +257,10 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
   }
 }
 
-template <typename T, bool PAIR, int W>
+// SPLIT: the CTAs of a cluster each take a share of one tile's steps of K and
+// leave their sums in shared memory; then each adds up every p.split-th token's,
+// in the order of the shares, and stores them.  A cluster has one tile.
+template <typename T, bool PAIR, int W, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_q8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const Params p) {
   pdl_trigger();
@@ -266,8 +283,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)cluster_rank() : 0;
-  const int first = PAIR ? (int)cluster_id_x() : (int)blockIdx.x;
-  const int stride = PAIR ? (int)num_clusters_x() : (int)gridDim.x;
+  const int first = PAIR || SPLIT ? (int)cluster_id_x() : (int)blockIdx.x;
+  const int stride = PAIR || SPLIT ? (int)num_clusters_x() : (int)gridDim.x;
+  const int share = SPLIT ? (int)cluster_rank() : 0;
+  const int raw0 = SPLIT ? p.num_raw * share / p.split : 0;
+  const int num_raw = SPLIT ? p.num_raw * (share + 1) / p.split - raw0 : p.num_raw;
   constexpr int CTAS = PAIR ? 2 : 1;
   const int twarps = (p.ntc + 31) / 32;  // of each set, the warps that have tokens
   // Tile -> group, this CTA's first channel, the tile's first token.  Tiles
@@ -280,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     m0 = tm * p.nt;
   };
   const WaitCtx wc{p.wait_ns, p.err, abort_flag};
+  float sum_sw = 0.f, sum_bias = 0.f;  // SPLIT: this lane's channel's, for the last pass
   // Tiles of this CTA (or pair).
   const int my_tiles = first < p.num_tiles ? (p.num_tiles - first + stride - 1) / stride : 0;
 
@@ -320,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int tile = first; ok && tile < p.num_tiles; tile += stride) {
         int g, n0, m0;
         coords(tile, g, n0, m0);
-        for (int rk = 0; rk < p.num_raw; ++rk) {
+        for (int rk = raw0; rk < raw0 + num_raw; ++rk) {
           if (!wait_one(raw_empty(s), ph ^ 1u, ERRBIT_WAIT_PRODUCER, wc)) {
             ok = false;
             break;
@@ -367,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + (uint32_t)(acc * p.nt);
         uint32_t accumulate = 0;
 #pragma unroll 1
-        for (int rk = 0; ok && rk < p.num_raw; ++rk) {
+        for (int rk = 0; ok && rk < num_raw; ++rk) {
           // The two halves of a raw stage.
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -406,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ converters
     const int cw = warp - kFirstConv, set = cw / kSetWarps, role = cw - set * kSetWarps;
     const uint32_t full0 = PAIR ? mapa_shared(conv_full(0), 0) : conv_full(0);
-    const int halves = 2 * my_tiles * p.num_raw;  // the launch keeps this below 2^31
+    const int halves = 2 * my_tiles * num_raw;  // the launch keeps this below 2^31
     if (role < kWWarps) {
       // The channel is the TMEM lane, and a warp reaches the quarter warp % 4.
       const int row = (warp & 3) * 32 + lane;
@@ -449,6 +470,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
+      if constexpr (SPLIT) {
+        // Sums [token][128 channels], where the raw stages were: every copy has
+        // landed and been converted once the MMAs are done.
+#pragma unroll 1
+        for (int c0 = 16 * odd; c0 < live_cols; c0 += 32) {
+          float v[16];
+          tmem_ld_32x16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) st_shared_f32(sRaw + (uint32_t)((c0 + i) * 512 + (q * 32 + lane) * 4), v[i]);
+        }
+        sum_sw = sw;
+        sum_bias = bias;
+        continue;
+      }
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * p.nt);
       const float2 sw2 = f2(sw), bias2 = f2(bias);
       const size_t step = (size_t)p.G * p.N;
@@ -494,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // No commit may still be on its way to this CTA's barriers at the end:
     // wait for the last use of every stage.
     if (ok && warp == kFirstEpi) {
-      const long long its = 2ll * lt * p.num_raw;
+      const long long its = 2ll * lt * num_raw;
       for (long long j = its > kConv ? its - kConv : 0; ok && j < its; ++j)
         ok = wait_warp(conv_empty((int)(j % kConv)), (uint32_t)(j / kConv) & 1u, ERRBIT_WAIT_DRAIN, wc);
     }
@@ -504,29 +539,97 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // Neither CTA of a pair leaves while the other may still read its shared
   // memory or signal its barriers; TMEM is freed by both together.
-  if (PAIR) cluster_barrier();
+  if (PAIR || SPLIT) cluster_barrier();
+  if constexpr (SPLIT) {
+    if (warp >= kFirstEpi) {
+      int g, n0, m0;
+      coords(first, g, n0, m0);
+      const int ch = (warp & 3) * 32 + lane, odd = (warp - kFirstEpi) >> 2, n = n0 + ch;
+      const int live_cols = min(p.nt, p.M - m0);
+      const uint32_t scales = sScale + (uint32_t)(warp - kFirstEpi) * 1024u;
+      uint32_t sums[kMaxSplit];  // this channel's of each share
+#pragma unroll
+      for (int k = 0; k < kMaxSplit; ++k) sums[k] = mapa_shared(sRaw + 4u * (uint32_t)ch, k < p.split ? (uint32_t)k : 0u);
+      if (n < p.N) {
+        // Four tokens at a time: all their shares' loads are in flight.
+#pragma unroll 1
+        for (int c0 = share + p.split * odd; c0 < live_cols; c0 += 8 * p.split) {
+          float x[4][kMaxSplit];
+          const size_t step = (size_t)2 * p.split * p.G * p.N;
+          const size_t at = ((size_t)(m0 + c0) * p.G + g) * p.N + n;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = c0 + 2 * i * p.split;
+#pragma unroll
+            for (int k = 0; k < kMaxSplit; ++k) {
+              x[i][k] = 0.f;
+              if (k < p.split && c < live_cols) x[i][k] = ld_cluster_f32(sums[k] + (uint32_t)c * 512u);
+            }
+          }
+          T r[4];
+          if (p.resid) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              r[i] = c0 + 2 * i * p.split < live_cols ? static_cast<const T*>(p.resid)[at + i * step] : from_f<T>(0.f);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = c0 + 2 * i * p.split;
+            if (c >= live_cols) break;
+            float v = x[i][0];
+#pragma unroll
+            for (int k = 1; k < kMaxSplit; ++k) v += x[i][k];
+            v = fmaf(v * ld_shared_f32(scales + 4u * (uint32_t)c), sum_sw, sum_bias);
+            if (p.resid) v += to_f(r[i]);
+            static_cast<T*>(p.out)[at + i * step] = from_f<T>(v);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    cluster_barrier();  // the others may still be reading this CTA's sums
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<PAIR>(tmem, kTmemCols);
   }
 }
 
-template <typename T, bool PAIR, int W>
+template <typename T, bool PAIR, int W, bool SPLIT>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& a, const Params& p, cudaStream_t st) {
-  auto k = k_linear_q8<T, PAIR, W>;
+  auto k = k_linear_q8<T, PAIR, W, SPLIT>;
   const int smem = 1024 + p.raw_stages * p.raw_bytes + kConv * p.conv_bytes + kScaleBytes + kBarBytes;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
-  const int slots = PAIR ? sm_count() / 2 : sm_count();
+  const int cluster = SPLIT ? p.split : PAIR ? 2 : 1;
+  const int slots = SPLIT ? p.num_tiles : sm_count() / cluster;
   const int n = p.num_tiles < slots ? p.num_tiles : slots;
-  return launch_k(k, dim3(PAIR ? 2 * n : n), dim3(kThreads), smem, st, PAIR ? 2 : 1, w, a, p);
+  return launch_k(k, dim3(cluster * n), dim3(kThreads), smem, st, cluster, w, a, p);
 }
 
 // The accumulators of a CTA alone (up to 96 tokens) leave TMEM room for six
 // stages of weights, those of a pair for three.
 template <typename T>
 cudaError_t dispatch(const CUtensorMap& w, const CUtensorMap& a, const Params& p, bool pair, cudaStream_t st) {
-  return pair ? launch<T, true, 3>(w, a, p, st) : launch<T, false, 6>(w, a, p, st);
+  return pair          ? launch<T, true, 3, false>(w, a, p, st)
+         : p.split > 1 ? launch<T, false, 6, true>(w, a, p, st)
+                       : launch<T, false, 6, false>(w, a, p, st);
+}
+
+// CTAs to a tile of nt tokens and num_raw steps (CTAs alone).  Few tiles leave
+// most SMs idle; sharing a tile's steps costs two cluster barriers and the sums'
+// way through shared memory.  36 clusters of four and 76 of two fit the GPU at
+// once.  us, one CTA / two / four to a tile:
+//   30 tiles of 16 tokens: 8 steps 7.0 / 7.1 / 6.9, 12 steps 8.4 / 7.8 / 7.1,
+//   30 steps 15.0 / 11.1 / 8.9; of 96: 10 steps 9.3 / 10.8 / 9.2, 12 steps
+//   10.2 / 11.4 / 9.3, 30 steps 17.9 / 15.6 / 11.6
+//   70 tiles of 16 tokens: 10 steps 7.8 / 7.9, 12 steps 8.6 / 8.3, 30 steps
+//   15.1 / 11.6; of 96: 16 steps 12.0 / 12.7, 30 steps 18.1 / 16.1
+// Eight to a tile gain little more (15 tiles of 30 steps 8.1 against 8.5) and lose
+// where no more than 15 such clusters fit (16 tiles 14.9).
+int split_of(long long tiles, int nt, int num_raw) {
+  if (tiles <= 36) return num_raw >= 8 + nt / 48 ? 4 : 1;
+  return tiles <= 72 && num_raw >= 10 + nt / 10 ? 2 : 1;
 }
 
 }  // namespace
@@ -558,6 +661,7 @@ cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t 
   p.conv_bytes = p.ntc * kConvK * 2;
   p.raw_stages = (kSmemMax - 1024 - kScaleBytes - kBarBytes - kConv * p.conv_bytes) / p.raw_bytes;
   if (p.raw_stages > kMaxRaw) p.raw_stages = kMaxRaw;
+  p.split = pair ? 1 : split_of(tiles, p.nt, p.num_raw);
   const long long rounds = (tiles + (pair ? sm_count() / 2 : sm_count()) - 1) / (pair ? sm_count() / 2 : sm_count());
   if (rounds * p.num_raw >= (1ll << 30)) return cudaErrorInvalidValue;  // more than 10^19 operations
   // kind::f16, fp16 operands (type 0), fp32 accumulator, both K-major.

@@ -306,6 +306,55 @@ def test_linear_q8(M, G, K, N, dt):
     check_linear(run_linear(*data, K, dt), *data, K, dt)
 
 
+# Few tiles of a long K: one, two and four CTAs to a tile, on both sides of each rule (steps of 128 columns,
+# tiles); one token, whole and ragged tiles of them; more than one token tile of few channels.
+SPLIT_SHAPES = [(1, 1, 1000, 128), (1, 1, 896, 128), (1, 1, 1281, 5120), (1, 1, 1280, 5120), (2, 1, 2023, 300),
+                (7, 21, 1504, 96), (96, 1, 1153, 130), (96, 2, 1152, 128), (95, 18, 2048, 128), (33, 19, 2048, 100),
+                (16, 36, 1030, 128), (17, 37, 1630, 120), (64, 72, 2060, 64), (96, 40, 2305, 60), (1, 73, 1520, 64),
+                (300, 2, 2100, 128), (21, 3, 3104, 48), (1, 1, 3840, 2570), (50, 1, 40000, 200)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,G,K,N", SPLIT_SHAPES)
+def test_linear_q8_few_tiles(M, G, K, N, dt):
+    bias, resid = (M + N) % 3 != 0, (M + K) % 2 == 0
+    data = linear_data(M, G, K, N, dt, 2 * M + K + N, bias, resid)
+    out = run_linear(*data, K, dt)
+    check_linear(out, *data, K, dt)
+    assert torch.equal(out, run_linear(*data, K, dt))
+    # A token without a scale: its row only.
+    data[1][M // 2, 0] = np.nan
+    bad = run_linear(*data, K, dt)
+    assert torch.isnan(bad[M // 2, 0]).all()
+    keep = torch.ones((M, G), dtype=torch.bool, device=bad.device)
+    keep[M // 2, 0] = False
+    assert torch.equal(bad[keep], out[keep])
+
+
+def test_linear_q8_few_tiles_in_place_in_a_graph_and_beside_another():
+    M, G, K, N, dt = 90, 3, 2100, 400, "bf16"
+    data = linear_data(M, G, K, N, dt, 11, True, True)
+    ref = run_linear(*data, K, dt)
+    args = [dev(t) for t in data[:4]] + [dev(data[4], dt)]
+    first = dev(data[5], dt)
+    bufs = [first.clone(), first.clone()]
+    layer = B.make_layer(M, G, K, N, dt)
+    graphs = []
+    for buf in bufs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            ok(B.rmx_linear_q8(layer, *args, buf, buf, torch.cuda.current_stream()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for buf, g, st in zip(bufs, graphs, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                buf.copy_(first)
+                g.replay()
+    sync()
+    assert all(torch.equal(buf, ref) for buf in bufs)
+
+
 def test_linear_q8_lowest_int8_and_padding():
     """-128 is allowed, and columns past K count for nothing where one operand has zeros there."""
     M, G, K, N = 20, 2, 50, 70
