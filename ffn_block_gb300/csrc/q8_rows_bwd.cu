@@ -55,7 +55,7 @@ template <typename T, int L, int NCH, bool CK, bool VEC>
 __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, const int W, const int rpb) {
   pdl_enter();
   __shared__ float red[64];
-  extern __shared__ float cols[];  // rpb > 1: [C] partials of the block
+  extern __shared__ float cols[];  // partials of the block's sets of warps, [sets - 1][C]
   const int lane = threadIdx.x & (L - 1), part = threadIdx.x / L, rib = part / W, w = part - rib * W;
   const float inv_n = 1.f / (float)a.C;
   const int groups = a.P / kQ8Group;
@@ -144,33 +144,44 @@ __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, 
       if (live) store_chunk<T, L, VEC>(static_cast<T*>(a.dx) + (size_t)row * a.C, c_of(j), a.C, t[j]);
     }
   }
+  // The block's partials: parts of a warp in a tree of shuffles, then sets of warps
+  // (a row's, or one) in order, the first set adding the others' to its own.
+  // (Taking turns at one row of partials, a barrier a turn: 17 us for 3363 rows of 32,
+  // 8 like this.)
   float* pg = a.pg + (size_t)blockIdx.x * a.C;
+  const int sets = L == 32 ? rpb : blockDim.x / 32, set = L == 32 ? rib : threadIdx.x >> 5;
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = col<L, VEC>(c_of(j), i);
+        float& v = i & 1 ? acc[j][i / 2].y : acc[j][i / 2].x;
+        f(v, c);
+      }
+  };
+  each([&](float& v, int c) {
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (set > 0 && c < a.C) cols[(set - 1) * a.C + c] = v;
+  });
+  if (sets > 1) __syncthreads();
+  if (set > 0) return;
 #pragma unroll 1
-  for (int r = 0; r < rpb; ++r) {
-    if (rib == r) {
-#pragma unroll
-      for (int j = 0; j < NCH; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = col<L, VEC>(c_of(j), i);
-          const float v = i & 1 ? acc[j][i / 2].y : acc[j][i / 2].x;
-          if (c < a.C) {
-            if (rpb == 1) pg[c] = v;
-            else cols[c] = r ? cols[c] + v : v;
-          }
-        }
-    }
-    if (rpb > 1) __syncthreads();
-  }
-  if (rpb > 1)
-    for (int c = threadIdx.x; c < a.C; c += blockDim.x) pg[c] = cols[c];
+  for (int r = 1; r < sets; ++r)
+    each([&](float& v, int c) {
+      if (c < a.C) v += cols[(r - 1) * a.C + c];
+    });
+  each([&](float& v, int c) {
+    if (c < a.C) pg[c] = v;
+  });
 }
 
 // How rows are spread: L lanes of W warps a row, NCH blocks of 8 * L columns
 // each, rpb rows a thread block (eight to ten warps).  Short rows take part of a
-// warp: 1,000,000 rows of 40 columns 296 us with a warp a row, 114 with 8 lanes.
+// warp: 1,000,000 rows of 40 columns 296 us with a warp a row, 100 with 8 lanes.
 // One block a warp where 16 warps hold the row: 65536 x 1280 in 211 us with a
-// warp a row, 124 with five.
+// warp a row, 122 with five.
 struct Spread {
   int L, W, nch, rpb, threads;
 };
@@ -188,7 +199,8 @@ Spread spread_of(int C) {
 template <typename T, bool CK, bool VEC>
 cudaError_t rows_bwd(const RowsBwd& a, cudaStream_t st) {
   const Spread s = spread_of(a.C);
-  const size_t smem = s.rpb > 1 ? (size_t)a.C * sizeof(float) : 0;
+  const int sets = s.L == 32 ? s.rpb : s.threads / 32;
+  const size_t smem = (size_t)(sets - 1) * a.C * sizeof(float);  // 9 KB at most
   auto k = s.L == 8      ? k_rows_bwd<T, 8, 1, CK, VEC>
            : s.L == 16   ? k_rows_bwd<T, 16, 1, CK, VEC>
            : s.nch == 1  ? k_rows_bwd<T, 32, 1, CK, VEC>
