@@ -17,65 +17,51 @@ namespace rmx {
 namespace {
 
 // Copies of up to this many elements take an element a thread (k_pad_small), the
-// others a warp a row.  A step with 32 such copies: 116 us by elements and 136 by
+// others a warp a row.  A step with 32 such copies: 113 us by elements and 136 by
 // rows for 8 samples of T = 8, D = 72, H = 148; 571 us and 535 for 256 samples of
 // T = 10, D = 1230, H = 2460 (with the elements' form up to 2^22).  2^18 and 2^20
 // measured alike.
 constexpr size_t kPadSmall = 1 << 19;
 
+// Destination and source as rows of dw and sw elements (a half each), dn and sn
+// of them to an outer index; what the source does not have is zero.  The
+// destination is written in order.
+struct Run {
+  int dw, sw, dn, sn;
+  long long total;
+};
+
 // Small copies: one thread per destination element, its place from 32-bit
 // divisions, so that nothing waits for the element before it.
 template <typename E>
-__global__ void __launch_bounds__(256) k_pad_small(const E* __restrict__ src, E* __restrict__ dst, PadMap m,
-                                                   int pack, uint32_t total) {
+__global__ void __launch_bounds__(256) k_pad_small(const E* __restrict__ src, E* __restrict__ dst, const Run p) {
   pdl_enter();
   const uint32_t idx = blockIdx.x * 256 + threadIdx.x;
-  if (idx >= total) return;
-  const uint32_t hs = m.cols / m.halves, hsp = m.cols_p / m.halves;
-  const uint32_t dcols = pack ? m.cols_p : m.cols, drows = pack ? m.rows_p : m.rows;
-  const uint32_t d = idx / dcols, c = idx - d * dcols, o = d / drows, r = d - o * drows;
-  if (pack) {
-    // padded (o, r, c) <- logical (o, r, h * hs + cc) with c = h * hsp + cc
-    const uint32_t h = c / hsp, cc = c - h * hsp;
-    dst[idx] = r < (uint32_t)m.rows && cc < hs ? src[(size_t)(o * m.rows + r) * m.cols + h * hs + cc] : E(0);
-  } else {
-    // logical (o, r, c) <- padded (o, r, h * hsp + cc) with c = h * hs + cc
-    const uint32_t h = c / hs, cc = c - h * hs;
-    dst[idx] = src[(size_t)(o * m.rows_p + r) * m.cols_p + h * hsp + cc];
-  }
+  if (idx >= (uint32_t)p.total) return;
+  const uint32_t d = idx / (uint32_t)p.dw, c = idx - d * p.dw, o = d / (uint32_t)p.dn, r = d - o * p.dn;
+  dst[idx] = r < (uint32_t)p.sn && c < (uint32_t)p.sw ? src[((size_t)o * p.sn + r) * p.sw + c] : E(0);
 }
 
-// Large ones: eight warps a CTA, a warp takes up to 1024 columns of one half of
-// a destination row at a time (its place is worked out once), neighbouring lanes
-// neighbouring columns.  8192 rows of 1001 16-bit values: 41 us an element a
-// thread, 17 us like this.
+// Large ones: a warp takes up to 1024 columns of a destination row at a time (its
+// place is divided out once), neighbouring lanes neighbouring columns.  8192 rows
+// of 1001 16-bit values: 17 us; 41 an element a thread with 64-bit divisions, 23
+// as runs of 1024 elements across rows, whose loads wait for the place.
 template <typename E>
-__global__ void __launch_bounds__(256) k_pad_copy(const E* __restrict__ src, E* __restrict__ dst, PadMap m,
-                                                  int pack) {
+__global__ void __launch_bounds__(256) k_pad_copy(const E* __restrict__ src, E* __restrict__ dst, const Run p,
+                                                  int segs, long long items) {
   pdl_enter();
-  const int hs = m.cols / m.halves, hsp = m.cols_p / m.halves;
-  const int dcols = pack ? m.cols_p : m.cols, drows = pack ? m.rows_p : m.rows;
   const int lane = threadIdx.x & 31;
-  const int W = pack ? hsp : hs, segs = (W + 1023) / 1024, per_row = m.halves * segs;
-  const long long items = (long long)m.outer * drows * per_row, step = (long long)gridDim.x * 8;
-  const bool narrow = items < (1ll << 31);  // one 32-bit division for the place
+  const long long step = (long long)gridDim.x * 8;
+  const bool narrow = items < (1ll << 31);  // 32-bit divisions
   for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += step) {
-    const long long d = narrow ? (long long)((uint32_t)it / (uint32_t)per_row) : it / per_row;
-    const long long o = narrow ? (long long)((uint32_t)d / (uint32_t)drows) : d / drows;
-    const int r = (int)(d - o * drows), part = (int)(it - d * per_row), h = part / segs;
-    const int c0 = (part - h * segs) * 1024, c1 = min(W, c0 + 1024);
-    E* out = dst + d * dcols + (long long)h * W;
-    if (pack) {
-      // padded (o, r, h * hsp + cc) <- logical (o, r, h * hs + cc)
-      const E* in = src + (o * m.rows + r) * (long long)m.cols + (long long)h * hs;
+    const long long d = narrow ? (long long)((uint32_t)it / (uint32_t)segs) : it / segs;
+    const long long o = narrow ? (long long)((uint32_t)d / (uint32_t)p.dn) : d / p.dn;
+    const int r = (int)(d - o * p.dn), c0 = (int)(it - d * segs) * 1024, c1 = min(p.dw, c0 + 1024);
+    const int real = r < p.sn ? p.sw : 0;
+    const E* in = src + (o * p.sn + r) * p.sw;
+    E* out = dst + d * p.dw;
 #pragma unroll 8
-      for (int cc = c0 + lane; cc < c1; cc += 32) out[cc] = r < m.rows && cc < hs ? in[cc] : E(0);
-    } else {
-      // logical (o, r, h * hs + cc) <- padded (o, r, h * hsp + cc)
-      const E* in = src + (o * m.rows_p + r) * (long long)m.cols_p + (long long)h * hsp;
-#pragma unroll 8
-      for (int cc = c0 + lane; cc < c1; cc += 32) out[cc] = in[cc];
-    }
+    for (int c = c0 + lane; c < c1; c += 32) out[c] = c < real ? in[c] : E(0);
   }
 }
 
@@ -117,20 +103,20 @@ cudaError_t launch_pad_copy(const void* src, void* dst, int dtype, const PadMap&
   if (m.outer < 0 || m.rows < 0 || m.rows > m.rows_p || m.cols > m.cols_p || m.halves < 1 ||
       m.cols % m.halves || m.cols_p % m.halves)
     return cudaErrorInvalidValue;
-  const size_t total = (size_t)m.outer * (pack ? (size_t)m.rows_p * m.cols_p : (size_t)m.rows * m.cols);
-  if (total == 0) return cudaSuccess;
-  const int w = (pack ? m.cols_p : m.cols) / m.halves;
-  const size_t items = (size_t)m.outer * (pack ? m.rows_p : m.rows) * m.halves * ((w + 1023) / 1024);
+  const int hs = m.cols / m.halves, hsp = m.cols_p / m.halves;
+  Run p{hsp, hs, m.rows_p * m.halves, m.rows * m.halves, (long long)m.outer * m.rows_p * m.cols_p};
+  if (!pack) p = Run{hs, hsp, m.rows * m.halves, m.rows_p * m.halves, (long long)m.outer * m.rows * m.cols};
+  if (p.total == 0) return cudaSuccess;
   auto go = [&](auto e) {
     using E = decltype(e);
     const E* from = static_cast<const E*>(src);
     E* to = static_cast<E*>(dst);
-    if (total <= kPadSmall)
-      return launch_k(k_pad_small<E>, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, 1, from, to, m,
-                      pack ? 1 : 0, (uint32_t)total);
-    const size_t want = (items + 7) / 8, most = (size_t)sm_count() * 16;
-    return launch_k(k_pad_copy<E>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, 1, from, to, m,
-                    pack ? 1 : 0);
+    if (p.total <= (long long)kPadSmall)
+      return launch_k(k_pad_small<E>, dim3((unsigned)((p.total + 255) / 256)), dim3(256), 0, st, 1, from, to, p);
+    const int segs = (p.dw + 1023) / 1024;
+    const long long items = p.total / p.dw * segs, want = (items + 7) / 8, most = (long long)sm_count() * 16;
+    return launch_k(k_pad_copy<E>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, 1, from, to, p, segs,
+                    items);
   };
   return dtype == 0 ? go(uint32_t{}) : go(uint16_t{});
 }
