@@ -643,8 +643,12 @@ cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t 
   // A CTA alone up to 96 tokens (what three warps convert), a pair above: the
   // pair shares the tokens' conversion, which a CTA alone would do for all of
   // them.  16 groups of 1280 -> 5120, us alone / as a pair: 64 tokens 29.5 /
-  // 30.0, 96 31.9 / 32.7, 97 47 / 33.7, 192 50 / 36, 1024 231 / 151.
-  const bool pair = d.M > kMaxAlone && d.N > 128;
+  // 30.0, 96 31.9 / 32.7, 97 47 / 33.7, 192 50 / 36, 1024 231 / 151.  But alone
+  // while there is an SM for every tile: they are narrower, and can be shared
+  // (pair / alone: 706 x 2 tokens, 2979 -> 214, 17.9 / 11.1; 490 x 5, 2147 -> 357,
+  // 16.3 / 13.7; 192 x 8, 256 -> 1024, 7.7 / 5.9).
+  const long long alone = (long long)d.G * ((d.N + 127) / 128) * ((d.M + kMaxAlone - 1) / kMaxAlone);
+  const bool pair = d.M > kMaxAlone && d.N > 128 && alone > sm_count();
   const int most = pair ? kMaxNT : kMaxAlone;
   p.tiles_m = (d.M + most - 1) / most;
   const int even = (d.M + p.tiles_m - 1) / p.tiles_m;

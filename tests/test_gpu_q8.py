@@ -331,6 +331,21 @@ def test_linear_q8_few_tiles(M, G, K, N, dt):
     assert torch.equal(bad[keep], out[keep])
 
 
+# Pairs of CTAs: more tiles of up to 96 tokens and 128 channels than SMs (one fewer, one more), one token tile of
+# a pair and two, ragged ends of all three.
+PAIR_SHAPES = [(97, 38, 64, 256), (97, 39, 64, 256), (97, 60, 70, 129), (112, 80, 33, 200), (192, 80, 128, 256), (193, 40, 129, 257),
+               (200, 18, 320, 384), (256, 13, 1000, 512), (385, 20, 64, 600), (700, 3, 416, 771), (1024, 4, 130, 640),
+               (300, 25, 4100, 200), (128, 150, 40, 130)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,G,K,N", PAIR_SHAPES + [(706, 2, 2979, 214), (129, 1, 1100, 257), (385, 9, 1000, 256)])
+def test_linear_q8_many_tokens(M, G, K, N, dt):
+    bias, resid = (M + G) % 3 != 0, (M + K) % 2 == 0
+    data = linear_data(M, G, K, N, dt, M + 3 * K + N, bias, resid)
+    check_linear(run_linear(*data, K, dt), *data, K, dt)
+
+
 def test_linear_q8_few_tiles_in_place_in_a_graph_and_beside_another():
     M, G, K, N, dt = 90, 3, 2100, 400, "bf16"
     data = linear_data(M, G, K, N, dt, 11, True, True)
