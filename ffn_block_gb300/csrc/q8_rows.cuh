@@ -90,13 +90,13 @@ __device__ __forceinline__ uint2 low_bytes(const float2 (&t)[4]) {
 // Eight int8 of a row whose pitch holds them; `keep` false writes zeros.
 template <int L, bool VEC>
 __device__ __forceinline__ void store_bytes(int8_t* row, int c0, int P, const float2 (&t)[4], bool keep) {
-  const uint2 b = keep ? low_bytes(t) : make_uint2(0, 0);
   if constexpr (VEC) {
-    if (c0 < P) *reinterpret_cast<uint2*>(row + c0) = b;
+    if (c0 < P) *reinterpret_cast<uint2*>(row + c0) = keep ? low_bytes(t) : make_uint2(0, 0);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (col<L, VEC>(c0, i) < P) row[col<L, VEC>(c0, i)] = (int8_t)((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
+      if (col<L, VEC>(c0, i) < P)
+        row[col<L, VEC>(c0, i)] = keep ? (int8_t)__float_as_uint(i & 1 ? t[i / 2].y : t[i / 2].x) : (int8_t)0;
   }
 }
 template <int L, bool VEC> __device__ __forceinline__ uint2 load_bytes(const int8_t* row, int c0, int P) {
