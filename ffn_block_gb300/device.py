@@ -45,6 +45,7 @@ class RankMixerDevice:
         self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=self.device)
         self.c_params = B.make_params(self.params)
         self.c_grads = B.make_grads(self.grads)
+        self.q8 = None  # int8 weights and their scales, from the first quantize_weights
 
     def forward(self, stream=None) -> None:
         B.check(B.rmx_forward(self.cfg, _ptr_or_none(self.x), self.c_params, self.saved, self.saved_bytes,
@@ -62,15 +63,25 @@ class RankMixerDevice:
     # ---------------------------------------------------------------- 8 bits
 
     def quantize_weights(self, stream=None) -> None:
-        """int8 copies of w1 and wout for forward_q8 (once per weight update)."""
+        """int8 copies of w1 and wout for forward_q8 (once per weight update).
+
+        The first call makes the buffers, every later one writes them again in
+        place, so a graph captured from forward_q8 stays valid.  As with the
+        parameters themselves, the caller orders an update after the work that
+        still reads the old copies."""
+        if self.q8 is None:
+            self._make_q8_buffers()
+        s = self.shape
+        for name, K, N in (("w1", s.D, 2 * s.H), ("wout", s.H, s.D)):
+            B.check(B.rmx_weight_q8(B.make_layer(max(s.B, 1), s.T, K, N, s.dtype), self.params[name], self.q8[name],
+                                    self.q8[name + "_scale"], stream), "rmx_weight_q8")
+
+    def _make_q8_buffers(self) -> None:
         s = self.shape
         self.q8 = {}
         for name, K, N in (("w1", s.D, 2 * s.H), ("wout", s.H, s.D)):
-            q = torch.empty((s.T, N, B.rmx_q8_pitch(K)), dtype=torch.int8, device=self.device)
-            scale = torch.empty((s.T, N), dtype=torch.float32, device=self.device)
-            B.check(B.rmx_weight_q8(B.make_layer(max(s.B, 1), s.T, K, N, s.dtype), self.params[name], q, scale, stream),
-                    "rmx_weight_q8")
-            self.q8[name], self.q8[name + "_scale"] = q, scale
+            self.q8[name] = torch.empty((s.T, N, B.rmx_q8_pitch(K)), dtype=torch.int8, device=self.device)
+            self.q8[name + "_scale"] = torch.empty((s.T, N), dtype=torch.float32, device=self.device)
         self.c_q8 = B.make_q8_weights(self.q8["w1"], self.q8["w1_scale"], self.q8["wout"], self.q8["wout_scale"])
         self.ws_q8 = torch.empty(max(B.rmx_forward_q8_workspace_bytes(self.cfg), 1), dtype=torch.uint8,
                                  device=self.device)
