@@ -61,6 +61,15 @@ class RankMixerDevice:
         self.backward(stream)
 
     # ---------------------------------------------------------------- 8 bits
+    # Buffers that these methods make are taken from the pool of the stream
+    # that fills them: what torch's current stream has freed, its pending work
+    # may still use.
+
+    def _torch_stream(self, stream):
+        """The torch stream of a `stream` argument (None: the legacy default stream)."""
+        if stream is None or (isinstance(stream, int) and stream in (0, 1)):  # 1: cudaStreamLegacy
+            return torch.cuda.default_stream(self.device)
+        return torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
 
     def quantize_weights(self, stream=None) -> None:
         """int8 copies of w1 and wout for forward_q8 (once per weight update).
@@ -70,7 +79,8 @@ class RankMixerDevice:
         parameters themselves, the caller orders an update after the work that
         still reads the old copies."""
         if self.q8 is None:
-            self._make_q8_buffers()
+            with torch.cuda.stream(self._torch_stream(stream)):
+                self._make_q8_buffers()
         s = self.shape
         for name, K, N in (("w1", s.D, 2 * s.H), ("wout", s.H, s.D)):
             B.check(B.rmx_weight_q8(B.make_layer(max(s.B, 1), s.T, K, N, s.dtype), self.params[name], self.q8[name],
@@ -93,14 +103,19 @@ class RankMixerDevice:
 
     def pack_saved(self, stream=None) -> torch.Tensor:
         """The saved activations of the last forward as 8-bit checkpoints."""
-        out = torch.empty(max(B.rmx_saved8_bytes(self.cfg), 1), dtype=torch.uint8, device=self.device)
+        with torch.cuda.stream(self._torch_stream(stream)):
+            out = torch.empty(max(B.rmx_saved8_bytes(self.cfg), 1), dtype=torch.uint8, device=self.device)
         B.check(B.rmx_saved_pack8(self.cfg, self.saved, self.saved_bytes, out, out.numel(), stream), "rmx_saved_pack8")
         return out
 
     def unpack_saved(self, packed: torch.Tensor, stream=None) -> None:
-        """Checkpoints of pack_saved back into the saved buffer, for backward()."""
+        """Checkpoints of pack_saved back into the saved buffer, for backward().
+
+        `packed` may be dropped at once: its memory is not used for anything
+        else before `stream` has read it."""
         B.check(B.rmx_saved_unpack8(self.cfg, packed, packed.numel(), self.saved, self.saved_bytes, stream),
                 "rmx_saved_unpack8")
+        packed.record_stream(self._torch_stream(stream))
 
     def results(self) -> dict:
         """y, dx and every gradient as float64 numpy arrays (synchronises)."""

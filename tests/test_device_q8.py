@@ -1,8 +1,10 @@
 """Buffers of RankMixerDevice's 8-bit methods, with the library's calls faked (no GPU)."""
 
+import contextlib
 import os
 
 import pytest
+import torch
 
 from ffn_block_gb300 import binding as B
 from ffn_block_gb300 import inputs as I
@@ -25,6 +27,21 @@ def blk(monkeypatch):
             return B.RMX_OK
         return call
 
+    # Streams: torch's current one is "current" unless a context says otherwise.
+    blk.allocated, blk.recorded, current = [], [], ["current"]
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: blk.allocated.append(current[-1]) or empty(*a, **k))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s, device=None: ("external", s))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: blk.recorded.append((t.data_ptr(), s)))
     for name in ("rmx_weight_q8", "rmx_forward_q8", "rmx_saved_pack8", "rmx_saved_unpack8"):
         monkeypatch.setattr(B, name, fake(name))
     return blk
@@ -42,3 +59,18 @@ def test_weights_are_quantised_again_in_place(blk):
     writes = [c[1][2:4] for c in blk.calls]
     assert writes == 2 * [(first["w1"], first["w1_scale"]), (first["wout"], first["wout_scale"])]
     del keep
+
+
+class Stream:
+    cuda_stream = 0x4000
+
+
+@pytest.mark.parametrize("stream,expect", [(None, "default"), (0, "default"), (1, "default"), (0x4000, ("external", 0x4000)),
+                                           (Stream, Stream)])
+def test_buffers_belong_to_the_stream_that_uses_them(blk, stream, expect):
+    blk.quantize_weights(stream)
+    packed = blk.pack_saved(stream)
+    assert blk.allocated == 6 * [expect]        # two weights, two scales, the workspace, the checkpoint
+    assert blk.recorded == []
+    blk.unpack_saved(packed, stream)
+    assert blk.recorded == [(packed.data_ptr(), expect)]
