@@ -181,7 +181,7 @@ __device__ __forceinline__ void arrive_if(uint32_t bar, bool pred) {
 // of half it - 6 are done, weights to TMEM stage it % W once those of half
 // it - W are (W is 3 where the accumulators leave room for no more); the
 // barriers are those of the conv stages either way.
-template <int W, bool WEIGHTS>
+template <bool PAIR, int W, bool WEIGHTS>
 __device__ __forceinline__ void convert(int set, int row, bool live, int halves, uint32_t src0, uint32_t raw_bytes,
                                         int raw_stages, uint32_t raw_bar, uint32_t conv_full, uint32_t conv_empty,
                                         uint32_t dst0, uint32_t conv_bytes, const WaitCtx& wc) {
@@ -198,6 +198,18 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
   int rs = set >> 1;
   uint32_t src = ((src0 + (uint32_t)rs * raw_bytes) | swz) ^ ((uint32_t)(set & 1) << 6);  // bit 6: the upper half
   uint32_t rph = 0, lap = 0;  // parities of the raw stages' and the conv stages' laps
+  // A raw stage that has been read.  The copy that fills it again is of the
+  // async proxy: only a proxy fence orders the warp's reads before its writes.
+  // (Without it a read that had been issued, but waited behind the epilogue's
+  // stores, returned the next contents.)  As soon as the reads are issued for
+  // CTAs alone, after the conversion for pairs, where the fence's wait costs
+  // more than the stage (the other way round: one sample 1280 -> 5120 73.0 /
+  // 74.3 us, 1024 x 16 157 / 161, 1000 x 40 3600 -> 1200 262 / 271).
+  auto hand_back = [&](uint32_t bar) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    arrive_if(bar, one);
+  };
 #pragma unroll 1
   for (int i = set; i < halves; i += 2 * kSets) {
 #pragma unroll
@@ -210,11 +222,7 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
       for (int c = 0; c < 4; c += 2) {
         const uint4 v = ld_shared_v4(src ^ (uint32_t)(c << 4));
         const uint4 w = ld_shared_v4(src ^ (uint32_t)((c + 1) << 4));
-        if (c == 2) {
-          // Read: the raw stage is handed back.
-          __syncwarp();
-          arrive_if(rbar + 8u * kMaxRaw, one);
-        }
+        if (c == 2 && !PAIR) hand_back(rbar + 8u * kMaxRaw);
         uint32_t* q = o + 8 * c;
         widen(v.x, q[0], q[1]);
         widen(v.y, q[2], q[3]);
@@ -225,6 +233,7 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
         widen(w.z, q[12], q[13]);
         widen(w.w, q[14], q[15]);
       }
+      if (PAIR) hand_back(rbar + 8u * kMaxRaw);
       // The half whose MMAs free this place: six back (this conv stage, the
       // lap before), or three (the other one of this set).
       constexpr bool kThree = WEIGHTS && W == 3;
@@ -431,17 +440,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (role < kWWarps) {
       // The channel is the TMEM lane, and a warp reaches the quarter warp % 4.
       const int row = (warp & 3) * 32 + lane;
-      convert<W, true>(set, row, true, halves, sRaw + (uint32_t)row * 128u, p.raw_bytes, p.raw_stages, raw_full(0), full0,
-                       conv_empty(0), tmemA + ((uint32_t)((warp & 3) * 32) << 16), 0, wc);
+      convert<PAIR, W, true>(set, row, true, halves, sRaw + (uint32_t)row * 128u, p.raw_bytes, p.raw_stages,
+                             raw_full(0), full0, conv_empty(0), tmemA + ((uint32_t)((warp & 3) * 32) << 16), 0, wc);
     } else {
       // Warps without tokens stay out; a lane without a token reads the first
       // token's place and writes nothing.
       const int row = (role - kWWarps) * 32 + lane;
       const bool live = row < p.ntc;
       if (row - lane < p.ntc)
-        convert<W, false>(set, row, live, halves, sRaw + 128 * kRawK + (live ? (uint32_t)row * 128u : 0u),
-                          p.raw_bytes, p.raw_stages, raw_full(0), full0, conv_empty(0), sConv + (uint32_t)row * 128u,
-                          p.conv_bytes, wc);
+        convert<PAIR, W, false>(set, row, live, halves, sRaw + 128 * kRawK + (live ? (uint32_t)row * 128u : 0u),
+                                p.raw_bytes, p.raw_stages, raw_full(0), full0, conv_empty(0),
+                                sConv + (uint32_t)row * 128u, p.conv_bytes, wc);
     }
     __syncwarp();
   } else {
