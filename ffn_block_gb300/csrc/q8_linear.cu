@@ -133,14 +133,55 @@ struct WaitCtx {
   unsigned int* err;
   volatile int* abort;
 };
+// How the CTAs of a pair hand data over.  One CTA's warps arrive on a barrier
+// of the other at cluster scope, relaxed.  What they wrote to or read from TMEM
+// is ordered by the tcgen05 fences on both sides (TENSOR); what they wrote to
+// their shared memory by a release fence before the arrival, restricted to
+// shared memory, and a wait that acquires at cluster scope (MEMORY).  An
+// arrival that itself releases at cluster scope waits for all writes of its
+// thread, global ones too, about 1000 cycles: with one thread of the odd CTA
+// passing its warps' arrivals on in that way, 1024 x 64 tokens 1280 -> 5120
+// take 1212 us, in this way 620 to 680 (as the power limit allows).
+enum Order { LOCAL, TENSOR, MEMORY };
+// Arrival by the lanes with pred set (one of a converged warp), on a barrier of
+// this CTA (LOCAL) or of the cluster.
+template <Order O> __device__ __forceinline__ void arrive_if(uint32_t bar, bool pred) {
+  if (O == MEMORY) asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  if (O == LOCAL)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"((uint32_t)pred)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar), "r"((uint32_t)pred)
+        : "memory");
+}
+// One look at a barrier of this CTA on which LOCAL threads and copies arrive, or
+// the pair's other CTA and the issuer's commits too.
+template <Order O> __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) {
+  if (O == LOCAL) return mbar_try_wait(bar, parity);
+  if (O == MEMORY) return mbar_try_wait_cluster(bar, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // The rest of a bounded wait, out of line: it spins, now and then looking at
 // the clock and at whether another warp has given up.
+template <Order O>
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, unsigned int bit, uint64_t limit_ns,
                                      unsigned int* err, volatile int* abort) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     for (int i = 0; i < 1024; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+      if (look<O>(bar, parity)) return true;
     if (*abort) return false;
     if (globaltimer_ns() - t0 > limit_ns) {
       atomicOr(err, bit);
@@ -149,30 +190,20 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, unsigned int
     }
   }
 }
+template <Order O>
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t ph, unsigned int bit, const WaitCtx& w) {
 #pragma unroll 1
   for (int i = 0; i < 512; ++i)
-    if (mbar_try_wait(bar, ph)) return true;
-  return wait_on(bar, ph, bit, w.limit_ns, w.err, w.abort);
+    if (look<O>(bar, ph)) return true;
+  return wait_on<O>(bar, ph, bit, w.limit_ns, w.err, w.abort);
 }
 // The same by a whole warp, which goes on or gives up together.
+template <Order O>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t ph, unsigned int bit, const WaitCtx& w) {
 #pragma unroll 1
   for (int i = 0; i < 512; ++i)
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) return true;
-  return __all_sync(0xffffffffu, wait_on(bar, ph, bit, w.limit_ns, w.err, w.abort));
-}
-// Arrival by the lanes with pred set (one of a converged warp), on this CTA's
-// barrier or another's of the cluster.  CTA scope orders nothing in another
-// CTA's memory, which a cluster-scope release would do at the price of a fence
-// (about 1000 cycles); what is handed over here is read by the tensor cores
-// of the arriving thread's own SM (its TMEM, and its shared memory behind a
-// proxy fence), the other CTA only issuing the MMA.
-__device__ __forceinline__ void arrive_if(uint32_t bar, bool pred) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar), "r"((uint32_t)pred)
-      : "memory");
+    if (__all_sync(0xffffffffu, look<O>(bar, ph))) return true;
+  return __all_sync(0xffffffffu, wait_on<O>(bar, ph, bit, w.limit_ns, w.err, w.abort));
 }
 
 // A converter warp's run.  Half `it` (64 k) of the CTA's run is half it % 2 of
@@ -185,6 +216,7 @@ template <bool PAIR, int W, bool WEIGHTS>
 __device__ __forceinline__ void convert(int set, int row, bool live, int halves, uint32_t src0, uint32_t raw_bytes,
                                         int raw_stages, uint32_t raw_bar, uint32_t conv_full, uint32_t conv_empty,
                                         uint32_t dst0, uint32_t conv_bytes, const WaitCtx& wc) {
+  constexpr Order ORDER = !PAIR ? LOCAL : WEIGHTS ? TENSOR : MEMORY;  // tokens are handed over in shared memory
   const bool one = (threadIdx.x & 31) == 0;
   // 16-byte chunk j of a 128-byte row sits at j ^ (row & 7): rows are 128
   // bytes aligned, so its address is (row's | swizzle) ^ (j << 4).
@@ -208,7 +240,7 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
   auto hand_back = [&](uint32_t bar) {
     fence_proxy_async_smem();
     __syncwarp();
-    arrive_if(bar, one);
+    arrive_if<LOCAL>(bar, one);
   };
 #pragma unroll 1
   for (int i = set; i < halves; i += 2 * kSets) {
@@ -216,7 +248,7 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
     for (int j = 0; j < 2; ++j) {
       if (j && i + kSets >= halves) return;
       const uint32_t rbar = raw_bar + 8u * (uint32_t)rs;
-      if (!wait_warp(rbar, rph, ERRBIT_WAIT_ROWS, wc)) return;
+      if (!wait_warp<LOCAL>(rbar, rph, ERRBIT_WAIT_ROWS, wc)) return;
       uint32_t o[32];
 #pragma unroll
       for (int c = 0; c < 4; c += 2) {
@@ -239,7 +271,7 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
       constexpr bool kThree = WEIGHTS && W == 3;
       const uint32_t e = cempty + (((j & 1) != 0) != kThree ? 8u * kSets : 0u);
       const uint32_t eph = kThree && (j & 1) ? lap : lap ^ 1u;
-      if (!wait_warp(e, eph, ERRBIT_WAIT_ROWS, wc)) return;
+      if (!wait_warp<ORDER>(e, eph, ERRBIT_WAIT_ROWS, wc)) return;
       if (WEIGHTS) {
         tc_fence_after();
         tmem_st_32x32(dst[j], o);
@@ -254,7 +286,7 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
         fence_proxy_async_smem();
       }
       __syncwarp();
-      arrive_if(cfull + (j ? 8u * kSets : 0u), one);
+      arrive_if<ORDER>(cfull + (j ? 8u * kSets : 0u), one);
       if (j) lap ^= 1u;
       // Three halves on: one raw stage and a half.
       const int adv = ((set + j) & 1) ? 2 : 1;
@@ -298,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int raw0 = SPLIT ? p.num_raw * share / p.split : 0;
   const int num_raw = SPLIT ? p.num_raw * (share + 1) / p.split - raw0 : p.num_raw;
   constexpr int CTAS = PAIR ? 2 : 1;
+  constexpr Order CROSS = PAIR ? TENSOR : LOCAL;
   const int twarps = (p.ntc + 31) / 32;  // of each set, the warps that have tokens
   // Tile -> group, this CTA's first channel, the tile's first token.  Tiles
   // that share weights are neighbours.
@@ -351,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int g, n0, m0;
         coords(tile, g, n0, m0);
         for (int rk = raw0; rk < raw0 + num_raw; ++rk) {
-          if (!wait_one(raw_empty(s), ph ^ 1u, ERRBIT_WAIT_PRODUCER, wc)) {
+          if (!wait_one<LOCAL>(raw_empty(s), ph ^ 1u, ERRBIT_WAIT_PRODUCER, wc)) {
             ok = false;
             break;
           }
@@ -389,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t conv_step = (uint32_t)p.conv_bytes >> 4;  // descriptor addresses count 16 bytes
       for (int lt = 0; ok && lt < my_tiles; ++lt) {
         const int acc = lt & 1;
-        if (!wait_one(d_empty(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u, ERRBIT_WAIT_MMA, wc)) {
+        if (!wait_one<CROSS>(d_empty(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u, ERRBIT_WAIT_MMA, wc)) {
           ok = false;
           break;
         }
@@ -401,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The two halves of a raw stage.
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!wait_one(conv_full(s), ph, ERRBIT_WAIT_MMA, wc)) {
+            if (!wait_one<PAIR ? MEMORY : LOCAL>(conv_full(s), ph, ERRBIT_WAIT_MMA, wc)) {
               ok = false;
               break;
             }
@@ -474,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = lane; c < p.nt; c += 32)
         st_shared_f32(scales + 4u * (uint32_t)c, c < live_cols ? p.sa[(size_t)(m0 + c) * p.G + g] : 0.f);
       __syncwarp();
-      if (!wait_warp(d_full(acc), (uint32_t)(lt >> 1) & 1u, ERRBIT_WAIT_EPILOGUE, wc)) {
+      if (!wait_warp<CROSS>(d_full(acc), (uint32_t)(lt >> 1) & 1u, ERRBIT_WAIT_EPILOGUE, wc)) {
         ok = false;
         break;
       }
@@ -533,14 +566,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      arrive_if(PAIR ? mapa_shared(d_empty(acc), 0) : d_empty(acc), lane == 0);
+      arrive_if<CROSS>(PAIR ? mapa_shared(d_empty(acc), 0) : d_empty(acc), lane == 0);
     }
     // No commit may still be on its way to this CTA's barriers at the end:
     // wait for the last use of every stage.
     if (ok && warp == kFirstEpi) {
       const long long its = 2ll * lt * num_raw;
       for (long long j = its > kConv ? its - kConv : 0; ok && j < its; ++j)
-        ok = wait_warp(conv_empty((int)(j % kConv)), (uint32_t)(j / kConv) & 1u, ERRBIT_WAIT_DRAIN, wc);
+        ok = wait_warp<CROSS>(conv_empty((int)(j % kConv)), (uint32_t)(j / kConv) & 1u, ERRBIT_WAIT_DRAIN, wc);
     }
   }
 

@@ -15,9 +15,11 @@ pytestmark = pytest.mark.gpu
 # CTAs alone, several tiles each, and two and four CTAs to a tile
 ALONE = [(64, 130, 1000, 300), (96, 100, 1024, 520), (16, 200, 700, 640), (5, 40, 1000, 5000)]
 SPLIT = [(90, 6, 1024, 600), (16, 70, 1030, 100), (1, 1, 1040, 4500), (96, 18, 1024, 200)]
+# several tiles a pair
+PAIRS = [(192, 90, 128, 256), (100, 100, 1000, 300), (400, 40, 1000, 520), (97, 160, 40, 257), (1024, 4, 1040, 640)]
 
 
-@pytest.mark.parametrize("M,G,K,N", ALONE + SPLIT)
+@pytest.mark.parametrize("M,G,K,N", ALONE + SPLIT + PAIRS)
 def test_linear_beside_other_work(M, G, K, N):
     g = torch.Generator(device="cuda").manual_seed(M + K)
     P = B.rmx_q8_pitch(K)
