@@ -543,6 +543,9 @@ __global__ void __launch_bounds__(THREADS + (SUMS ? 32 * SUM_WARPS : 0), 1)
             }
           }
         }
+        // The stage's next contents come by the async proxy, which only a proxy
+        // fence orders behind these reads.
+        fence_proxy_async_smem();
         // The four warps meet, and go on or give up together.
         asm volatile(
             "{\n\t.reg .pred a, b;\n\t"
