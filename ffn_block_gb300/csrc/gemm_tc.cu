@@ -522,8 +522,14 @@ __global__ void __launch_bounds__(THREADS + (SUMS ? 32 * SUM_WARPS : 0), 1)
       uint32_t ok = 1;
       int s = (int)(it % STAGES);
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (lane == 0)
-          ok = mbar_wait_bounded(used_bar(s), (phases >> s) & 1u, p.wait_limit_ns, p.err, ERRBIT_WAIT_ROWS, abort_flag);
+        // In a pair the odd CTA's copies are counted on the even one's `full`,
+        // and what says that they have landed is the even CTA's commit: the
+        // wait acquires at cluster scope, and these plain loads with it.
+        if (lane == 0) {
+          const uint32_t parity = (phases >> s) & 1u;
+          ok = PAIR ? mbar_wait_bounded_cluster(used_bar(s), parity, p.wait_limit_ns, p.err, ERRBIT_WAIT_ROWS, abort_flag)
+                    : mbar_wait_bounded(used_bar(s), parity, p.wait_limit_ns, p.err, ERRBIT_WAIT_ROWS, abort_flag);
+        }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         phases ^= 1u << s;
         if (ok) {
