@@ -230,6 +230,10 @@ __global__ void __maxnreg__(MODE == LNB_MIXED_TOO ? 128 : 96) k_ln_bwd_ring(cons
       const float k = warp_sum4_transposed(rsum[0], rsum[1], rsum[2], rsum[3]);
       if ((lane & 7) == 0) rb[(lane >> 3) * 32 + warp] = k;
     }
+    // The row sums have used what was read of the first two tensors, but
+    // nothing yet the residual: a proxy fence orders its reads before the
+    // copies that fill the stages again.
+    if (MODE == LNB_RESID) fence_proxy_async_smem();
     if (__syncthreads_or(!ok)) {
       aborted = true;
       break;
