@@ -80,6 +80,7 @@ struct LinearQ8 {
   const void *bias, *resid;  // may be null
   void* out;
 };
+bool linear_q8_supported(const LinearQ8& d);  // looks at the sizes only
 cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t st);
 
 }  // namespace rmx

@@ -25,6 +25,9 @@ bool layer_ok(const rmx_layer* l) {
   const long long G = l->G, most = 1ll << 30;
   return G * l->M <= most && G * l->K <= most && G * l->N <= most;
 }
+// A group's weights as the tensor maps take them: int8 [N][P] and 16-bit [K][N]
+// strides below 2^40 bytes.
+bool weights_fit(const rmx_layer& l) { return (long long)q8_pitch(l.K) * ((l.N + 7) / 8 * 8) < (1ll << 39); }
 // Null is allowed; a pointer that is given must be aligned.
 rmx_status check_opt(const void* p) { return p ? check_ptr(p) : RMX_OK; }
 
@@ -143,6 +146,7 @@ rmx_status rmx_rms_norm_backward(const rmx_rows* shape, const void* dn, const vo
 
 rmx_status rmx_weight_q8(const rmx_layer* layer, const void* w, int8_t* q, float* scale, rmx_stream stream) {
   if (!layer_ok(layer)) return RMX_ERR_INVALID_ARG;
+  if (!weights_fit(*layer)) return RMX_ERR_UNSUPPORTED;
   RMX_TRY(check_ptr(w));
   RMX_TRY(check_ptr(q));
   RMX_TRY(check_ptr(scale));
@@ -154,6 +158,7 @@ rmx_status rmx_weight_q8(const rmx_layer* layer, const void* w, int8_t* q, float
 rmx_status rmx_linear_q8(const rmx_layer* layer, const int8_t* a, const float* a_scale, const int8_t* w,
                          const float* w_scale, const void* bias, const void* resid, void* out, rmx_stream stream) {
   if (!layer_ok(layer)) return RMX_ERR_INVALID_ARG;
+  if (!weights_fit(*layer)) return RMX_ERR_UNSUPPORTED;
   if (layer->M == 0) return RMX_OK;
   for (const void* p : {(const void*)a, (const void*)a_scale, (const void*)w, (const void*)w_scale, (const void*)out})
     RMX_TRY(check_ptr(p));
@@ -161,6 +166,7 @@ rmx_status rmx_linear_q8(const rmx_layer* layer, const int8_t* a, const float* a
   RMX_TRY(check_opt(resid));
   const LinearQ8 d{layer->M, layer->G, layer->K, layer->N, q8_pitch(layer->K), layer->dtype, a, w, a_scale, w_scale,
                    bias, resid, out};
+  if (!linear_q8_supported(d)) return RMX_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Launch l("linear_q8", st);
   return l.done(launch_linear_q8(d, device_error_word(), st));
@@ -189,7 +195,7 @@ rmx_status rmx_ckpt8_unpack(const rmx_rows* shape, const int8_t* q, const int8_t
 }
 
 size_t rmx_ckpt8_wgrad_workspace_bytes(const rmx_layer* layer) {
-  if (!layer_ok(layer)) return 0;
+  if (!layer_ok(layer) || !weights_fit(*layer)) return 0;
   return wgrad_ws(*layer).total;
 }
 
@@ -197,6 +203,7 @@ rmx_status rmx_ckpt8_wgrad(const rmx_layer* layer, const int8_t* q, const int8_t
                            void* db, void* ws, size_t ws_bytes, rmx_stream stream) {
   if (!layer_ok(layer)) return RMX_ERR_INVALID_ARG;
   const rmx_layer& l = *layer;
+  if (!weights_fit(l)) return RMX_ERR_UNSUPPORTED;
   RMX_TRY(check_ptr(dw));
   RMX_TRY(check_opt(db));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

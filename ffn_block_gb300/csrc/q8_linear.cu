@@ -674,10 +674,9 @@ int split_of(long long tiles, int nt, int num_raw) {
   return tiles <= 72 && num_raw >= 10 + nt / 10 ? 2 : 1;
 }
 
-}  // namespace
-
-cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t st) {
-  Params p;
+// The sizes, tiles and stages of a product.  False where the kernel's counters
+// would not hold it.
+bool plan(const LinearQ8& d, Params& p, bool& pair) {
   p.M = d.M;
   p.G = d.G;
   p.K = d.K;
@@ -690,7 +689,7 @@ cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t 
   // (pair / alone: 706 x 2 tokens, 2979 -> 214, 17.9 / 11.1; 490 x 5, 2147 -> 357,
   // 16.3 / 13.7; 192 x 8, 256 -> 1024, 7.7 / 5.9).
   const long long alone = (long long)d.G * ((d.N + 127) / 128) * ((d.M + kMaxAlone - 1) / kMaxAlone);
-  const bool pair = d.M > kMaxAlone && d.N > 128 && alone > sm_count();
+  pair = d.M > kMaxAlone && d.N > 128 && alone > sm_count();
   const int most = pair ? kMaxNT : kMaxAlone;
   p.tiles_m = (d.M + most - 1) / most;
   const int even = (d.M + p.tiles_m - 1) / p.tiles_m;
@@ -700,7 +699,7 @@ cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t 
   const int tn = pair ? 256 : 128;
   p.tiles_n = (d.N + tn - 1) / tn;
   const long long tiles = (long long)d.G * p.tiles_n * p.tiles_m;
-  if (tiles > (1ll << 30)) return cudaErrorInvalidValue;
+  if (tiles > (1ll << 30)) return false;
   p.num_tiles = (int)tiles;
   p.num_raw = (d.K + kRawK - 1) / kRawK;  // columns past K are zeros
   p.raw_bytes = 128 * kRawK + p.ntc * kRawK;
@@ -708,8 +707,23 @@ cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t 
   p.raw_stages = (kSmemMax - 1024 - kScaleBytes - kBarBytes - kConv * p.conv_bytes) / p.raw_bytes;
   if (p.raw_stages > kMaxRaw) p.raw_stages = kMaxRaw;
   p.split = pair ? 1 : split_of(tiles, p.nt, p.num_raw);
-  const long long rounds = (tiles + (pair ? sm_count() / 2 : sm_count()) - 1) / (pair ? sm_count() / 2 : sm_count());
-  if (rounds * p.num_raw >= (1ll << 30)) return cudaErrorInvalidValue;  // more than 10^19 operations
+  const int at_once = pair ? sm_count() / 2 : sm_count();
+  const long long rounds = at_once > 0 ? (tiles + at_once - 1) / at_once : tiles;
+  return rounds * p.num_raw < (1ll << 30);  // past that: more than 10^19 operations
+}
+
+}  // namespace
+
+bool linear_q8_supported(const LinearQ8& d) {
+  Params p;
+  bool pair;
+  return plan(d, p, pair);
+}
+
+cudaError_t launch_linear_q8(const LinearQ8& d, unsigned int* err, cudaStream_t st) {
+  Params p;
+  bool pair;
+  if (!plan(d, p, pair)) return cudaErrorInvalidValue;
   // kind::f16, fp16 operands (type 0), fp32 accumulator, both K-major.
   p.idesc = (1u << 4) | ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)((pair ? 256 : 128) >> 4) << 24);
   p.sa = d.sa;

@@ -294,7 +294,10 @@ typedef struct {
 
 /* A per-token linear layer: M samples, G tokens (groups), K inputs, N
  * outputs.  Activations are [M, G, K] and [M, G, N], weights one [K, N] (or
- * its transpose) per group. */
+ * its transpose) per group.  K and N up to 2^20, G up to 65535, and G * M,
+ * G * K and G * N up to 2^30 (else RMX_ERR_INVALID_ARG); weights of 2^39
+ * elements a group, padded, and products of more than about 10^19 operations
+ * are refused (RMX_ERR_UNSUPPORTED) before anything is enqueued. */
 typedef struct {
   int M, G, K, N;
   int dtype; /* storage type of out, bias, resid, dy, dw, db */
