@@ -12,8 +12,10 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("dt,dims", [("bf16", dict(B=256, T=32, D=512, H=1536)), ("f16", dict(B=100, T=40, D=1200, H=2400)),
-                                     ("f32", dict(B=64, T=16, D=256, H=512)), ("tf32", dict(B=64, T=16, D=256, H=512))],
-                         ids=["bf16", "f16", "f32", "tf32"])
+                                     ("f32", dict(B=64, T=16, D=256, H=512)), ("tf32", dict(B=64, T=16, D=256, H=512)),
+                                     # the general form of norm0's backward (T not a multiple of 8, padded rows)
+                                     ("bf16", dict(B=700, T=10, D=1200, H=1800)), ("f16", dict(B=700, T=10, D=630, H=1260))],
+                         ids=["bf16", "f16", "f32", "tf32", "general", "padded"])
 def test_step_beside_other_work(dt, dims):
     shape = I.Shape(dtype=dt, **dims)
     blk = RankMixerDevice(shape, I.make_inputs(shape, seed=11, ln_params="random"))
