@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(W * L < 256 ? 256 : W * L, W * L < 256 ? 2 : 1
       // A row that holds an infinity or a NaN has no scale: NaN, and zeros.
       const bool fine = top < kInfBits;
       float mx = __uint_as_float(top);
-      if (w == 0 && lane == 0) a.scale[row] = fine ? mx / 127.f * rstd : __uint_as_float(0x7fc00000u);
+      if (w == 0 && lane == 0) a.scale[row] = fine ? fminf(mx / 127.f * rstd, kMaxScale) : __uint_as_float(0x7fc00000u);
       if (mx < 0x1p-100f) {
         // Tiny rows are lifted so that 127 / max stays finite.
         mx *= 0x1p100f;
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(256) k_weight_q8(int K, int N, int P, const T*
 #pragma unroll
   for (int i = 0; i < 8; ++i) am = max(am, mx[i][tx]);
   if (ty == 0 && n0 + tx < N)
-    scale[(size_t)g * N + n0 + tx] = am < kInfBits ? __uint_as_float(am) / 127.f : __uint_as_float(0x7fc00000u);
+    scale[(size_t)g * N + n0 + tx] = am < kInfBits ? fminf(__uint_as_float(am) / 127.f, kMaxScale) : __uint_as_float(0x7fc00000u);
   const bool fine = am < kInfBits;
   const float lift = __uint_as_float(am) < 0x1p-100f ? 0x1p100f : 1.f;
   const float mul = am && fine ? 127.f / (__uint_as_float(am) * lift) : 0.f;

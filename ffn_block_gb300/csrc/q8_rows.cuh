@@ -107,6 +107,9 @@ template <int L, bool VEC> __device__ __forceinline__ uint2 load_bytes(const int
     if (col<L, VEC>(c0, i) < P) w[i / 4] |= (uint32_t)(uint8_t)row[col<L, VEC>(c0, i)] << (8 * (i & 3));
   return make_uint2(w[0], w[1]);
 }
+// The largest scale of 127 steps: 127 times it is still finite (1 / 127 of the
+// largest float32, rounded, is one unit too much).
+constexpr float kMaxScale = 0x1.020406p+121f;
 // Eight int8 as floats 2^23 + 128 + q: byte ^ 0x80 in the low mantissa byte of
 // 2^23.  Subtracting kBias is exact.
 constexpr float kBias = 8388736.0f;  // 2^23 + 128
