@@ -11,6 +11,8 @@
 // written 86 us, 6.3 TB/s to HBM, 94% of the measured copy rate; read back
 // 36 us; a checkpoint of it packed in 34 us and read back in 37 (6 TB/s).
 
+#include <float.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -93,9 +95,12 @@ __global__ void __launch_bounds__(W * L < 256 ? 256 : W * L, W * L < 256 ? 2 : 1
       }
     }
     if (a.q) {
-      // A row that holds an infinity or a NaN has no scale: NaN, and zeros.
-      const bool fine = top < kInfBits;
+      // A row that holds an infinity or a NaN has no scale: NaN, and zeros.  Its
+      // largest value is mx * rstd: rstd is infinite where the squares' mean
+      // (and eps) is zero, and zero where it is past float32.
       float mx = __uint_as_float(top);
+      const float largest = mx * rstd;
+      const bool fine = fabsf(largest) <= FLT_MAX;
       if (w == 0 && lane == 0) a.scale[row] = fine ? fminf(mx / 127.f * rstd, kMaxScale) : __uint_as_float(0x7fc00000u);
       if (mx < 0x1p-100f) {
         // Tiny rows are lifted so that 127 / max stays finite.
@@ -105,7 +110,7 @@ __global__ void __launch_bounds__(W * L < 256 ? 256 : W * L, W * L < 256 ? 2 : 1
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], f2(0x1p100f));
       }
-      const float mul = mx > 0.f ? 127.f / mx : 0.f;
+      const float mul = largest > 0.f ? 127.f / mx : 0.f;
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         float2 t[4];

@@ -307,12 +307,15 @@ typedef struct {
 int rmx_q8_pitch(int cols);
 
 /* RMS norm with the residual's addition and an 8-bit output:
- *   h = x + r;  rstd = 1 / sqrt(mean(h^2) + eps);  n = h * rstd * gamma
+ *   h = x + r;  rstd = 1 / sqrt(mean(h^2) + eps);  n = h * gamma * rstd
  * x [rows, cols]; r (may be null) likewise; gamma [cols].  The sum, the
  * statistics and n are float32; the norm is taken of the unrounded sum.
  * Outputs: h [rows, cols] (null: not written), y = n in the storage type
  * (null: not written), q and scale = n as q8 rows (both null: not written),
  * rstd [rows] float32 (null: not written).  y or q must be given.
+ * n is formed as (h * gamma) * rstd.  Where the mean square passes float32's
+ * range, rstd is 0 and so is n (NaN where h * gamma passes it too); where it is
+ * 0 and eps too, rstd is infinite and n infinite or NaN.
  * h may be x or r itself; nothing else may overlap.  cols <= 16384. */
 rmx_status rmx_rms_norm_q8(const rmx_rows* shape, float eps, const void* x, const void* r, const void* gamma,
                            void* h, void* y, int8_t* q, float* scale, float* rstd, rmx_stream stream);
