@@ -2,15 +2,15 @@
 //   out[m,g,n] = (sum_k a[m,g,k] * w[g,n,k]) * sa[m,g] * sw[g,n] + bias[g,n] + resid[m,g,n]
 //
 // The integers run on the 16-bit floating tensor cores: an int8 is exact in
-// fp16, a product of two is exact in the fp32 accumulator and so is every sum
-// below 2^24.  (sm_103a has no fast integer tensor path.)  The operands stay
-// 8 bits wide up to the SM: TMA brings int8 tiles into shared memory, and two
-// groups of warps turn them into fp16 there, the weights into tensor memory
-// (the MMA's A operand) and the tokens into swizzled shared memory (its B
-// operand).  An output tile is channels x tokens, so that few tokens are a
-// narrow tile, not a padded one: 128 channels a CTA (256 a CTA pair) by up to
-// 192 tokens.  The bound is the tensor rate from about 150 tokens on, the
-// stream of the weights below.
+// fp16, a product of two is exact in the fp32 accumulator and so is the sum
+// while no partial sum passes 2^24.  (sm_103a has no fast integer tensor path.)
+// The operands stay 8 bits wide up to the SM: TMA brings int8 tiles into shared
+// memory, and two groups of warps turn them into fp16 there, the weights into
+// tensor memory (the MMA's A operand) and the tokens into swizzled shared
+// memory (its B operand).  An output tile is channels x tokens, so that few
+// tokens are a narrow tile, not a padded one: 128 channels a CTA (256 a CTA
+// pair) by up to 192 tokens.  The bound is the tensor rate from about 150
+// tokens on, the stream of the weights below.
 //
 // Roles (31 warps, one CTA per SM, persistent over tiles):
 //   warp 0       TMA producer: 128 k of the CTA's channels and tokens a stage

@@ -353,9 +353,12 @@ rmx_status rmx_weight_q8(const rmx_layer* layer, const void* w, int8_t* q, float
  * a [M, G, P] and w [G, N, P] int8 in [-128, 127] with P = rmx_q8_pitch(K) and
  * zero columns K .. P-1 (those of one operand suffice); a_scale [M, G] and
  * w_scale [G, N] float32; bias [G, N] and resid, out [M, G, N] in the storage
- * type (bias, resid may be null; out may be resid itself).  The integer sum
- * is exact below 2^24 in magnitude; larger ones may round to the 24 bits of
- * float32.  The rest is float32, rounded once. */
+ * type (bias, resid may be null; out may be resid itself). The integer sum
+ * is exact while every partial sum stays within 2^24 in magnitude, as it does
+ * for K <= 1024 whatever the values.  Beyond, each 16 columns may round the sum
+ * so far to 24 bits: it is off by at most about K / 16 * 2^-23 of the largest
+ * partial sum, also where the terms cancel and the result is small.  The rest is
+ * float32, rounded once. */
 rmx_status rmx_linear_q8(const rmx_layer* layer, const int8_t* a, const float* a_scale, const int8_t* w,
                          const float* w_scale, const void* bias, const void* resid, void* out, rmx_stream stream);
 
