@@ -136,12 +136,12 @@ struct WaitCtx {
 // How the CTAs of a pair hand data over.  One CTA's warps arrive on a barrier
 // of the other at cluster scope, relaxed.  What they wrote to or read from TMEM
 // is ordered by the tcgen05 fences on both sides (TENSOR); what they wrote to
-// their shared memory by a release fence before the arrival, restricted to
-// shared memory, and a wait that acquires at cluster scope (MEMORY).  An
-// arrival that itself releases at cluster scope waits for all writes of its
-// thread, global ones too, about 1000 cycles: with one thread of the odd CTA
-// passing its warps' arrivals on in that way, 1024 x 64 tokens 1280 -> 5120
-// take 1212 us, in this way 620 to 680 (as the power limit allows).
+// their shared memory by a release fence before the arrival and an acquire
+// fence after the wait (MEMORY), both restricted to shared memory.  An arrival
+// that itself releases at cluster scope waits for all writes of its thread,
+// global ones too, about 1000 cycles: with one thread of the odd CTA passing its
+// warps' arrivals on in that way, 1024 x 64 tokens 1280 -> 5120 take 1212 us, in
+// this way 679 (693 with waits that acquire by themselves).
 enum Order { LOCAL, TENSOR, MEMORY };
 // Arrival by the lanes with pred set (one of a converged warp), on a barrier of
 // this CTA (LOCAL) or of the cluster.
@@ -158,11 +158,7 @@ template <Order O> __device__ __forceinline__ void arrive_if(uint32_t bar, bool 
         "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar), "r"((uint32_t)pred)
         : "memory");
 }
-// One look at a barrier of this CTA on which LOCAL threads and copies arrive, or
-// the pair's other CTA and the issuer's commits too.
-template <Order O> __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) {
-  if (O == LOCAL) return mbar_try_wait(bar, parity);
-  if (O == MEMORY) return mbar_try_wait_cluster(bar, parity);
+__device__ __forceinline__ bool try_wait_relaxed_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -173,6 +169,15 @@ template <Order O> __device__ __forceinline__ bool look(uint32_t bar, uint32_t p
       : "memory");
   return ok != 0;
 }
+// One look at a barrier of this CTA on which LOCAL threads and copies arrive, or
+// the pair's other CTA and the issuer's commits too.
+template <Order O> __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) {
+  return O == LOCAL ? mbar_try_wait(bar, parity) : try_wait_relaxed_cluster(bar, parity);
+}
+// What follows a look that succeeded.
+template <Order O> __device__ __forceinline__ void seen() {
+  if (O == MEMORY) asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
 // The rest of a bounded wait, out of line: it spins, now and then looking at
 // the clock and at whether another warp has given up.
 template <Order O>
@@ -181,7 +186,10 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, unsigned int
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     for (int i = 0; i < 1024; ++i)
-      if (look<O>(bar, parity)) return true;
+      if (look<O>(bar, parity)) {
+        seen<O>();
+        return true;
+      }
     if (*abort) return false;
     if (globaltimer_ns() - t0 > limit_ns) {
       atomicOr(err, bit);
@@ -194,7 +202,10 @@ template <Order O>
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t ph, unsigned int bit, const WaitCtx& w) {
 #pragma unroll 1
   for (int i = 0; i < 512; ++i)
-    if (look<O>(bar, ph)) return true;
+    if (look<O>(bar, ph)) {
+      seen<O>();
+      return true;
+    }
   return wait_on<O>(bar, ph, bit, w.limit_ns, w.err, w.abort);
 }
 // The same by a whole warp, which goes on or gives up together.
@@ -202,7 +213,10 @@ template <Order O>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t ph, unsigned int bit, const WaitCtx& w) {
 #pragma unroll 1
   for (int i = 0; i < 512; ++i)
-    if (__all_sync(0xffffffffu, look<O>(bar, ph))) return true;
+    if (__all_sync(0xffffffffu, look<O>(bar, ph))) {
+      seen<O>();
+      return true;
+    }
   return __all_sync(0xffffffffu, wait_on<O>(bar, ph, bit, w.limit_ns, w.err, w.abort));
 }
 
@@ -233,10 +247,12 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
   // A raw stage that has been read.  The copy that fills it again is of the
   // async proxy: only a proxy fence orders the warp's reads before its writes.
   // (Without it a read that had been issued, but waited behind the epilogue's
-  // stores, returned the next contents.)  As soon as the reads are issued for
-  // CTAs alone, after the conversion for pairs, where the fence's wait costs
-  // more than the stage (the other way round: one sample 1280 -> 5120 73.0 /
-  // 74.3 us, 1024 x 16 157 / 161, 1000 x 40 3600 -> 1200 262 / 271).
+  // stores, returned the next contents.)  CTAs alone give it back as soon as the
+  // reads are issued (one sample 1280 -> 5120 73.0 us, after the conversion
+  // 74.3); a pair's weights after the conversion and its tokens after their
+  // stores, with the fence that these need anyway, since there the fences cost
+  // more than the stage (1024 x 64 1280 -> 5120 678 us, both after the
+  // conversion 686; 1024 x 16 156 us, at once 161).
   auto hand_back = [&](uint32_t bar) {
     fence_proxy_async_smem();
     __syncwarp();
@@ -265,7 +281,7 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
         widen(w.z, q[12], q[13]);
         widen(w.w, q[14], q[15]);
       }
-      if (PAIR) hand_back(rbar + 8u * kMaxRaw);
+      if (PAIR && WEIGHTS) hand_back(rbar + 8u * kMaxRaw);
       // The half whose MMAs free this place: six back (this conv stage, the
       // lap before), or three (the other one of this set).
       constexpr bool kThree = WEIGHTS && W == 3;
@@ -287,6 +303,7 @@ __device__ __forceinline__ void convert(int set, int row, bool live, int halves,
       }
       __syncwarp();
       arrive_if<ORDER>(cfull + (j ? 8u * kSets : 0u), one);
+      if (PAIR && !WEIGHTS) arrive_if<LOCAL>(rbar + 8u * kMaxRaw, one);
       if (j) lap ^= 1u;
       // Three halves on: one raw stage and a half.
       const int adv = ((set + j) & 1) ? 2 : 1;
