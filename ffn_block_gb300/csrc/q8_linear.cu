@@ -31,15 +31,18 @@
 // sum over k what it is.
 //
 // Measured (GB300; us for one call among others): 1024 samples x 64 tokens
-// through 1280 -> 5120 590 us (1460 TFLOP/s, 76% of the measured cuBLAS bf16
-// rate; 640 us where the board is held at its power limit), 1000 x 40 through
-// 3600 -> 1200 240 us, one sample x 64 tokens through 1280 -> 5120 73 us
-// (5.8 TB/s, 87% of the measured copy rate).  What bounds the large products
-// is the SM's instruction issue: a step of 64 k of a 256 x 176 tile takes the
-// tensor cores 352 cycles, and about 1440 instructions (560 of them the
-// conversion itself, 260 the epilogue) at an IPC of 2.6.  With an epilogue of
-// 4 warps or tiles of 208 tokens the epilogue bounds it instead; outputs
-// through shared memory and TMA cost more instructions than they save.
+// through 1280 -> 5120 664 us (1290 TFLOP/s, 67% of the measured cuBLAS bf16
+// rate; 620 in short runs, 700 where the board is held at its power limit),
+// 1000 x 40 through 3600 -> 1200 279 us, one sample x 64 tokens through 1280 ->
+// 5120 73 us (5.8 TB/s, 87% of the measured copy rate).  The library's 16-bit
+// products of these sizes take 467, 231 and 118 us: this one is for few tokens
+// and for weights and activations that are 8 bits wide already.  What bounds the
+// large products is the SM's instruction issue: a step of 64 k of a 256 x 176
+// tile takes the tensor cores 352 cycles, and about 1440 instructions (560 of
+// them the conversion itself, 260 the epilogue) at an IPC of 2.6, and the fences
+// and waits of the hand-over between a pair's CTAs.  With an epilogue of 4 warps
+// or tiles of 208 tokens the epilogue bounds it instead; outputs through shared
+// memory and TMA cost more instructions than they save.
 
 #include <cuda.h>
 
@@ -701,10 +704,10 @@ bool plan(const LinearQ8& d, Params& p, bool& pair) {
   // A CTA alone up to 96 tokens (what three warps convert), a pair above: the
   // pair shares the tokens' conversion, which a CTA alone would do for all of
   // them.  16 groups of 1280 -> 5120, us alone / as a pair: 64 tokens 29.5 /
-  // 30.0, 96 31.9 / 32.7, 97 47 / 33.7, 192 50 / 36, 1024 231 / 151.  But alone
+  // 30.0, 96 33.0 / 33.8, 97 47 / 34.6, 192 52 / 39, 1024 242 / 158.  But alone
   // while there is an SM for every tile: they are narrower, and can be shared
-  // (pair / alone: 706 x 2 tokens, 2979 -> 214, 17.9 / 11.1; 490 x 5, 2147 -> 357,
-  // 16.3 / 13.7; 192 x 8, 256 -> 1024, 7.7 / 5.9).
+  // (pair / alone: 706 x 2 tokens, 2979 -> 214, 18.3 / 10.7; 490 x 5, 2147 -> 357,
+  // 14.9 / 12.7; 192 x 8, 256 -> 1024, 7.4 / 5.4).
   const long long alone = (long long)d.G * ((d.N + 127) / 128) * ((d.M + kMaxAlone - 1) / kMaxAlone);
   pair = d.M > kMaxAlone && d.N > 128 && alone > sm_count();
   const int most = pair ? kMaxNT : kMaxAlone;

@@ -178,10 +178,14 @@ __global__ void __maxnreg__(NCH == 1 ? kRegs : 128) k_rows_bwd(const RowsBwd a, 
 }
 
 // How rows are spread: L lanes of W warps a row, NCH blocks of 8 * L columns
-// each, rpb rows a thread block (eight to ten warps).  Short rows take part of a
-// warp: 1,000,000 rows of 40 columns 296 us with a warp a row, 100 with 8 lanes.
-// One block a warp where 16 warps hold the row: 65536 x 1280 in 211 us with a
-// warp a row, 122 with five.
+// each, rpb rows a thread block: as many as ten warps hold, eight of one warp,
+// one where a row takes six warps or more.  Short rows take part of a warp:
+// 1,000,000 rows of 40 columns 296 us with a warp a row, 100 with 8 lanes.  One
+// block a warp where 16 warps hold the row: 65536 x 1280 in 211 us with a warp a
+// row, 122 with five.  Five warps a row fill an SM best (two rows a block, 30
+// warps); with one row a block and at most three blocks an SM, six and seven
+// warps a row leave it 18 and 21: of as many elements, with dh, rows of 1280
+// columns take 123 us, 1288 204, 1536 176, 1792 163, 2048 151, 2304 139, 2560 135.
 struct Spread {
   int L, W, nch, rpb, threads;
 };

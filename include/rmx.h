@@ -394,6 +394,8 @@ typedef struct {
 
 /* Forward pass for serving: rmx_forward with both contractions in int8 (their
  * inputs out1 and hidden quantised per sample and token) and nothing saved.
+ * Faster than rmx_forward where the weights' bytes bound it, at few samples,
+ * and slower at many.
  * params->w1 and params->wout are not read and may be null.  ws: scratch of
  * rmx_forward_q8_workspace_bytes.  x and y may not alias. */
 size_t rmx_forward_q8_workspace_bytes(const rmx_config* cfg);
