@@ -73,6 +73,22 @@ class rmx_q8_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "w1_scale", "wout", "wout_scale")]
 
 
+class rmx_drop(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("state", ctypes.c_void_p)]
+
+
+class rmx_routes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("tokens", "k", "experts", "cols", "dtype")]
+
+
+class rmx_groups(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("M", "G", "C", "dtype", "order")]
+
+
+class rmx_layer_f8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("M", "G", "K", "N", "dtype", "a_format", "b_format")]
+
+
 _VP, _SZ, _I, _P = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.POINTER
 _SIGNATURES = {
     "rmx_saved_bytes": (_SZ, [_P(rmx_config)]),
@@ -113,6 +129,24 @@ _SIGNATURES = {
     "rmx_saved8_bytes": (_SZ, [_P(rmx_config)]),
     "rmx_saved_pack8": (_I, [_P(rmx_config), _VP, _SZ, _VP, _SZ, _VP]),
     "rmx_saved_unpack8": (_I, [_P(rmx_config), _VP, _SZ, _VP, _SZ, _VP]),
+    "rmx_dropout": (_I, [_P(rmx_rows), _P(rmx_drop)] + [_VP] * 4),
+    "rmx_layer_norm": (_I, [_P(rmx_rows), ctypes.c_float, _P(rmx_drop)] + [_VP] * 9),
+    "rmx_layer_norm_backward_workspace_bytes": (_SZ, [_P(rmx_rows)]),
+    "rmx_layer_norm_backward": (_I, [_P(rmx_rows), _P(rmx_drop)] + [_VP] * 11 + [_SZ, _VP]),
+    "rmx_expert_sort_workspace_bytes": (_SZ, [_P(rmx_routes)]),
+    "rmx_expert_sort": (_I, [_P(rmx_routes)] + [_VP] * 5 + [_SZ, _VP]),
+    "rmx_expert_gather": (_I, [_P(rmx_routes)] + [_VP] * 3 + [_I] + [_VP] * 3),
+    "rmx_expert_combine": (_I, [_P(rmx_routes)] + [_VP] * 5),
+    "rmx_expert_combine_backward": (_I, [_P(rmx_routes)] + [_VP] * 7),
+    "rmx_f8_pitch": (_I, [_I]),
+    "rmx_f8_exps": (_I, [_I]),
+    "rmx_f8_ragged_pitch": (_I, [_I, _I]),
+    "rmx_quant_f8": (_I, [_P(rmx_rows), _I] + [_VP] * 4),
+    "rmx_dequant_f8": (_I, [_P(rmx_rows), _I] + [_VP] * 4),
+    "rmx_quant_f8_groups_workspace_bytes": (_SZ, [_P(rmx_groups)]),
+    "rmx_quant_f8_groups": (_I, [_P(rmx_groups), _I] + [_VP] * 8 + [_SZ, _VP]),
+    "rmx_linear_f8": (_I, [_P(rmx_layer_f8)] + [_VP] * 9),
+    "rmx_wgrad_f8": (_I, [_P(rmx_layer_f8)] + [_VP] * 7),
 }
 
 _lib = None
@@ -363,3 +397,121 @@ def rmx_saved_pack8(cfg, saved, saved_bytes: int, saved8, saved8_bytes: int, str
 def rmx_saved_unpack8(cfg, saved8, saved8_bytes: int, saved, saved_bytes: int, stream=None) -> int:
     return lib().rmx_saved_unpack8(ctypes.byref(cfg), _ptr(saved8), saved8_bytes, _ptr(saved), saved_bytes,
                                    _stream(stream))
+
+
+# ------------------------------------------------------------------ a sparse layer between blocks
+
+F8_CODES = {"e4m3": 0, "e5m2": 1}
+ORDER_CODES = {"tokens": 0, "groups": 1, "ragged": 2}
+
+
+def _f8(fmt: str | int) -> int:
+    return F8_CODES[fmt] if isinstance(fmt, str) else int(fmt)
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def make_drop(p: float, state=None) -> rmx_drop:
+    """Dropout with probability p; state: device memory of {seed, offset}, 64 bits each (a tensor is kept alive)."""
+    d = rmx_drop(p, _ptr(state))
+    d.tensor = state
+    return d
+
+
+def make_routes(tokens: int, k: int, experts: int, cols: int, dtype: str | int) -> rmx_routes:
+    return rmx_routes(tokens, k, experts, cols, _code(dtype))
+
+
+def make_groups(M: int, G: int, C: int, dtype: str | int, order: str | int) -> rmx_groups:
+    return rmx_groups(M, G, C, _code(dtype), ORDER_CODES[order] if isinstance(order, str) else int(order))
+
+
+def make_layer_f8(M: int, G: int, K: int, N: int, dtype: str | int, a_format: str | int = "e4m3",
+                  b_format: str | int = "e4m3") -> rmx_layer_f8:
+    return rmx_layer_f8(M, G, K, N, _code(dtype), _f8(a_format), _f8(b_format))
+
+
+def rmx_dropout(shape: rmx_rows, drop, x, r, out, stream=None) -> int:
+    return lib().rmx_dropout(ctypes.byref(shape), _ref(drop), _ptr(x), _ptr(r), _ptr(out), _stream(stream))
+
+
+def rmx_layer_norm(shape: rmx_rows, eps: float, drop, x, r, gamma, beta, h, y, mean, rstd, stream=None) -> int:
+    return lib().rmx_layer_norm(ctypes.byref(shape), eps, _ref(drop), _ptr(x), _ptr(r), _ptr(gamma), _ptr(beta),
+                                _ptr(h), _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream))
+
+
+def rmx_layer_norm_backward_workspace_bytes(shape: rmx_rows) -> int:
+    return lib().rmx_layer_norm_backward_workspace_bytes(ctypes.byref(shape))
+
+
+def rmx_layer_norm_backward(shape: rmx_rows, drop, dy, dh, h, mean, rstd, gamma, dr, dx, dgamma, dbeta, ws,
+                            ws_bytes: int, stream=None) -> int:
+    return lib().rmx_layer_norm_backward(ctypes.byref(shape), _ref(drop), _ptr(dy), _ptr(dh), _ptr(h), _ptr(mean),
+                                         _ptr(rstd), _ptr(gamma), _ptr(dr), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
+                                         _ptr(ws), ws_bytes, _stream(stream))
+
+
+def rmx_expert_sort_workspace_bytes(routes: rmx_routes) -> int:
+    return lib().rmx_expert_sort_workspace_bytes(ctypes.byref(routes))
+
+
+def rmx_expert_sort(routes: rmx_routes, expert, offsets, position, source, ws, ws_bytes: int, stream=None) -> int:
+    return lib().rmx_expert_sort(ctypes.byref(routes), _ptr(expert), _ptr(offsets), _ptr(position), _ptr(source),
+                                 _ptr(ws), ws_bytes, _stream(stream))
+
+
+def rmx_expert_gather(routes: rmx_routes, source, x, out, fmt="e4m3", q=None, exps=None, stream=None) -> int:
+    return lib().rmx_expert_gather(ctypes.byref(routes), _ptr(source), _ptr(x), _ptr(out), _f8(fmt), _ptr(q),
+                                   _ptr(exps), _stream(stream))
+
+
+def rmx_expert_combine(routes: rmx_routes, position, weight, y, out, stream=None) -> int:
+    return lib().rmx_expert_combine(ctypes.byref(routes), _ptr(position), _ptr(weight), _ptr(y), _ptr(out),
+                                    _stream(stream))
+
+
+def rmx_expert_combine_backward(routes: rmx_routes, position, weight, dout, y, dy, dweight, stream=None) -> int:
+    return lib().rmx_expert_combine_backward(ctypes.byref(routes), _ptr(position), _ptr(weight), _ptr(dout), _ptr(y),
+                                             _ptr(dy), _ptr(dweight), _stream(stream))
+
+
+def rmx_f8_pitch(cols: int) -> int:
+    return lib().rmx_f8_pitch(cols)
+
+
+def rmx_f8_exps(cols: int) -> int:
+    return lib().rmx_f8_exps(cols)
+
+
+def rmx_f8_ragged_pitch(rows: int, groups: int) -> int:
+    return lib().rmx_f8_ragged_pitch(rows, groups)
+
+
+def rmx_quant_f8(shape: rmx_rows, fmt, x, q, exps, stream=None) -> int:
+    return lib().rmx_quant_f8(ctypes.byref(shape), _f8(fmt), _ptr(x), _ptr(q), _ptr(exps), _stream(stream))
+
+
+def rmx_dequant_f8(shape: rmx_rows, fmt, q, exps, x, stream=None) -> int:
+    return lib().rmx_dequant_f8(ctypes.byref(shape), _f8(fmt), _ptr(q), _ptr(exps), _ptr(x), _stream(stream))
+
+
+def rmx_quant_f8_groups_workspace_bytes(groups: rmx_groups) -> int:
+    return lib().rmx_quant_f8_groups_workspace_bytes(ctypes.byref(groups))
+
+
+def rmx_quant_f8_groups(groups: rmx_groups, fmt, offsets, x, q, exps, qt, exps_t, sums, ws, ws_bytes: int,
+                        stream=None) -> int:
+    return lib().rmx_quant_f8_groups(ctypes.byref(groups), _f8(fmt), _ptr(offsets), _ptr(x), _ptr(q), _ptr(exps),
+                                     _ptr(qt), _ptr(exps_t), _ptr(sums), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def rmx_linear_f8(layer: rmx_layer_f8, offsets, a, a_exps, w, w_exps, bias, resid, out, stream=None) -> int:
+    return lib().rmx_linear_f8(ctypes.byref(layer), _ptr(offsets), _ptr(a), _ptr(a_exps), _ptr(w), _ptr(w_exps),
+                               _ptr(bias), _ptr(resid), _ptr(out), _stream(stream))
+
+
+def rmx_wgrad_f8(layer: rmx_layer_f8, offsets, at, at_exps, bt, bt_exps, dw, stream=None) -> int:
+    return lib().rmx_wgrad_f8(ctypes.byref(layer), _ptr(offsets), _ptr(at), _ptr(at_exps), _ptr(bt), _ptr(bt_exps),
+                              _ptr(dw), _stream(stream))

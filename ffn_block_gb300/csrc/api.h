@@ -30,6 +30,18 @@ class Launch {
 
 bool aligned16(const void* p);
 rmx_status check_ptr(const void* p);  // non-null and 16-byte aligned
+// Null is allowed; a pointer that is given must be aligned.
+inline rmx_status check_opt(const void* p) { return p ? check_ptr(p) : RMX_OK; }
+
+// ---- operators on dense rows of a storage type
+inline bool storage_ok(int dtype) { return dtype == RMX_F32 || dtype == RMX_BF16 || dtype == RMX_F16; }
+inline size_t storage_bytes(int dtype) { return dtype == RMX_F32 ? 4 : 2; }
+// Rows and columns small enough that every byte offset fits 62 bits and every
+// row index of a chunked pass 40.
+inline bool rows_ok(const rmx_rows* s) {
+  return s && s->rows >= 0 && s->rows <= (1ll << 36) && s->cols >= 1 && s->cols <= (1 << 24) && storage_ok(s->dtype);
+}
+inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // One grouped GEMM under a profile name: tensor cores where the contract and
 // the shape allow, CUDA cores otherwise.

@@ -1,0 +1,446 @@
+// Routing rows to experts: slots sorted by expert, rows gathered in that order,
+// experts' rows added up at their tokens, and the backward of that.
+//
+// The sort counts.  A warp takes its slots in order, 32 at a time: lanes with
+// the same expert find one another (match), so a slot's place among them is a
+// population count, and the first of them moves the warp's own counter on.  No
+// atomics: the order is the slots' own.  Few slots are sorted by one CTA in one
+// launch; many by three: each warp counts its share, each expert's counts are
+// summed over the warps, and each warp places its share.
+
+#include "common.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "q8_rows.cuh"
+#include "sparse.h"
+
+namespace rmx {
+namespace {
+
+__device__ __forceinline__ uint32_t lanes_below() {
+  uint32_t m;
+  asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));
+  return m;
+}
+__device__ __forceinline__ int expert_of(const int32_t* expert, long long slot, long long end, int E) {
+  const int e = slot < end ? expert[slot] : -1;
+  return (uint32_t)e < (uint32_t)E ? e : -1;
+}
+// Slots [begin, end) of a warp (32 at a time, all lanes together) counted into
+// its own hist[E].
+__device__ __forceinline__ void count_slots(const int32_t* expert, long long begin, long long end, int E, int* hist) {
+  const int lane = threadIdx.x & 31;
+  for (long long s = begin; s < end; s += 32) {
+    const int e = expert_of(expert, s + lane, end, E);
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && (same & lanes_below()) == 0) hist[e] += __popc(same);
+    __syncwarp();
+  }
+}
+// The same slots given their places: hist[e] is the warp's next place of expert e.
+__device__ __forceinline__ void place_slots(const int32_t* expert, long long begin, long long end, int E, int* hist,
+                                            int32_t* position, int32_t* source) {
+  const int lane = threadIdx.x & 31;
+  for (long long s = begin; s < end; s += 32) {
+    const long long slot = s + lane;
+    const int e = expert_of(expert, slot, end, E);
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    const uint32_t below = same & lanes_below();
+    const int first = e >= 0 ? hist[e] : 0;
+    __syncwarp();
+    if (e >= 0 && below == 0) hist[e] = first + __popc(same);
+    __syncwarp();
+    if (slot < end) {
+      const int at = e >= 0 ? first + __popc(below) : -1;
+      position[slot] = at;
+      if (e >= 0) source[at] = (int32_t)slot;
+    }
+  }
+}
+// Exclusive prefix over the block's threads of v; `total` gets the sum.  tmp: 33
+// ints.  blockDim.x is a multiple of 32.
+__device__ __forceinline__ int block_prefix(int v, int* tmp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) tmp[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    const int mine = lane < warps ? tmp[lane] : 0;
+    int s = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane < warps) tmp[lane] = s - mine;
+    if (lane == 31) tmp[32] = s;
+  }
+  __syncthreads();
+  total = tmp[32];
+  return tmp[warp] + inc - v;
+}
+
+constexpr int kOneWarps = 32;
+constexpr int kOneSlots = 8192;  // up to here one CTA sorts by itself
+
+__global__ void __launch_bounds__(32 * kOneWarps) k_sort_one(int S, int E, const int32_t* expert, int32_t* offsets,
+                                                             int32_t* position, int32_t* source) {
+  pdl_enter();
+  extern __shared__ int hist[];  // [warps][E]
+  __shared__ int tmp[33];
+  const int warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < kOneWarps * E; i += 32 * kOneWarps) hist[i] = 0;
+  __syncthreads();
+  const int share = ((S + kOneWarps - 1) / kOneWarps + 31) / 32 * 32;
+  const int begin = min(S, warp * share), end = min(S, begin + share);
+  count_slots(expert, begin, end, E, hist + warp * E);
+  __syncthreads();
+  int n = 0;
+  const int e = threadIdx.x;  // E <= 1024 threads
+  if (e < E)
+    for (int w = 0; w < kOneWarps; ++w) {
+      const int c = hist[w * E + e];
+      hist[w * E + e] = n;
+      n += c;
+    }
+  int total;
+  const int off = block_prefix(n, tmp, total);
+  if (e < E) {
+    offsets[e] = off;
+    for (int w = 0; w < kOneWarps; ++w) hist[w * E + e] += off;
+  }
+  if (threadIdx.x == 0) offsets[E] = total;
+  __syncthreads();
+  place_slots(expert, begin, end, E, hist + warp * E, position, source);
+  for (int i = total + threadIdx.x; i < S; i += 32 * kOneWarps) source[i] = -1;
+}
+
+// ws: counts [warps][E], then totals [E].
+constexpr int kManyWarps = 8;
+__global__ void __launch_bounds__(32 * kManyWarps) k_sort_count(int S, int E, int share, int warps, const int32_t* expert,
+                                                                int32_t* counts) {
+  pdl_enter();
+  extern __shared__ int hist[];
+  const int warp = threadIdx.x >> 5, gw = blockIdx.x * kManyWarps + warp;
+  for (int i = threadIdx.x; i < kManyWarps * E; i += 32 * kManyWarps) hist[i] = 0;
+  __syncthreads();
+  const long long begin = min((long long)S, (long long)gw * share), end = min((long long)S, begin + share);
+  count_slots(expert, begin, end, E, hist + warp * E);
+  __syncthreads();
+  const int rows = min(kManyWarps, warps - (int)blockIdx.x * kManyWarps);
+  int32_t* out = counts + (size_t)blockIdx.x * kManyWarps * E;
+  for (int i = threadIdx.x; i < rows * E; i += 32 * kManyWarps) out[i] = hist[i];
+}
+// counts become, per expert, the sums over the warps before; a CTA takes 32
+// experts, a warp of it a range of the rows.
+__global__ void __launch_bounds__(1024) k_sort_scan(int E, int warps, int32_t* counts, int32_t* totals) {
+  pdl_enter();
+  __shared__ int sums[32][33];
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+  const int share = (warps + 31) / 32, begin = min(warps, part * share), end = min(warps, begin + share);
+  int n = 0;
+  if (e < E)
+    for (int w = begin; w < end; ++w) n += counts[(size_t)w * E + e];
+  sums[part][lane] = n;
+  __syncthreads();
+  int before = 0;
+  for (int p = 0; p < part; ++p) before += sums[p][lane];
+  if (e < E) {
+    if (part == 31) totals[e] = before + n;
+    for (int w = begin; w < end; ++w) {
+      const int c = counts[(size_t)w * E + e];
+      counts[(size_t)w * E + e] = before;
+      before += c;
+    }
+  }
+}
+__global__ void __launch_bounds__(32 * kManyWarps) k_sort_place(int S, int E, int share, int warps, const int32_t* expert,
+                                                                const int32_t* counts, const int32_t* totals,
+                                                                int32_t* offsets, int32_t* position, int32_t* source) {
+  pdl_enter();
+  extern __shared__ int hist[];  // [8][E], then offsets [E]
+  __shared__ int tmp[33];
+  int* off = hist + kManyWarps * E;
+  int run = 0;
+  for (int e0 = 0; e0 < E; e0 += 32 * kManyWarps) {
+    const int e = e0 + threadIdx.x;
+    int total;
+    const int before = block_prefix(e < E ? totals[e] : 0, tmp, total);
+    if (e < E) off[e] = run + before;
+    run += total;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e < E; e += 32 * kManyWarps) offsets[e] = off[e];
+    if (threadIdx.x == 0) offsets[E] = run;
+  }
+  const int rows = min(kManyWarps, warps - (int)blockIdx.x * kManyWarps);
+  const int32_t* in = counts + (size_t)blockIdx.x * kManyWarps * E;
+  for (int i = threadIdx.x; i < rows * E; i += 32 * kManyWarps) hist[i] = in[i] + off[i % E];
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, gw = blockIdx.x * kManyWarps + warp;
+  const long long begin = min((long long)S, (long long)gw * share), end = min((long long)S, begin + share);
+  if (begin < end) place_slots(expert, begin, end, E, hist + warp * E, position, source);
+  for (long long i = run + (long long)blockIdx.x * blockDim.x + threadIdx.x; i < S; i += (long long)gridDim.x * blockDim.x)
+    source[i] = -1;
+}
+// A warp's share of the slots: 512, or what keeps the warps at 4096.
+int share_of(int S) {
+  const int least = (int)(((long long)S + 4095) / 4096);
+  return least <= 512 ? 512 : (least + 31) / 32 * 32;
+}
+
+// ---------------------------------------------------------------- rows
+// A unit is a block of 8 * L columns of a row.
+struct Units {
+  int bpr;
+  long long total;
+};
+template <int L> Units units_of(long long rows, int C) {
+  Units u;
+  u.bpr = (C + 8 * L - 1) / (8 * L);
+  u.total = rows * u.bpr;
+  return u;
+}
+__device__ __forceinline__ long long row_of(const Units& u, long long i, int& blk) {
+  const long long r = u.total < (1ll << 31) ? (long long)((uint32_t)i / (uint32_t)u.bpr) : i / u.bpr;
+  blk = (int)(i - r * u.bpr);
+  return r;
+}
+
+constexpr int kBatch = 4;
+template <typename T, int L, bool VEC>
+__global__ void __launch_bounds__(256) k_gather(const Units u, int S, int k, int C, const int32_t* source, const T* x,
+                                                T* out) {
+  pdl_enter();
+  constexpr int PER = 256 / L;
+  const int lane = threadIdx.x & (L - 1);
+  const long long step = (long long)gridDim.x * PER * kBatch;
+  for (long long u0 = (long long)blockIdx.x * PER * kBatch + threadIdx.x / L; u0 < u.total; u0 += step) {
+    Chunk<T> c[kBatch];
+    long long row[kBatch];
+    int c0[kBatch], src[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const long long i = u0 + j * PER;
+      int blk = 0;
+      row[j] = i < u.total ? row_of(u, i, blk) : -1;
+      c0[j] = col0<L, VEC>(blk, lane);
+      src[j] = row[j] >= 0 ? source[row[j]] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if ((uint32_t)src[j] < (uint32_t)S) c[j] = load_chunk<T, L, VEC>(x + (size_t)((uint32_t)src[j] / (uint32_t)k) * C, c0[j], C);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if ((uint32_t)src[j] < (uint32_t)S) {
+        T* o = out + (size_t)row[j] * C;
+        if constexpr (VEC) {
+          constexpr int V = 16 / (int)sizeof(T);
+          const uint4* s = reinterpret_cast<const uint4*>(&c[j]);
+#pragma unroll
+          for (int i = 0; i < 8 / V; ++i)
+            if (c0[j] + i * V < C) reinterpret_cast<uint4*>(o + c0[j])[i] = s[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (col<L, VEC>(c0[j], i) < C) o[col<L, VEC>(c0[j], i)] = c[j].v[i];
+        }
+      }
+  }
+}
+
+template <typename T, int L, bool VEC>
+__global__ void __launch_bounds__(256) k_combine(const Units u, int S, int k, int C, const int32_t* position,
+                                                 const float* weight, const T* y, T* out) {
+  pdl_enter();
+  constexpr int PER = 256 / L;
+  const int lane = threadIdx.x & (L - 1);
+  const long long step = (long long)gridDim.x * PER;
+  for (long long i = (long long)blockIdx.x * PER + threadIdx.x / L; i < u.total; i += step) {
+    int blk;
+    const long long t = row_of(u, i, blk);
+    const int c0 = col0<L, VEC>(blk, lane);
+    const int32_t* pos = position + t * k;
+    const float* w = weight ? weight + t * k : nullptr;
+    float2 acc[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = f2(0.f);
+    for (int j0 = 0; j0 < k; j0 += 4) {
+      Chunk<T> c[4];
+      int p[4];
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[j] = j0 + j < k ? pos[j0 + j] : -1;
+        f[j] = j0 + j < k && w ? w[j0 + j] : 1.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((uint32_t)p[j] < (uint32_t)S) c[j] = load_chunk<T, L, VEC>(y + (size_t)p[j] * C, c0, C);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((uint32_t)p[j] < (uint32_t)S) {
+          float2 v[4];
+          to_pairs(c[j], v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] = fma2(v[e], f2(f[j]), acc[e]);
+        }
+    }
+    store_chunk<T, L, VEC>(out + (size_t)t * C, c0, C, acc);
+  }
+}
+
+// A token belongs to L lanes of W warps with NCH blocks each, dout's row in
+// registers while its k rows of y pass.
+template <typename T, int L, int NCH, bool VEC>
+__global__ void __launch_bounds__(512) k_combine_bwd(int tokens, int S, int k, int C, const int W, const int rpb,
+                                                     const int32_t* position, const float* weight, const T* dout,
+                                                     const T* y, T* dy, float* dweight) {
+  pdl_enter();
+  __shared__ float red[64];
+  const int lane = threadIdx.x & (L - 1), part = threadIdx.x / L, rib = part / W, w = part - rib * W;
+  float* my_red = red + rib * 2 * W;
+  auto c_of = [&](int j) { return col0<L, VEC>(w + j * W, lane); };
+  const long long step = (long long)gridDim.x * rpb;
+  const int first_of_warp = L == 32 ? rib : (threadIdx.x >> 5) * (32 / L);
+  int slot = 0;
+  for (long long t = (long long)blockIdx.x * rpb + rib; t - rib + first_of_warp < tokens; t += step) {
+    const bool live = L == 32 || t < tokens;
+    Chunk<T> cd[NCH];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) cd[j] = load_chunk<T, L, VEC>(dout + (size_t)(live ? t : 0) * C, c_of(j), live ? C : 0);
+    for (int i = 0; i < k; ++i) {
+      const int p = live ? position[t * k + i] : -1;
+      const bool in = (uint32_t)p < (uint32_t)S;
+      const float f = in && weight ? weight[t * k + i] : 1.f;
+      const size_t at = (size_t)(in ? p : 0) * C;
+      Chunk<T> cy[NCH];
+      if (dweight) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) cy[j] = load_chunk<T, L, VEC>(y + at, c_of(j), in ? C : 0);
+      }
+      float2 dot = f2(0.f);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        float2 d[4], v[4];
+        to_pairs(cd[j], d);
+        if (dweight) {
+          to_pairs(cy[j], v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot = fma2(d[e], v[e], dot);
+        }
+        if (dy) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] = mul2(d[e], f2(f));
+          if (in) store_chunk<T, L, VEC>(dy + at, c_of(j), C, d);
+        }
+      }
+      if (dweight) {
+        float s = lanes_sum<L>(dot.x + dot.y);
+        if (L == 32 && W > 1) {
+          float* r = my_red + slot * W;
+          if (lane == 0) r[w] = s;
+          asm volatile("bar.sync %0, %1;" ::"r"(1 + rib), "r"(32 * W) : "memory");
+          s = 0.f;
+          for (int q = 0; q < W; ++q) s += r[q];
+          slot ^= 1;
+        }
+        if (live && w == 0 && lane == 0) dweight[t * k + i] = in ? s : 0.f;
+      }
+    }
+  }
+}
+
+unsigned grid_of(long long units, int per_block) {
+  const long long want = (units + per_block - 1) / per_block, most = (long long)sm_count() * 64;
+  return (unsigned)(want < most ? want : most);
+}
+
+template <typename T, bool VEC>
+cudaError_t gather(const Routes& r, const int32_t* source, const void* x, void* out, cudaStream_t st) {
+  auto go = [&](auto k, const Units& u, int per) {
+    return launch_k(k, dim3(grid_of(u.total, per * kBatch)), dim3(256), 0, st, 1, u, r.S, r.k, r.C, source, (const T*)x,
+                    (T*)out);
+  };
+  if (r.C <= 64) return go(k_gather<T, 8, VEC>, units_of<8>(r.S, r.C), 32);
+  return go(k_gather<T, 32, VEC>, units_of<32>(r.S, r.C), 8);
+}
+template <typename T, bool VEC>
+cudaError_t combine(const Routes& r, const int32_t* position, const float* weight, const void* y, void* out,
+                    cudaStream_t st) {
+  auto go = [&](auto k, const Units& u, int per) {
+    return launch_k(k, dim3(grid_of(u.total, per)), dim3(256), 0, st, 1, u, r.S, r.k, r.C, position, weight, (const T*)y,
+                    (T*)out);
+  };
+  if (r.C <= 64) return go(k_combine<T, 8, VEC>, units_of<8>(r.T, r.C), 32);
+  return go(k_combine<T, 32, VEC>, units_of<32>(r.T, r.C), 8);
+}
+template <typename T, bool VEC>
+cudaError_t combine_bwd(const Routes& r, const int32_t* position, const float* weight, const void* dout, const void* y,
+                        void* dy, float* dweight, cudaStream_t st) {
+  const int blocks = (r.C + 255) / 256;
+  auto go = [&](auto k, int L, int nch) {
+    const int W = L < 32 ? 1 : (blocks + nch - 1) / nch;
+    const int rpb = W == 1 ? 256 / L : W < 8 ? 8 / W : 1;
+    const long long want = ((long long)r.T + rpb - 1) / rpb, most = (long long)sm_count() * 16;
+    return launch_k(k, dim3((unsigned)(want < most ? want : most)), dim3(L * W * rpb), 0, st, 1, r.T, r.S, r.k, r.C, W, rpb,
+                    position, weight, (const T*)dout, (const T*)y, (T*)dy, dweight);
+  };
+  if (r.C <= 64) return go(k_combine_bwd<T, 8, 1, VEC>, 8, 1);
+  if (r.C <= 128) return go(k_combine_bwd<T, 16, 1, VEC>, 16, 1);
+  if (blocks <= 1) return go(k_combine_bwd<T, 32, 1, VEC>, 32, 1);
+  if (blocks == 5) return go(k_combine_bwd<T, 32, 5, VEC>, 32, 5);
+  return go(k_combine_bwd<T, 32, 4, VEC>, 32, 4);
+}
+
+}  // namespace
+
+int sort_warps(int S, int E) {
+  (void)E;
+  if (S <= kOneSlots) return 0;
+  const int share = share_of(S);
+  return (int)(((long long)S + share - 1) / share);
+}
+
+cudaError_t launch_expert_sort(const Routes& r, const int32_t* expert, int32_t* offsets, int32_t* position,
+                               int32_t* source, int32_t* ws, int pass, cudaStream_t st) {
+  const int warps = sort_warps(r.S, r.E), E = r.E;
+  if (warps == 0) {
+    const int smem = kOneWarps * E * (int)sizeof(int);  // 128 KB at most
+    cudaError_t e = cudaFuncSetAttribute(k_sort_one, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kOneWarps * kMaxExperts * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+    return launch_k(k_sort_one, dim3(1), dim3(32 * kOneWarps), smem, st, 1, r.S, E, expert, offsets, position, source);
+  }
+  const int share = share_of(r.S), ctas = (warps + kManyWarps - 1) / kManyWarps;
+  int32_t* totals = ws + (size_t)warps * E;
+  const int hist = kManyWarps * E * (int)sizeof(int);
+  if (pass == 0) return launch_k(k_sort_count, dim3(ctas), dim3(32 * kManyWarps), hist, st, 1, r.S, E, share, warps, expert, ws);
+  if (pass == 1) return launch_k(k_sort_scan, dim3((E + 31) / 32), dim3(1024), 0, st, 1, E, warps, ws, totals);
+  return launch_k(k_sort_place, dim3(ctas), dim3(32 * kManyWarps), hist + E * (int)sizeof(int), st, 1, r.S, E, share, warps,
+                  expert, (const int32_t*)ws, (const int32_t*)totals, offsets, position, source);
+}
+
+cudaError_t launch_expert_gather(const Routes& r, const int32_t* source, const void* x, void* out, cudaStream_t st) {
+  RMX_BY_DTYPE(r.dtype,
+               return rows_aligned(r.C, sizeof(T)) ? gather<T, true>(r, source, x, out, st) : gather<T, false>(r, source, x, out, st))
+}
+cudaError_t launch_expert_combine(const Routes& r, const int32_t* position, const float* weight, const void* y,
+                                  void* out, cudaStream_t st) {
+  RMX_BY_DTYPE(r.dtype, return rows_aligned(r.C, sizeof(T)) ? combine<T, true>(r, position, weight, y, out, st)
+                                                            : combine<T, false>(r, position, weight, y, out, st))
+}
+cudaError_t launch_expert_combine_bwd(const Routes& r, const int32_t* position, const float* weight, const void* dout,
+                                      const void* y, void* dy, float* dweight, cudaStream_t st) {
+  RMX_BY_DTYPE(r.dtype, return rows_aligned(r.C, sizeof(T))
+                                   ? combine_bwd<T, true>(r, position, weight, dout, y, dy, dweight, st)
+                                   : combine_bwd<T, false>(r, position, weight, dout, y, dy, dweight, st))
+}
+
+}  // namespace rmx

@@ -1,0 +1,444 @@
+// 8-bit floating rows: quantisation of rows (with or without a gather before
+// it), of rows and columns of grouped rows in one pass, and reading back.
+//
+// A block of 128 values keeps q * 2^(e - 127).  Scaling by a power of two is
+// exact, so the only rounding is the conversion to 8 bits.  The exponent comes
+// from the largest magnitude's bits: 448 and 57344 are both 7/8 of a power of
+// two, so e follows from its exponent and from whether its mantissa passes 1.75.
+// Bound by HBM: 16-bit values in, bytes out.
+
+#include <float.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "q8_rows.cuh"
+#include "ragged.cuh"
+#include "sparse.h"
+
+namespace rmx {
+namespace {
+
+constexpr int kNaNExp = 255;
+
+// Exponent byte of a block whose largest magnitude has the bits `top`: the
+// smallest e >= 0 with max <= 1.75 * 2^LIM * 2^(e - 127), LIM = 8 (e4m3: 448) or
+// 15 (e5m2: 57344).
+template <bool E5> __device__ __forceinline__ int block_exp(uint32_t top) {
+  if (top >= kInfBits) return kNaNExp;
+  const int e = (int)(top >> 23) - (E5 ? 15 : 8) + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, 0);
+}
+// 2^(127 - e): what a block's values are multiplied by; 0 for a NaN block.
+__device__ __forceinline__ float block_inv(int e) {
+  // e <= 248, so the result is a normal number, and 2^127 at e = 0.
+  return e == kNaNExp ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);
+}
+template <bool E5> __device__ __forceinline__ uint32_t to_f8x2(float lo, float hi) {
+  uint16_t r;
+  if (E5) asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Eight values times inv, as bytes; a NaN block (inv 0) gives zeros.
+template <bool E5> __device__ __forceinline__ uint2 to_f8x8(const float2 (&v)[4], float inv) {
+  if (inv == 0.f) return make_uint2(0, 0);
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = to_f8x2<E5>(v[i].x * inv, v[i].y * inv);
+  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+// Bits of the largest magnitude of eight values; NaN comes out above infinity
+// above every number.
+__device__ __forceinline__ uint32_t top_of(const Chunk<float>& k) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(k.v[i]) & 0x7fffffffu);
+  return m;
+}
+template <typename T> __device__ __forceinline__ uint32_t top_of(const Chunk<T>& k) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&k);
+  uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  return m;  // two halves, see as_f32_bits
+}
+// The larger of two such results.
+template <typename T> __device__ __forceinline__ uint32_t top_max(uint32_t a, uint32_t b) {
+  return sizeof(T) == 4 ? max(a, b) : __vmaxu2(a, b);
+}
+// Such a result as the bits of a float32.
+template <typename T> __device__ __forceinline__ uint32_t as_f32_bits(uint32_t m) {
+  if (sizeof(T) == 4) return m;
+  const uint32_t top = max(m >> 16, m & 0xffffu);
+  if (std::is_same<T, bf16>::value) return top << 16;
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
+}
+
+// A block belongs to eight lanes: lane l has columns 8 l .. 8 l + 7 and 64 + 8 l
+// .. (so that neighbouring lanes' accesses are neighbours).
+template <typename T, bool VEC> struct Load {
+  static __device__ __forceinline__ Chunk<T> chunk(const T* row, int c0, int C) {
+    if constexpr (VEC) {
+      return load_chunk<T, 32, true>(row, c0, C);
+    } else {
+      Chunk<T> k;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) k.v[i] = c0 + i < C ? row[c0 + i] : from_f<T>(0.f);
+      return k;
+    }
+  }
+};
+
+// Blocks of 128 columns at a time to each eight lanes.
+constexpr int kBatch = 2;
+template <typename T, bool VEC, bool E5, bool GATHER>
+__global__ void __launch_bounds__(256) k_quant_f8(const QuantRows a, const int bpr, const int EP, const long long total) {
+  pdl_enter();
+  const int l = threadIdx.x & 7;
+  const long long step = (long long)gridDim.x * 32 * kBatch;
+  const T* x = static_cast<const T*>(a.x);
+  // Whole warps stay in the loop together (their shuffles take every lane).
+  for (long long w0 = ((long long)blockIdx.x * 32 + (threadIdx.x >> 5) * 4) * kBatch; w0 < total; w0 += step) {
+    Chunk<T> k[kBatch][2];
+    long long row[kBatch];
+    int blk[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const long long b = w0 + j * 4 + ((threadIdx.x >> 3) & 3);
+      row[j] = -1;
+      blk[j] = 0;
+      long long from = 0;
+      if (b < total) {
+        const long long r = total < (1ll << 31) ? (long long)((uint32_t)b / (uint32_t)bpr) : b / bpr;
+        blk[j] = (int)(b - r * bpr);
+        row[j] = from = r;
+        if (GATHER) {
+          const int s = a.source[r];
+          if ((uint32_t)s < (uint32_t)a.R) from = (uint32_t)s / (uint32_t)a.k;
+          else row[j] = -1;
+        }
+      }
+      const T* p = x + (size_t)from * a.C;
+      const int C = row[j] >= 0 ? a.C : 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) k[j][h] = Load<T, VEC>::chunk(p, blk[j] * 128 + 64 * h + 8 * l, C);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      uint32_t m = top_max<T>(top_of(k[j][0]), top_of(k[j][1]));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) m = top_max<T>(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (row[j] < 0) continue;
+      const int e = block_exp<E5>(as_f32_bits<T>(m));
+      const float inv = block_inv(e);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c0 = blk[j] * 128 + 64 * h + 8 * l;
+        float2 v[4];
+        to_pairs(k[j][h], v);
+        *reinterpret_cast<uint2*>(a.q + (size_t)row[j] * (bpr * 128) + c0) = to_f8x8<E5>(v, inv);
+        if (GATHER && a.out) {
+          T* o = static_cast<T*>(a.out) + (size_t)row[j] * a.C;
+          if constexpr (VEC) {
+            store_chunk<T, 32, true>(o, c0, a.C, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c0 + i < a.C) o[c0 + i] = k[j][h].v[i];
+          }
+        }
+      }
+      if (l == 0) {
+        uint8_t* ex = a.e + (size_t)row[j] * EP;
+        ex[blk[j]] = (uint8_t)e;
+        if (blk[j] == bpr - 1)
+          for (int i = bpr; i < EP; ++i) ex[i] = 0;
+      }
+    }
+  }
+}
+
+// The value of an exponent byte's step; NaN for a NaN block.
+__device__ __forceinline__ float block_step(int e) {
+  if (e == kNaNExp) return __uint_as_float(0x7fc00000u);
+  return e == 0 ? 0x1p-127f : __uint_as_float((uint32_t)e << 23);
+}
+// Two bytes as floats.
+template <bool E5> __device__ __forceinline__ float2 from_f8x2(uint32_t w) {
+  uint32_t h;
+  if (E5) asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  else asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+template <typename T> struct Largest;
+template <> struct Largest<float> { static constexpr float value = FLT_MAX; };
+template <> struct Largest<bf16> { static constexpr float value = 0x1.fep127f; };
+template <> struct Largest<f16> { static constexpr float value = 65504.f; };
+// q * step in the storage type; where q is finite, so is the result.
+template <typename T> __device__ __forceinline__ float read_back(float q, float step) {
+  const float v = q * step;
+  if (!(fabsf(q) <= FLT_MAX)) return v;
+  return fabsf(v) > Largest<T>::value ? copysignf(Largest<T>::value, v) : v;  // (a NaN step stays NaN)
+}
+
+template <typename T, bool VEC, bool E5>
+__global__ void __launch_bounds__(256) k_dequant_f8(long long total, int bpr, int EP, int C, const uint8_t* q,
+                                                    const uint8_t* e, T* x) {
+  pdl_enter();
+  const int l = threadIdx.x & 7;
+  const long long step = (long long)gridDim.x * 32;
+  for (long long b = (long long)blockIdx.x * 32 + (threadIdx.x >> 3); b < total; b += step) {
+    const long long row = total < (1ll << 31) ? (long long)((uint32_t)b / (uint32_t)bpr) : b / bpr;
+    const int blk = (int)(b - row * bpr);
+    const float s = block_step(e[(size_t)row * EP + blk]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c0 = blk * 128 + 64 * h + 8 * l;
+      const uint2 w = *reinterpret_cast<const uint2*>(q + (size_t)row * (bpr * 128) + c0);
+      float2 v[4] = {from_f8x2<E5>(w.x & 0xffffu), from_f8x2<E5>(w.x >> 16), from_f8x2<E5>(w.y & 0xffffu),
+                     from_f8x2<E5>(w.y >> 16)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = make_float2(read_back<T>(v[i].x, s), read_back<T>(v[i].y, s));
+      T* o = x + (size_t)row * C;
+      if constexpr (VEC) {
+        store_chunk<T, 32, true>(o, c0, C, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c0 + i < C) o[c0 + i] = from_f<T>(i & 1 ? v[i / 2].y : v[i / 2].x);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- rows and columns
+// A CTA takes 128 rows of a group by 128 columns through shared memory: the
+// row pass gives eight lanes a row, the column pass a thread two columns of 32
+// rows (its words in a row of shared memory are its neighbours', without bank
+// conflicts), four threads a column.
+constexpr int kTile = 128, kThreads = 256;
+
+template <typename T> struct Pair2;
+template <> struct Pair2<float> {
+  using W = float2;
+  static __device__ __forceinline__ float2 pair(W w) { return w; }
+};
+template <> struct Pair2<bf16> {
+  using W = uint32_t;
+  static __device__ __forceinline__ float2 pair(W w) { return bf16x2_to_f2(w); }
+};
+template <> struct Pair2<f16> {
+  using W = uint32_t;
+  static __device__ __forceinline__ float2 pair(W w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+};
+
+template <typename T, bool VEC, bool E5>
+__global__ void __launch_bounds__(kThreads) k_quant_groups(const QuantGroups a, const int ctiles, const int EP) {
+  pdl_enter();
+  extern __shared__ uint4 smem_q[];
+  T* tile = reinterpret_cast<T*>(smem_q);  // [128][128]
+  int* first = reinterpret_cast<int*>(tile + kTile * kTile);  // ragged: [G + 1] and [G + 1]
+  int* before = first + a.G + 1;
+  __shared__ uint32_t ctop[4][kTile];
+  __shared__ float csum[4][kTile];
+  const int blk = blockIdx.x / ctiles, c0 = (blockIdx.x - blk * ctiles) * kTile;
+  // The block's group, its first row and how many rows it has, where its column
+  // blocks go.
+  int g, b, rows;
+  long long row0;
+  if (a.offsets) {
+    ragged_scan<kThreads>(a.offsets, a.G, a.M, kTile, first, before);
+    if (blk >= before[a.G]) return;
+    g = ragged_group(before, a.G, blk);
+    b = blk - before[g];
+    rows = min(kTile, first[g + 1] - first[g] - b * kTile);
+    row0 = first[g] + b * kTile;
+  } else {
+    const int per = (a.M + kTile - 1) / kTile;
+    g = blk / per;
+    b = blk - g * per;
+    rows = min(kTile, a.M - b * kTile);
+    row0 = b * kTile;
+  }
+  const T* x = static_cast<const T*>(a.x) + (size_t)g * a.group_stride + (size_t)row0 * a.row_stride;
+  const int t = threadIdx.x;
+
+  // In: zeros outside.
+  if constexpr (VEC) {
+    constexpr int V = 16 / (int)sizeof(T), PER = kTile / V;  // 16-byte vectors of a row
+    for (int i = t; i < kTile * PER; i += kThreads) {
+      const int r = i / PER, c = (i - r * PER) * V;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rows && c0 + c < a.C) v = *reinterpret_cast<const uint4*>(x + (size_t)r * a.row_stride + c0 + c);
+      *reinterpret_cast<uint4*>(tile + r * kTile + c) = v;
+    }
+  } else {
+    for (int i = t; i < kTile * kTile; i += kThreads) {
+      const int r = i >> 7, c = i & 127;
+      tile[i] = r < rows && c0 + c < a.C ? x[(size_t)r * a.row_stride + c0 + c] : from_f<T>(0.f);
+    }
+  }
+  __syncthreads();
+
+  if (a.q) {
+    const int l = t & 7;
+    for (int r = t >> 3; r < kTile; r += kThreads / 8) {
+      Chunk<T> k[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) k[h] = load_chunk<T, 32, true>(tile + r * kTile, 64 * h + 8 * l, kTile);
+      uint32_t m = top_max<T>(top_of(k[0]), top_of(k[1]));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) m = top_max<T>(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (r >= rows) continue;
+      const int e = block_exp<E5>(as_f32_bits<T>(m));
+      const float inv = block_inv(e);
+      const size_t qr = (size_t)g * a.q_group + (size_t)(row0 + r) * a.q_row;
+      uint8_t* q = a.q + qr * ((size_t)ctiles * kTile) + c0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 v[4];
+        to_pairs(k[h], v);
+        *reinterpret_cast<uint2*>(q + 64 * h + 8 * l) = to_f8x8<E5>(v, inv);
+      }
+      if (l == 0) {
+        uint8_t* ex = a.e + qr * EP;
+        ex[c0 / kTile] = (uint8_t)e;
+        if (c0 + kTile >= a.C)
+          for (int i = ctiles; i < EP; ++i) ex[i] = 0;
+      }
+    }
+  }
+  if (!a.qt && !a.part) return;
+  using W = typename Pair2<T>::W;
+  const W* words = reinterpret_cast<const W*>(tile);  // [128][64]
+  const int cp = t & 63, quarter = t >> 6, r0 = quarter * 32;
+  {
+    uint32_t m0 = 0, m1 = 0;
+    float2 s = f2(0.f);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float2 v = Pair2<T>::pair(words[(r0 + i) * 64 + cp]);
+      m0 = max(m0, __float_as_uint(v.x) & 0x7fffffffu);
+      m1 = max(m1, __float_as_uint(v.y) & 0x7fffffffu);
+      s = add2(s, v);
+    }
+    ctop[quarter][2 * cp] = m0;
+    ctop[quarter][2 * cp + 1] = m1;
+    csum[quarter][2 * cp] = s.x;
+    csum[quarter][2 * cp + 1] = s.y;
+  }
+  __syncthreads();
+  if (a.part && t < kTile && c0 + t < a.C)
+    a.part[(size_t)blk * a.C + c0 + t] = (csum[0][t] + csum[1][t]) + (csum[2][t] + csum[3][t]);
+  if (!a.qt) return;
+  // Where column c of group g keeps its blocks: at block b, or (ragged) at the
+  // block's own number.
+  const int kb = a.offsets ? blk : b;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int cl = 2 * cp + h, c = c0 + cl;
+    const uint32_t top = max(max(ctop[0][cl], ctop[1][cl]), max(ctop[2][cl], ctop[3][cl]));
+    const int e = block_exp<E5>(top);
+    const float inv = block_inv(e);
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 p = Pair2<T>::pair(words[(r0 + 4 * i + j) * 64 + cp]);
+        v[j] = h ? p.y : p.x;
+      }
+      o[i] = inv == 0.f ? 0u : to_f8x2<E5>(v[0] * inv, v[1] * inv) | to_f8x2<E5>(v[2] * inv, v[3] * inv) << 16;
+    }
+    if (c >= a.C) continue;
+    const size_t cr = a.offsets ? (size_t)c : (size_t)g * a.C + c;
+    uint4* q = reinterpret_cast<uint4*>(a.qt + cr * a.tp + (size_t)kb * kTile + r0);
+    q[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    q[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    if (quarter == 0) {
+      uint8_t* ex = a.et + cr * a.tep;
+      ex[kb] = (uint8_t)e;
+      if (!a.offsets && (b + 1) * kTile >= a.M)
+        for (int i = b + 1; i < a.tep; ++i) ex[i] = 0;
+    }
+  }
+}
+
+// A group's column sums from its blocks' in their order; a thread a column.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_group_sums(const QuantGroups a) {
+  pdl_enter();
+  extern __shared__ int scan[];
+  int* first = scan;
+  int* before = first + a.G + 1;
+  const int ct = (a.C + kThreads - 1) / kThreads;
+  const int g = blockIdx.x / ct, c = (blockIdx.x - g * ct) * kThreads + threadIdx.x;
+  long long b0, b1;
+  if (a.offsets) {
+    ragged_scan<kThreads>(a.offsets, a.G, a.M, kTile, first, before);
+    b0 = before[g];
+    b1 = before[g + 1];
+  } else {
+    const int per = (a.M + kTile - 1) / kTile;
+    b0 = (long long)g * per;
+    b1 = b0 + per;
+  }
+  if (c >= a.C) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (long long b = b0; b < b1; ++b) s += a.part[(size_t)b * a.C + c];
+  static_cast<T*>(a.sums)[(size_t)g * a.C + c] = from_f<T>(s);
+}
+
+unsigned grid_of(long long units, int per_block) {
+  const long long want = (units + per_block - 1) / per_block, most = (long long)sm_count() * 64;
+  return (unsigned)(want < most ? want : most);
+}
+
+template <typename T, bool VEC, bool E5> cudaError_t quant(const QuantRows& a, cudaStream_t st) {
+  const int bpr = f8_blocks(a.C), EP = f8_exps(a.C);
+  const long long total = a.R * bpr;
+  auto k = a.source ? k_quant_f8<T, VEC, E5, true> : k_quant_f8<T, VEC, E5, false>;
+  return launch_k(k, dim3(grid_of(total, 32 * kBatch)), dim3(256), 0, st, 1, a, bpr, EP, total);
+}
+template <typename T, bool VEC, bool E5>
+cudaError_t dequant(long long R, int C, const uint8_t* q, const uint8_t* e, void* x, cudaStream_t st) {
+  const long long total = R * f8_blocks(C);
+  return launch_k(k_dequant_f8<T, VEC, E5>, dim3(grid_of(total, 32)), dim3(256), 0, st, 1, total, f8_blocks(C), f8_exps(C), C,
+                  q, e, (T*)x);
+}
+template <typename T, bool VEC, bool E5> cudaError_t quant_groups(const QuantGroups& a, cudaStream_t st) {
+  const int ctiles = f8_blocks(a.C);
+  const int smem = kTile * kTile * (int)sizeof(T) + (a.offsets ? 2 * (a.G + 1) * (int)sizeof(int) : 0);
+  auto k = k_quant_groups<T, VEC, E5>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kTile * kTile * (int)sizeof(T) + 2 * (kMaxExperts + 1) * (int)sizeof(int));
+  if (e != cudaSuccess) return e;
+  return launch_k(k, dim3((unsigned)(a.blocks * ctiles)), dim3(kThreads), smem, st, 1, a, ctiles, f8_exps(a.C));
+}
+
+#define BY_FORM(f, T, C, fmt, ...)                                                         \
+  (rows_aligned(C, sizeof(T)) ? (fmt ? f<T, true, true>(__VA_ARGS__) : f<T, true, false>(__VA_ARGS__)) \
+                              : (fmt ? f<T, false, true>(__VA_ARGS__) : f<T, false, false>(__VA_ARGS__)))
+
+}  // namespace
+
+cudaError_t launch_quant_f8(const QuantRows& a, cudaStream_t st) {
+  RMX_BY_DTYPE(a.dtype, return BY_FORM(quant, T, a.C, a.format, a, st))
+}
+cudaError_t launch_dequant_f8(long long R, int C, int dtype, int format, const uint8_t* q, const uint8_t* e, void* x,
+                              cudaStream_t st) {
+  RMX_BY_DTYPE(dtype, return BY_FORM(dequant, T, C, format, R, C, q, e, x, st))
+}
+cudaError_t launch_quant_f8_groups(const QuantGroups& a, cudaStream_t st) {
+  RMX_BY_DTYPE(a.dtype, return BY_FORM(quant_groups, T, a.C, a.format, a, st))
+}
+cudaError_t launch_quant_f8_sums(const QuantGroups& a, cudaStream_t st) {
+  const int smem = a.offsets ? 2 * (a.G + 1) * (int)sizeof(int) : 0;
+  const unsigned grid = (unsigned)(a.G * ((a.C + kThreads - 1) / kThreads));
+  RMX_BY_DTYPE(a.dtype, return launch_k(k_group_sums<T>, dim3(grid), dim3(kThreads), smem, st, 1, a))
+}
+
+}  // namespace rmx

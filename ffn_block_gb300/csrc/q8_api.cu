@@ -11,14 +11,6 @@ using namespace rmx;
 
 namespace {
 
-bool storage_ok(int dtype) { return dtype == RMX_F32 || dtype == RMX_BF16 || dtype == RMX_F16; }
-size_t esize(int dtype) { return dtype == RMX_F32 ? 4 : 2; }
-
-// Rows and columns small enough that every byte offset fits 62 bits and every
-// row index of a chunked pass 40.
-bool rows_ok(const rmx_rows* s) {
-  return s && s->rows >= 0 && s->rows <= (1ll << 36) && s->cols >= 1 && s->cols <= (1 << 24) && storage_ok(s->dtype);
-}
 bool layer_ok(const rmx_layer* l) {
   if (!l || l->M < 0 || l->G < 1 || l->K < 1 || l->N < 1 || !storage_ok(l->dtype)) return false;
   if (l->K > (1 << 20) || l->N > (1 << 20) || l->G > 65535) return false;
@@ -28,11 +20,6 @@ bool layer_ok(const rmx_layer* l) {
 // A group's weights as the tensor maps take them: int8 [N][P] and 16-bit [K][N]
 // strides below 2^40 bytes.
 bool weights_fit(const rmx_layer& l) { return (long long)q8_pitch(l.K) * ((l.N + 7) / 8 * 8) < (1ll << 39); }
-// Null is allowed; a pointer that is given must be aligned.
-rmx_status check_opt(const void* p) { return p ? check_ptr(p) : RMX_OK; }
-
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
 // Workspace of the weight gradient: the unpacked activation [M, G, Kp], and
 // for rows that are not a whole number of 16-byte vectors (16-bit types)
 // padded copies of dy and dw; float32: the bias gradient's column partials.
@@ -43,7 +30,7 @@ struct WgradWs {
 };
 WgradWs wgrad_ws(const rmx_layer& l) {
   WgradWs w;
-  const size_t e = esize(l.dtype), rows = (size_t)l.M * l.G;
+  const size_t e = storage_bytes(l.dtype), rows = (size_t)l.M * l.G;
   w.padded = l.dtype != RMX_F32 && (l.K % 8 || l.N % 8);
   w.Kp = w.padded ? (l.K + 7) / 8 * 8 : l.K;
   w.Np = w.padded ? (l.N + 7) / 8 * 8 : l.N;
@@ -126,7 +113,7 @@ rmx_status rmx_rms_norm_backward(const rmx_rows* shape, const void* dn, const vo
   RMX_TRY(check_ptr(dgamma));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (shape->rows == 0)
-    return cudaMemsetAsync(dgamma, 0, shape->cols * esize(shape->dtype), st) == cudaSuccess ? RMX_OK : RMX_ERR_CUDA;
+    return cudaMemsetAsync(dgamma, 0, shape->cols * storage_bytes(shape->dtype), st) == cudaSuccess ? RMX_OK : RMX_ERR_CUDA;
   if ((h != nullptr) == (q != nullptr) || (q != nullptr) != (exps != nullptr)) return RMX_ERR_INVALID_ARG;
   for (const void* p : {dn, (const void*)rstd, gamma, (const void*)dx, (const void*)ws}) RMX_TRY(check_ptr(p));
   for (const void* p : {dh, h, (const void*)q, (const void*)exps}) RMX_TRY(check_opt(p));
@@ -207,7 +194,7 @@ rmx_status rmx_ckpt8_wgrad(const rmx_layer* layer, const int8_t* q, const int8_t
   RMX_TRY(check_ptr(dw));
   RMX_TRY(check_opt(db));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const size_t e = esize(l.dtype);
+  const size_t e = storage_bytes(l.dtype);
   if (l.M == 0) {
     if (cudaMemsetAsync(dw, 0, (size_t)l.G * l.K * l.N * e, st) != cudaSuccess) return RMX_ERR_CUDA;
     if (db && cudaMemsetAsync(db, 0, (size_t)l.G * l.N * e, st) != cudaSuccess) return RMX_ERR_CUDA;

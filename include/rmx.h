@@ -414,6 +414,200 @@ rmx_status rmx_saved_pack8(const rmx_config* cfg, const void* saved, size_t save
 rmx_status rmx_saved_unpack8(const rmx_config* cfg, const void* saved8, size_t saved8_bytes, void* saved,
                              size_t saved_bytes, rmx_stream stream);
 
+/* ------------------------------------------------------------------------
+ * A sparse layer between blocks: rows that go to a few of many experts, their
+ * products in 8-bit floating point, dropout and layer norm with the residual.
+ *
+ *   x -> rmx_expert_sort, rmx_expert_gather -> rows by expert (also in 8 bits)
+ *     -> rmx_linear_f8 -> rmx_expert_combine -> c
+ *   rmx_layer_norm(c, x): h = drop(c) + x, y = norm(h)
+ *   backward: rmx_layer_norm_backward, rmx_expert_combine_backward,
+ *             rmx_quant_f8_groups, rmx_linear_f8 (dX), rmx_wgrad_f8 (dW),
+ *             rmx_expert_combine without weights (dx)
+ *
+ * The conventions are those above: caller-owned dense row-major device memory,
+ * 16-byte aligned pointers, work enqueued on `stream`, arguments checked before
+ * anything is enqueued, repeated calls bitwise identical (no atomics on
+ * results), nothing may overlap unless said so, a workspace belongs to one call
+ * at a time.  Calls can be captured into CUDA graphs; make the first call on a
+ * device outside a capture.  dtype is RMX_F32, RMX_BF16 or RMX_F16. */
+
+/* Dropout.  An element is kept where its 16 random bits are at least
+ * t = round(65536 p), and is then multiplied by 65536 / (65536 - t), so that the
+ * expected value is the element's own whatever t; p in [0, 1] (p = 1 drops all,
+ * p below 2^-17 none).  A dropped element gives exactly 0, whatever it holds.
+ * The bits come from Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011): element (row, col) of a call takes
+ * counter (col / 8 | row >> 32 << 24, row mod 2^32, offset mod 2^32, offset >>
+ * 32), key (seed mod 2^32, seed >> 32), output word col % 8 / 2, its lower half
+ * for even columns.  No mask is stored: the backward draws the same bits again
+ * from the same state.
+ * state (device, 16-byte aligned): {seed, offset}, read when the work runs, so a
+ * captured graph takes new bits from new contents.  It may be null where p
+ * drops nothing or all. */
+typedef struct {
+  float p;
+  const uint64_t* state;
+} rmx_drop;
+
+/* out = drop(x) + r.  r may be null; out may be x or r itself.  With dout in
+ * place of x and no r: its backward (dr is dout).  cols up to 2^24.  drop may be
+ * null (nothing dropped). */
+rmx_status rmx_dropout(const rmx_rows* shape, const rmx_drop* drop, const void* x, const void* r, void* out,
+                       rmx_stream stream);
+
+/* Layer norm with the residual's addition and dropout before it:
+ *   h = drop(x) + r;  mean, var = moments of h over the row (biased variance)
+ *   rstd = 1 / sqrt(var + eps);  y = (h - mean) * rstd * gamma + beta
+ * x [rows, cols]; r likewise or null; gamma, beta [cols], null: 1 and 0; drop may
+ * be null.  The sum, the statistics and y are float32; the norm is taken of the
+ * unrounded sum.  Outputs: h and y in the storage type, mean, rstd [rows]
+ * float32; h, mean and rstd may be null.  h may be x or r itself.  A constant
+ * row with eps 0 has an infinite rstd and y NaN.  cols <= 16384. */
+rmx_status rmx_layer_norm(const rmx_rows* shape, float eps, const rmx_drop* drop, const void* x, const void* r,
+                          const void* gamma, const void* beta, void* h, void* y, float* mean, float* rstd,
+                          rmx_stream stream);
+
+/* Its backward for the gradient dy of y, from the h, mean and rstd of the
+ * forward: with xh = (h - mean) * rstd and t = dy * gamma,
+ *   dr = rstd * (t - mean(t) - xh * mean(t * xh)) + dh
+ *   dx = drop(dr),  dgamma = sum over rows of dy * xh,  dbeta = sum of dy
+ * dr is the gradient of the sum h and of r.  dh: the gradient that reaches h
+ * from elsewhere (may be null).  dx, dgamma and dbeta may be null; drop, with the
+ * forward's p and state, is only read where dx is given.  dr may be dy or dh.
+ * ws: rmx_layer_norm_backward_workspace_bytes.  rows == 0 writes zero dgamma
+ * and dbeta.  cols <= 16384. */
+size_t rmx_layer_norm_backward_workspace_bytes(const rmx_rows* shape);
+rmx_status rmx_layer_norm_backward(const rmx_rows* shape, const rmx_drop* drop, const void* dy, const void* dh,
+                                   const void* h, const float* mean, const float* rstd, const void* gamma, void* dr,
+                                   void* dx, void* dgamma, void* dbeta, void* ws, size_t ws_bytes,
+                                   rmx_stream stream);
+
+/* Routing of `tokens` rows to k of `experts` each: slot t * k + j is token t's
+ * j-th choice.  tokens * k < 2^31, experts <= 1024, k <= 64, cols <= 16384. */
+typedef struct {
+  int tokens, k, experts;
+  int cols;  /* of the rows that are moved (rmx_expert_sort does not read it) */
+  int dtype; /* theirs */
+} rmx_routes;
+
+/* Slots sorted by expert, in their own order within an expert.  expert [tokens,
+ * k]: an id outside 0 .. experts-1 drops the slot.  offsets [experts + 1]: expert
+ * e has the sorted rows offsets[e] .. offsets[e+1]-1.  position [tokens, k]: the
+ * slot's sorted row, -1 where it is dropped.  source [tokens * k]: the sorted
+ * row's slot, -1 for rows behind the last expert's.  An expert may come several
+ * times among a token's choices.  ws: rmx_expert_sort_workspace_bytes. */
+size_t rmx_expert_sort_workspace_bytes(const rmx_routes* routes);
+rmx_status rmx_expert_sort(const rmx_routes* routes, const int32_t* expert, int32_t* offsets, int32_t* position,
+                           int32_t* source, void* ws, size_t ws_bytes, rmx_stream stream);
+
+/* The tokens' rows in sorted order: out[i] = x[source[i] / k], x [tokens, cols],
+ * out [tokens * k, cols]; also or instead as 8-bit rows q, exps (see below) of
+ * the given rmx_f8 format.  Rows without a source are left as they were.  out, or
+ * q and exps, may be null. */
+rmx_status rmx_expert_gather(const rmx_routes* routes, const int32_t* source, const void* x, void* out, int format,
+                             uint8_t* q, uint8_t* exps, rmx_stream stream);
+
+/* The experts' rows back at their tokens:
+ *   out[t] = sum over j of weight[t,j] * y[position[t,j]]
+ * y [tokens * k, cols] in sorted order; weight [tokens, k] float32 (null: 1); the
+ * sum is float32, in the order of j.  Dropped slots add nothing, whatever their
+ * weight; a token without any gets zeros.  Without weights it is the gather's
+ * backward (dx from the gradient of the sorted rows). */
+rmx_status rmx_expert_combine(const rmx_routes* routes, const int32_t* position, const float* weight, const void* y,
+                              void* out, rmx_stream stream);
+
+/* Its backward for dout [tokens, cols]:
+ *   dy[position[t,j]] = weight[t,j] * dout[t],  dweight[t,j] = sum of dout[t] * y[position[t,j]]
+ * dy [tokens * k, cols] (rows without a source are left as they were), dweight
+ * [tokens, k] float32, 0 for dropped slots.  dweight may be null, and y then
+ * too; dy may be null; dy may be y itself. */
+rmx_status rmx_expert_combine_backward(const rmx_routes* routes, const int32_t* position, const float* weight,
+                                       const void* dout, const void* y, void* dy, float* dweight, rmx_stream stream);
+
+/* 8-bit floating rows.  A row of C columns is cut into blocks of 128; a block
+ * keeps q * 2^(e - 127), q of the given format, e one byte: the smallest e >= 0
+ * with max|block| <= 448 * 2^(e - 127) (e4m3; 57344 for e5m2), so that only q is
+ * rounded (to nearest, ties to even) and nothing saturates.  A block that holds
+ * an infinity or a NaN has e = 255 and reads back as NaN; a zero block has e = 0.
+ * A row takes rmx_f8_pitch(C) bytes of q (C rounded up to 128, zeros behind C)
+ * and rmx_f8_exps(C) bytes of exponents (one a block, rounded up to 4, zeros
+ * behind the last); 0 for C < 1 or C > 2^24. */
+typedef enum { RMX_E4M3 = 0, RMX_E5M2 = 1 } rmx_f8;
+int rmx_f8_pitch(int cols);
+int rmx_f8_exps(int cols);
+
+/* x [rows, cols] as 8-bit rows, and their values back in the storage type
+ * (rounded where it has fewer bits, a finite value that passes its range to the
+ * largest one). */
+rmx_status rmx_quant_f8(const rmx_rows* shape, int format, const void* x, uint8_t* q, uint8_t* exps,
+                        rmx_stream stream);
+rmx_status rmx_dequant_f8(const rmx_rows* shape, int format, const uint8_t* q, const uint8_t* exps, void* x,
+                          rmx_stream stream);
+
+/* Rows in groups: of tokens, weights, or experts.
+ *   RMX_ORDER_TOKENS  x [M, G, C]: row m of group g, the activations of a per-token layer
+ *   RMX_ORDER_GROUPS  x [G, M, C]: the weights of one (M inputs, C outputs)
+ *   RMX_ORDER_RAGGED  x [M, C]: rows sorted by expert, group g the rows offsets[g]
+ *                     .. offsets[g+1]-1 (device; G <= 1024); M is the most there may be
+ * M, C up to 2^24, G * M up to 2^30 and G * C too (RAGGED: M up to 2^30). */
+typedef enum { RMX_ORDER_TOKENS = 0, RMX_ORDER_GROUPS = 1, RMX_ORDER_RAGGED = 2 } rmx_order;
+typedef struct {
+  int M, G, C;
+  int dtype;
+  int order; /* rmx_order */
+} rmx_groups;
+
+/* Both 8-bit forms of x in one pass:
+ *   q, exps      its rows as from rmx_quant_f8, in x's order
+ *   qt, exps_t   its columns: row c of group g holds x[.., g, c] over the group's
+ *                rows, in blocks of 128 of them.  TOKENS, GROUPS: [G, C,
+ *                rmx_f8_pitch(M)] and [G, C, rmx_f8_exps(M)].  RAGGED: [C, TP] and
+ *                [C, TP / 128 rounded up to 4] with TP = rmx_f8_ragged_pitch(M,
+ *                G); every group starts on a new block, zeros behind its rows,
+ *                blocks behind the last group's are left as they were.
+ *   sums         [G, C] in the storage type: the sum over the group's rows (the
+ *                bias gradient, where x is dy)
+ * Each of the three may be null (q and exps together, qt and exps_t too); RAGGED
+ * leaves rows behind offsets[G] as they were.  offsets: RAGGED only, else null.
+ * Offsets below 0, past M or falling are taken as the nearest that are not.
+ * ws: rmx_quant_f8_groups_workspace_bytes, read only where sums is given. */
+int rmx_f8_ragged_pitch(int rows, int groups);
+size_t rmx_quant_f8_groups_workspace_bytes(const rmx_groups* groups);
+rmx_status rmx_quant_f8_groups(const rmx_groups* groups, int format, const int32_t* offsets, const void* x,
+                               uint8_t* q, uint8_t* exps, uint8_t* qt, uint8_t* exps_t, void* sums, void* ws,
+                               size_t ws_bytes, rmx_stream stream);
+
+/* A layer of 8-bit floating operands: rmx_layer's sizes and limits, with the
+ * formats of both.  With offsets (device, [G + 1], G <= 1024) it is a layer of G
+ * experts, and M the most rows there may be, up to 2^30 (offsets as above). */
+typedef struct {
+  int M, G, K, N;
+  int dtype;              /* storage type of out, bias, resid, dw */
+  int a_format, b_format; /* rmx_f8 */
+} rmx_layer_f8;
+
+/* out[m,g,n] = sum_k a[m,g,k] * w[g,n,k] + bias[g,n] + resid[m,g,n]
+ * a: 8-bit rows (a_format) [M, G, K]; w: 8-bit rows (b_format) [G, N, K], i.e. qt
+ * of the weights [G, K, N]; out [M, G, N], bias [G, N], resid [M, G, N] (the last
+ * two may be null; out may be resid itself).  With offsets: a [M, K], out and
+ * resid [M, N], rows offsets[g] .. offsets[g+1]-1 by weight g; rows behind
+ * offsets[G] are left as they were.  The input's gradient is the same call on
+ * dy's rows and q of the weights (rows of N columns).
+ * Products and sums are float32 on the tensor cores (a block's two exponents are
+ * applied there), rounded once; a term or partial sum past float32's range is
+ * infinite or NaN, one below it zero. */
+rmx_status rmx_linear_f8(const rmx_layer_f8* layer, const int32_t* offsets, const uint8_t* a, const uint8_t* a_exps,
+                         const uint8_t* w, const uint8_t* w_exps, const void* bias, const void* resid, void* out,
+                         rmx_stream stream);
+
+/* Weight gradient: dw[g,k,n] = sum over the group's rows of a[m,g,k] * b[m,g,n],
+ * from the columns (qt, exps_t) of the layer's input (a_format, K columns) and of
+ * dy (b_format, N columns), ORDER_TOKENS without offsets and RAGGED with.  dw [G,
+ * K, N]; a group without rows gets zeros.  Precision as above. */
+rmx_status rmx_wgrad_f8(const rmx_layer_f8* layer, const int32_t* offsets, const uint8_t* at, const uint8_t* at_exps,
+                        const uint8_t* bt, const uint8_t* bt_exps, void* dw, rmx_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
