@@ -30,21 +30,34 @@ __device__ __forceinline__ DropBits drop_bits(const Drop& d) {
   return b;
 }
 
-// Which of columns 8 * grp .. 8 * grp + 7 of a row are kept, a bit each.
-__device__ __forceinline__ uint32_t keep8(const DropBits& b, long long row, int grp) {
-  uint32_t c0 = (uint32_t)grp | (uint32_t)(row >> 32) << 24, c1 = (uint32_t)row, c2 = b.o0, c3 = b.o1;
+// The eight columns 8 * grp .. 8 * grp + 7 of a row: 16 bits each, two to a word,
+// the lower half first.  N groups, 32 apart, round by round: a round of one
+// depends on the one before, and the groups fill one another's latency.
+template <int N>
+__device__ __forceinline__ void bits8(const DropBits& b, long long row, int grp, uint32_t (&c)[N][4]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    c[n][0] = (uint32_t)(grp + 32 * n) | (uint32_t)(row >> 32) << 24;
+    c[n][1] = (uint32_t)row;
+    c[n][2] = b.o0;
+    c[n][3] = b.o1;
+  }
   uint32_t k0 = b.k0, k1 = b.k1;
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
-    const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
-    c1 = (uint32_t)p1;
-    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
-    c3 = (uint32_t)p0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint64_t p0 = (uint64_t)c[n][0] * 0xD2511F53u, p1 = (uint64_t)c[n][2] * 0xCD9E8D57u;
+      c[n][0] = (uint32_t)(p1 >> 32) ^ c[n][1] ^ k0;
+      c[n][1] = (uint32_t)p1;
+      c[n][2] = (uint32_t)(p0 >> 32) ^ c[n][3] ^ k1;
+      c[n][3] = (uint32_t)p0;
+    }
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  const uint32_t w[4] = {c0, c1, c2, c3};
+}
+__device__ __forceinline__ uint32_t keep_mask(const DropBits& b, const uint32_t (&w)[4]) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -53,30 +66,54 @@ __device__ __forceinline__ uint32_t keep8(const DropBits& b, long long row, int 
   }
   return m;
 }
-
-// The keep bits of a lane's eight elements, bit i for element i.  VEC: eight
-// neighbouring columns, one draw.  Else element i is column c0 + L * i (c0 the
-// lane's first): eight neighbouring lanes share a draw, and each of them makes
-// the one for another i.  Every lane of the warp takes part.
-template <int L, bool VEC> __device__ __forceinline__ uint32_t keep_of(const DropBits& b, long long row, int c0) {
-  if constexpr (VEC) {
-    return keep8(b, row, c0 >> 3);
-  } else {
-    const int sub = threadIdx.x & 7;
-    const uint32_t mine = keep8(b, row, (c0 + L * sub) >> 3);
-    uint32_t m = 0;
+// Which of one group's are kept, a bit each.
+__device__ __forceinline__ uint32_t keep8(const DropBits& b, long long row, int grp) {
+  uint32_t w[1][4];
+  bits8<1>(b, row, grp, w);
+  return keep_mask(b, w[0]);
+}
+// v * scale where kept, exactly 0 elsewhere, by the words or the bits.
+__device__ __forceinline__ void drop_by_words(const DropBits& b, float scale, const uint32_t (&w)[4], float2 (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m |= ((__shfl_sync(0xffffffffu, mine, i, 8) >> sub) & 1u) << i;
-    return m;
+  for (int i = 0; i < 4; ++i) {
+    const float2 s = mul2(v[i], f2(scale));
+    v[i].x = (w[i] << 16) >= b.lim ? s.x : 0.f;
+    v[i].y = w[i] >= b.lim ? s.y : 0.f;
+  }
+}
+__device__ __forceinline__ void drop_by_mask(uint32_t keep, float scale, float2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 s = mul2(v[i], f2(scale));
+    v[i].x = keep & (1u << (2 * i)) ? s.x : 0.f;
+    v[i].y = keep & (2u << (2 * i)) ? s.y : 0.f;
   }
 }
 
-// v * scale where kept, exactly 0 elsewhere.
-__device__ __forceinline__ void drop_pairs(uint32_t keep, float scale, float2 (&v)[4]) {
+// Dropout of a lane's eight elements: v * scale where kept, exactly 0 elsewhere.
+// VEC: eight neighbouring columns, one draw.  Else element i is column c0 + L * i
+// (c0 the lane's first): eight neighbouring lanes share a draw, and each of them
+// makes the one for another i.  Every lane of the warp takes part.
+template <int L, bool VEC>
+__device__ __forceinline__ void drop_values(const DropBits& b, float scale, long long row, int c0, float2 (&v)[4]) {
+  if (b.mode == DROP_NONE) return;
+  if (b.mode == DROP_ALL) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i].x = keep & (1u << (2 * i)) ? v[i].x * scale : 0.f;
-    v[i].y = keep & (2u << (2 * i)) ? v[i].y * scale : 0.f;
+    for (int i = 0; i < 4; ++i) v[i] = f2(0.f);
+    return;
+  }
+  if constexpr (VEC) {
+    uint32_t w[1][4];
+    bits8<1>(b, row, c0 >> 3, w);
+    drop_by_words(b, scale, w[0], v);
+  } else {
+    const int sub = threadIdx.x & 7;
+    const uint32_t mine = keep8(b, row, (c0 + L * sub) >> 3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float& e = i & 1 ? v[i / 2].y : v[i / 2].x;
+      e = (__shfl_sync(0xffffffffu, mine, i, 8) >> sub) & 1u ? e * scale : 0.f;
+    }
   }
 }
 

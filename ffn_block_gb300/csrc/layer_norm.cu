@@ -79,8 +79,7 @@ __global__ void __launch_bounds__(256) k_dropout(long long row0, uint32_t units,
   for (int j = 0; j < kUnits; ++j) {
     float2 v[4];
     to_pairs(cx[j], v);
-    if (bits.mode == DROP_BITS) drop_pairs(keep_of<L, VEC>(bits, row[j], c0[j]), d.scale, v);
-    else if (bits.mode == DROP_ALL) drop_pairs(0, 0.f, v);
+    drop_values<L, VEC>(bits, d.scale, row[j], c0[j], v);
     if (r) {
       float2 w[4];
       to_pairs(cr[j], w);
@@ -113,11 +112,245 @@ cudaError_t dropout_t(long long R, int C, const Drop& d, const void* x, const vo
   return vec ? dropout<T, 32, true>(R, C, d, x, r, out, st) : dropout<T, 32, false>(R, C, d, x, r, out, st);
 }
 
+// ---------------------------------------------------------------- rows through shared memory
+// Rows of whole 16-byte vectors longer than 512 columns.  A warp has a segment
+// of NCH blocks of 256 columns of a row (rows of up to 1280 columns belong to
+// one warp) and brings its rows in with bulk copies into shared memory of its
+// own, `depth` rows ahead: what is in flight takes no registers, which hold the
+// row's values and (backward) the column sums, 16 a block.  Warps meet only where
+// a row has several.
+constexpr int kRingSmem = 200 * 1024, kRingMaxDepth = 3, kRingParams = 24 * 1024;
+constexpr uint64_t kDrainNs = 50ull * 1000ull * 1000ull;
+template <typename T, int SEG> struct RowRing {
+  T* base;            // [depth][nt][SEG]
+  uint32_t bar0;      // depth barriers
+  const T* src[3];
+  int nt, depth, seg0, C;
+  uint32_t bytes;     // of a segment
+  long long R, step;
+  int s;              // the stage of the row at hand, and its parity
+  uint32_t ph;
+  bool failed;
+
+  __device__ __forceinline__ void issue(long long row, int stage) const {
+    if ((threadIdx.x & 31) != 0 || row >= R) return;
+    const uint32_t bar = bar0 + 8u * (uint32_t)stage, dst = smem_u32(base + (size_t)stage * nt * SEG);
+    const size_t at = (size_t)row * C + seg0;
+    mbar_arrive_expect_tx(bar, bytes * (uint32_t)nt);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < nt) bulk_g2s(dst + (uint32_t)(i * SEG * (int)sizeof(T)), src[i] + at, bytes, bar);
+  }
+  // Eight values of the row at hand (its segment's columns past the row's end are
+  // zeros, written once).
+  static __device__ __forceinline__ Chunk<T> load(const T* p) {
+    Chunk<T> k;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(&k)[i] = reinterpret_cast<const uint4*>(p)[i];
+    return k;
+  }
+  // The warp's barriers; before the block meets.
+  __device__ __forceinline__ void init(int seg) {
+    for (int i = 0; i < depth * nt; ++i)
+      for (int c = seg + (int)(threadIdx.x & 31); c < SEG; c += 32) base[i * SEG + c] = from_f<T>(0.f);
+    if ((threadIdx.x & 31) == 0) {
+      for (int i = 0; i < depth; ++i) mbar_init(bar0 + 8u * (uint32_t)i, 1);
+      fence_mbar_init();
+    }
+    s = 0;
+    ph = 0;
+    failed = false;
+  }
+  __device__ __forceinline__ void start(long long row0) const {
+    for (int i = 0; i < depth; ++i) issue(row0 + i * step, i);
+  }
+  // Waits for the row at hand.  A wait that gives up leaves the block's barriers
+  // in step: the warp goes on (with what it finds), waits no more and issues
+  // nothing.
+  __device__ __forceinline__ const T* wait(unsigned long long limit, unsigned int* err, volatile int* abort) {
+    if (!failed) {
+      const bool ok = mbar_wait_bounded(bar0 + 8u * (uint32_t)s, ph, limit, err, ERRBIT_WAIT_ROWS, abort);
+      failed = !__all_sync(0xffffffffu, ok);
+    }
+    return base + (size_t)s * nt * SEG;
+  }
+  // The row has been read: its stage takes the one `depth` rows on.  The copy is of
+  // the async proxy: a proxy fence orders the warp's reads before its writes.
+  __device__ __forceinline__ void next(long long row) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (failed) return;
+    issue(row + depth * step, s);
+    if (++s == depth) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+  // After a wait that gave up (s, ph have stayed at that row): copies still on
+  // their way land before the shared memory is used again or the block ends.
+  __device__ __forceinline__ void drain(long long gave_up, unsigned int* err) {
+    if (!failed) return;
+    volatile int no_abort = 0;
+    for (int i = 0; i < depth && gave_up + i * step < R; ++i) {
+      mbar_wait_bounded(bar0 + 8u * (uint32_t)s, ph, kDrainNs, err, ERRBIT_WAIT_DRAIN, &no_abort);
+      if (++s == depth) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+  }
+};
+// W warps to a row, rpb rows at a time, as many as shared memory and `threads`
+// hold; deeper where there is room.
+struct RingSpread {
+  int W, nch, rpb, depth, smem;
+};
+RingSpread ring_spread(long long R, int C, int dtype, int nt, int threads) {
+  RingSpread s;
+  const int blocks = (C + 255) / 256;
+  s.W = (blocks + 4) / 5;
+  s.nch = (blocks + s.W - 1) / s.W;
+  const int row_bytes = nt * s.nch * 256 * (dtype == 0 ? 4 : 2);
+  int warps = kRingSmem / (2 * row_bytes);
+  if (warps > threads / 32) warps = threads / 32;
+  s.rpb = warps / s.W;
+  // Few rows: on as many SMs as there are.
+  const long long share = (R + sm_count() - 1) / sm_count();
+  if (s.rpb > share) s.rpb = (int)share;
+  s.depth = s.rpb > 0 ? kRingSmem / (s.rpb * s.W * row_bytes) : 0;
+  if (s.depth > kRingMaxDepth) s.depth = kRingMaxDepth;
+  s.smem = s.rpb * s.W * s.depth * row_bytes;
+  return s;
+}
+
 // ---------------------------------------------------------------- forward
-// A row belongs to L lanes of W warps (W > 1 only with L = 32), with NCH blocks
+constexpr int kFwdRingThreads = 512, kBwdRingThreads = 256;
+template <typename T, int NCH>
+__global__ void __launch_bounds__(kFwdRingThreads, 1)
+    k_layer_norm_ring(const LnFwd a, const int W, const int rpb, const int depth, const bool staged, unsigned int* err,
+                      const unsigned long long limit) {
+  pdl_trigger();
+  constexpr int SEG = NCH * 256;
+  extern __shared__ uint4 ring_smem[];
+  __shared__ float red[64];
+  __shared__ uint64_t bars[kRingMaxDepth * (kFwdRingThreads / 32)];
+  __shared__ int abort_flag;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rib = warp / W, w = warp - rib * W;
+  const int seg0 = w * SEG, seg = min(SEG, a.C - seg0);
+  RowRing<T, SEG> ring;
+  ring.nt = a.r ? 2 : 1;
+  ring.depth = depth;
+  ring.base = reinterpret_cast<T*>(ring_smem) + (size_t)warp * (depth * ring.nt * SEG);
+  ring.bar0 = smem_u32(bars + kRingMaxDepth * warp);
+  ring.src[0] = static_cast<const T*>(a.x);
+  ring.src[1] = static_cast<const T*>(a.r);
+  ring.src[2] = nullptr;
+  ring.seg0 = seg0;
+  ring.C = a.C;
+  ring.bytes = (uint32_t)(seg * (int)sizeof(T));
+  ring.R = a.R;
+  ring.step = (long long)gridDim.x * rpb;
+  ring.init(seg);
+  if (threadIdx.x == 0) abort_flag = 0;
+  __syncthreads();
+  pdl_wait();
+  const long long row0 = (long long)blockIdx.x * rpb + rib;
+  ring.start(row0);
+  const DropBits bits = drop_bits(a.drop);
+  const float inv_n = 1.f / (float)a.C;
+  float* my_red = red + rib * 2 * W;
+  // gamma and beta in shared memory behind the ring, where they fit.
+  T* const held = reinterpret_cast<T*>(ring_smem) + (size_t)rpb * W * (depth * ring.nt * SEG);
+  const int pitch = W * SEG;
+  if (staged) {
+    for (int c = 8 * (int)threadIdx.x; c < a.C; c += 8 * (int)blockDim.x) {
+      if (a.gamma) *reinterpret_cast<Chunk<T>*>(held + c) = load_chunk<T, 32, true>(static_cast<const T*>(a.gamma), c, a.C);
+      if (a.beta) *reinterpret_cast<Chunk<T>*>(held + pitch + c) = load_chunk<T, 32, true>(static_cast<const T*>(a.beta), c, a.C);
+    }
+    __syncthreads();
+  }
+  auto param = [&](const void* p, int i, int c) {
+    return staged ? ring.load(held + i * pitch + c) : load_chunk<T, 32, true>(static_cast<const T*>(p), c, a.C);
+  };
+  long long gave_up = row0;
+  for (long long row = row0; row < a.R; row += ring.step) {
+    const T* in = ring.wait(limit, err, &abort_flag);
+    if (!ring.failed) gave_up = row + ring.step;
+    const size_t at = (size_t)row * a.C;
+    float2 v[NCH][4], s2 = f2(0.f);
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c = j * 256 + lane * 8, c0 = seg0 + c;
+      to_pairs(ring.load(in + c), v[j]);
+      drop_values<32, true>(bits, a.drop.scale, row, c0, v[j]);
+      if (a.r) {
+        float2 r[4];
+        to_pairs(ring.load(in + SEG + c), r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], r[i]);
+      }
+      if (a.h) store_chunk<T, 32, true>(static_cast<T*>(a.h) + at, c0, a.C, v[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s2 = add2(s2, v[j][i]);
+    }
+    ring.next(row);
+    float s[1] = {s2.x + s2.y};
+    row_sums<32, 1>(s, my_red, 0, w, W, 1 + rib);
+    const float mean = s[0] * inv_n;
+    s2 = f2(0.f);
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], f2(-mean));
+      if (seg != SEG) mask_end<32, true>(v[j], seg0 + j * 256 + lane * 8, a.C);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s2 = fma2(v[j][i], v[j][i], s2);
+    }
+    s[0] = s2.x + s2.y;
+    row_sums<32, 1>(s, my_red, 1, w, W, 1 + rib);
+    const float rstd = 1.f / sqrtf(s[0] * inv_n + a.eps);
+    if (w == 0 && lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], f2(rstd));
+      float2 g[4], b[4];
+      if (a.gamma) {
+        to_pairs(param(a.gamma, 0, seg0 + j * 256 + lane * 8), g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], g[i]);
+      }
+      if (a.beta) {
+        to_pairs(param(a.beta, 1, seg0 + j * 256 + lane * 8), b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], b[i]);
+      }
+      store_chunk<T, 32, true>(static_cast<T*>(a.y) + at, seg0 + j * 256 + lane * 8, a.C, v[j]);
+    }
+  }
+  ring.drain(gave_up, err);
+}
+template <typename T> cudaError_t layer_norm_ring(const LnFwd& a, const RingSpread& s, cudaStream_t st) {
+  auto k = s.nch == 3 ? k_layer_norm_ring<T, 3> : s.nch == 4 ? k_layer_norm_ring<T, 4> : k_layer_norm_ring<T, 5>;
+  const int params = 2 * s.W * s.nch * 256 * (int)sizeof(T);
+  const bool staged = (a.gamma || a.beta) && params <= kRingParams;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem + kRingParams);
+  if (e != cudaSuccess) return e;
+  const long long want = (a.R + s.rpb - 1) / s.rpb;
+  return launch_k(k, dim3((unsigned)(want < sm_count() ? want : sm_count())), dim3(32 * s.W * s.rpb),
+                  s.smem + (staged ? params : 0), st, 1, a, s.W, s.rpb, s.depth, staged, device_error_word(), (unsigned long long)kWaitLimitNs);
+}
+
+// Other rows: a row belongs to L lanes of W warps (W > 1 only with L = 32), with NCH blocks
 // of 8 * L columns each; rpb rows at a time to a thread block.
-template <typename T, int L, int NCH, bool VEC>
-__global__ void __launch_bounds__(512) k_layer_norm(const LnFwd a, const int W, const int rpb) {
+// One block after another on an SM's resident ones starts each with its loads
+// exposed: the grid is what fits at once, and blocks go through the rows.
+template <int NCH> constexpr int fwd_blocks = NCH == 1 ? 6 : NCH == 2 ? 4 : 2;
+template <typename T, int L, int NCH, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? fwd_blocks<NCH> : 1) k_layer_norm(const LnFwd a, const int W, const int rpb) {
   pdl_enter();
   __shared__ float red[64];
   const int lane = threadIdx.x & (L - 1), part = threadIdx.x / L, rib = part / W, w = part - rib * W;
@@ -141,8 +374,7 @@ __global__ void __launch_bounds__(512) k_layer_norm(const LnFwd a, const int W, 
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       to_pairs(cx[j], v[j]);
-      if (bits.mode == DROP_BITS) drop_pairs(keep_of<L, VEC>(bits, row, c_of(j)), a.drop.scale, v[j]);
-      else if (bits.mode == DROP_ALL) drop_pairs(0, 0.f, v[j]);
+      drop_values<L, VEC>(bits, a.drop.scale, row, c_of(j), v[j]);
       if (a.r) {
         float2 r[4];
         to_pairs(cr[j], r);
@@ -208,15 +440,22 @@ Spread fwd_spread(int C) {
   return s;
 }
 template <typename T, bool VEC> cudaError_t layer_norm(const LnFwd& a, cudaStream_t st) {
+  if constexpr (VEC) {
+    const RingSpread r = ring_spread(a.R, a.C, a.dtype, a.r ? 2 : 1, kFwdRingThreads);
+    if (a.C > 512 && r.rpb >= 1 && r.W <= 16) return layer_norm_ring<T>(a, r, st);
+  }
   const Spread s = fwd_spread(a.C);
-  auto k = s.L == 8     ? k_layer_norm<T, 8, 1, VEC>
-           : s.L == 16  ? k_layer_norm<T, 16, 1, VEC>
-           : s.nch == 1 ? k_layer_norm<T, 32, 1, VEC>
-           : s.nch == 2 ? k_layer_norm<T, 32, 2, VEC>
-           : s.nch == 4 ? k_layer_norm<T, 32, 4, VEC>
-                        : k_layer_norm<T, 32, 5, VEC>;
-  const long long want = (a.R + s.rpb - 1) / s.rpb, most = (long long)sm_count() * 16;
-  return launch_k(k, dim3((unsigned)(want < most ? want : most)), dim3(s.threads), 0, st, 1, a, s.W, s.rpb);
+  auto go = [&](auto k, int per_sm) {
+    const long long want = (a.R + s.rpb - 1) / s.rpb, most = (long long)sm_count() * per_sm;
+    return launch_k(k, dim3((unsigned)(want < most ? want : most)), dim3(s.threads), 0, st, 1, a, s.W, s.rpb);
+  };
+  if (s.L == 8) return go(k_layer_norm<T, 8, 1, VEC, 256>, fwd_blocks<1>);
+  if (s.L == 16) return go(k_layer_norm<T, 16, 1, VEC, 256>, fwd_blocks<1>);
+  if (s.nch == 1) return go(k_layer_norm<T, 32, 1, VEC, 256>, fwd_blocks<1>);
+  if (s.nch == 2) return go(k_layer_norm<T, 32, 2, VEC, 256>, fwd_blocks<2>);
+  if (s.nch == 5) return go(k_layer_norm<T, 32, 5, VEC, 256>, fwd_blocks<5>);
+  if (s.threads <= 256) return go(k_layer_norm<T, 32, 4, VEC, 256>, fwd_blocks<4>);
+  return go(k_layer_norm<T, 32, 4, VEC, 512>, 1);
 }
 
 // ---------------------------------------------------------------- backward
@@ -298,8 +537,7 @@ __global__ void __launch_bounds__(512) k_layer_norm_bwd(const LnBwd a, const int
       }
       if (live) store_chunk<T, L, VEC>(static_cast<T*>(a.dr) + at, c_of(j), a.C, t);
       if (a.dx) {
-        if (bits.mode == DROP_BITS) drop_pairs(keep_of<L, VEC>(bits, row, c_of(j)), a.drop.scale, t);
-        else if (bits.mode == DROP_ALL) drop_pairs(0, 0.f, t);
+        drop_values<L, VEC>(bits, a.drop.scale, row, c_of(j), t);
         if (live) store_chunk<T, L, VEC>(static_cast<T*>(a.dx) + at, c_of(j), a.C, t);
       }
     }
@@ -347,6 +585,154 @@ __global__ void __launch_bounds__(512) k_layer_norm_bwd(const LnBwd a, const int
   });
 }
 
+template <typename T, int NCH>
+__global__ void __launch_bounds__(kBwdRingThreads, 1)
+    k_layer_norm_bwd_ring(const LnBwd a, const int W, const int rpb, const int depth, unsigned int* err,
+                          const unsigned long long limit) {
+  pdl_trigger();
+  constexpr int SEG = NCH * 256;
+  extern __shared__ uint4 ring_smem[];
+  __shared__ float red[64];
+  __shared__ uint64_t bars[kRingMaxDepth * (kBwdRingThreads / 32)];
+  __shared__ int abort_flag;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rib = warp / W, w = warp - rib * W;
+  const int seg0 = w * SEG, seg = min(SEG, a.C - seg0);
+  RowRing<T, SEG> ring;
+  ring.nt = a.dh ? 3 : 2;
+  ring.depth = depth;
+  ring.base = reinterpret_cast<T*>(ring_smem) + (size_t)warp * (depth * ring.nt * SEG);
+  ring.bar0 = smem_u32(bars + kRingMaxDepth * warp);
+  ring.src[0] = static_cast<const T*>(a.dy);
+  ring.src[1] = static_cast<const T*>(a.h);
+  ring.src[2] = static_cast<const T*>(a.dh);
+  ring.seg0 = seg0;
+  ring.C = a.C;
+  ring.bytes = (uint32_t)(seg * (int)sizeof(T));
+  ring.R = a.R;
+  ring.step = (long long)gridDim.x * rpb;
+  ring.init(seg);
+  if (threadIdx.x == 0) abort_flag = 0;
+  __syncthreads();
+  pdl_wait();
+  const long long row0 = (long long)blockIdx.x * rpb + rib;
+  ring.start(row0);
+  const DropBits bits = drop_bits(a.drop);
+  const float inv_n = 1.f / (float)a.C;
+  float* my_red = red + rib * 4 * W;
+  Chunk<T> gm[NCH];
+  if (a.gamma) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) gm[j] = load_chunk<T, 32, true>(static_cast<const T*>(a.gamma), seg0 + j * 256 + lane * 8, a.C);
+  }
+  float2 ag[NCH][4], ab[NCH][4];
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ag[j][i] = ab[j][i] = f2(0.f);
+  long long gave_up = row0;
+  int slot = 0;
+  float next_rstd = row0 < a.R ? a.rstd[row0] : 0.f, next_mean = row0 < a.R ? a.mean[row0] : 0.f;
+  for (long long row = row0; row < a.R; row += ring.step, slot ^= 1) {
+    const float rstd = next_rstd, shift = -next_mean * rstd;
+    if (row + ring.step < a.R) {
+      next_rstd = a.rstd[row + ring.step];
+      next_mean = a.mean[row + ring.step];
+    }
+    const T* in = ring.wait(limit, err, &abort_flag);
+    if (!ring.failed) gave_up = row + ring.step;
+    float2 m1 = f2(0.f), m2 = f2(0.f), xh[NCH][4], t[NCH][4];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      to_pairs(ring.load(in + j * 256 + lane * 8), t[j]);
+      to_pairs(ring.load(in + SEG + j * 256 + lane * 8), xh[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xh[j][i] = fma2(xh[j][i], f2(rstd), f2(shift));
+        ag[j][i] = fma2(t[j][i], xh[j][i], ag[j][i]);
+        ab[j][i] = add2(t[j][i], ab[j][i]);
+      }
+      if (a.gamma) {
+        float2 g[4];
+        to_pairs(gm[j], g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[j][i] = mul2(t[j][i], g[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m1 = add2(m1, t[j][i]);
+        m2 = fma2(t[j][i], xh[j][i], m2);
+      }
+    }
+    float m[2] = {m1.x + m1.y, m2.x + m2.y};
+    row_sums<32, 2>(m, my_red, slot, w, W, 1 + rib);
+    const float2 c1 = f2(-m[0] * inv_n), c2 = f2(-m[1] * inv_n), rs = f2(rstd);
+    const size_t at = (size_t)row * a.C;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c0 = seg0 + j * 256 + lane * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[j][i] = mul2(fma2(xh[j][i], c2, add2(t[j][i], c1)), rs);
+      if (a.dh) {
+        float2 d[4];
+        to_pairs(ring.load(in + 2 * SEG + j * 256 + lane * 8), d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[j][i] = add2(t[j][i], d[i]);
+      }
+      store_chunk<T, 32, true>(static_cast<T*>(a.dr) + at, c0, a.C, t[j]);
+      if (a.dx) {
+        drop_values<32, true>(bits, a.drop.scale, row, c0, t[j]);
+        store_chunk<T, 32, true>(static_cast<T*>(a.dx) + at, c0, a.C, t[j]);
+      }
+    }
+    ring.next(row);
+  }
+  ring.drain(gave_up, err);
+  __syncthreads();
+  // The block's partials: the rows' sets of warps in order, the first adding the
+  // others' to its own.
+  float* cols = reinterpret_cast<float*>(ring_smem);  // [rpb - 1][2][C]
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = seg0 + j * 256 + lane * 8 + i;
+        if (c < a.C) f(i & 1 ? ag[j][i / 2].y : ag[j][i / 2].x, i & 1 ? ab[j][i / 2].y : ab[j][i / 2].x, c);
+      }
+  };
+  if (rib > 0)
+    each([&](float& g, float& b, int c) {
+      cols[(2 * (rib - 1)) * a.C + c] = g;
+      cols[(2 * (rib - 1) + 1) * a.C + c] = b;
+    });
+  __syncthreads();
+  if (rib > 0) return;
+#pragma unroll 1
+  for (int r = 1; r < rpb; ++r)
+    each([&](float& g, float& b, int c) {
+      g += cols[(2 * (r - 1)) * a.C + c];
+      b += cols[(2 * (r - 1) + 1) * a.C + c];
+    });
+  each([&](float& g, float& b, int c) {
+    a.pg[(size_t)blockIdx.x * a.C + c] = g;
+    a.pb[(size_t)blockIdx.x * a.C + c] = b;
+  });
+}
+
+RingSpread bwd_ring_spread(const LnBwd& a) { return ring_spread(a.R, a.C, a.dtype, a.dh ? 3 : 2, kBwdRingThreads); }
+template <typename T> cudaError_t layer_norm_bwd_ring(const LnBwd& a, cudaStream_t st) {
+  const RingSpread s = bwd_ring_spread(a);
+  auto k = s.nch == 3 ? k_layer_norm_bwd_ring<T, 3> : s.nch == 4 ? k_layer_norm_bwd_ring<T, 4> : k_layer_norm_bwd_ring<T, 5>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+  if (e != cudaSuccess) return e;
+  return launch_k(k, dim3((unsigned)ln_bwd_rows_blocks(a)), dim3(32 * s.W * s.rpb), s.smem, st, 1, a, s.W, s.rpb, s.depth,
+                  device_error_word(), (unsigned long long)kWaitLimitNs);
+}
+// The longest rows need more warps than share a block's registers.
+bool ring_takes(const LnBwd& a) {
+  return a.C > 512 && rows_aligned(a.C, a.dtype == 0 ? 4 : 2) && bwd_ring_spread(a).rpb >= 1;
+}
+
 Spread bwd_spread(int C) {
   Spread s;
   const int blocks = (C + 255) / 256;
@@ -379,6 +765,11 @@ cudaError_t launch_layer_norm(const LnFwd& a, cudaStream_t st) {
   RMX_BY_DTYPE(a.dtype, return rows_aligned(a.C, sizeof(T)) ? layer_norm<T, true>(a, st) : layer_norm<T, false>(a, st))
 }
 int ln_bwd_rows_blocks(const LnBwd& a) {
+  if (ring_takes(a)) {
+    const int rpb = bwd_ring_spread(a).rpb;
+    const long long want = (a.R + rpb - 1) / rpb;
+    return (int)(want < sm_count() ? want : sm_count());
+  }
   const Spread s = bwd_spread(a.C);
   const long long want = (a.R + s.rpb - 1) / s.rpb;
   long long most = (long long)sm_count() * 3;
@@ -386,6 +777,7 @@ int ln_bwd_rows_blocks(const LnBwd& a) {
   return (int)(want < most ? want : most);
 }
 cudaError_t launch_layer_norm_bwd(const LnBwd& a, cudaStream_t st) {
+  if (ring_takes(a)) { RMX_BY_DTYPE(a.dtype, return layer_norm_bwd_ring<T>(a, st)) }
   RMX_BY_DTYPE(a.dtype,
                return rows_aligned(a.C, sizeof(T)) ? layer_norm_bwd<T, true>(a, st) : layer_norm_bwd<T, false>(a, st))
 }
