@@ -24,7 +24,7 @@
 //
 // Groups are tokens of a per-token layer, or experts with rows given by offsets in
 // device memory; the weight gradient contracts over a group's rows, whose columns
-// then lie in blocks of 128 from a block of the group's own on.
+// then lie in blocks of 128 rows, each group's from a block of its own on.
 
 #include <cuda.h>
 
@@ -98,18 +98,6 @@ __device__ __forceinline__ void tmem_st_32x8(uint32_t addr, const uint32_t* r) {
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// Four exponent bytes from byte `at` of a row of them (16-byte aligned rows of
-// whole words): two words where `at` is not a multiple of four, the second one
-// only while it is before `end`, the row's length.
-__device__ __forceinline__ uint32_t four_bytes(const uint8_t* row, int at, int end) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + (at >> 2);
-  const uint32_t lo = *w;
-  const int sh = 8 * (at & 3);
-  if (sh == 0) return lo;
-  const uint32_t hi = (at & ~3) + 4 < end ? w[1] : 0u;
-  return __funnelshift_r(lo, hi, sh);
-}
-
 template <typename T, bool PAIR, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT, const Params p) {
@@ -220,10 +208,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (rank == 0) mbar_expect_tx(full(s), (uint32_t)(p.stage_bytes * CTAS));
           const uint32_t dst = sRing + (uint32_t)(s * p.stage_bytes), fb = full0 + 8u * (uint32_t)s;
-          const int x = (t.kb0 + kb) * kK;
-          // Channels {k, N, G}; tokens {k, G, M}, or {k, K, G} of a weight gradient.
-          const int wg = MODE == WGRAD_RAGGED ? 0 : t.g;
-          const int c1 = MODE == EQUAL ? t.g : MODE == RAGGED ? 0 : mr, c2 = MODE == WGRAD ? t.g : MODE == WGRAD_RAGGED ? 0 : mr;
+          // Channels {k, N, G}; tokens {k, G, M}, or {k, K, G} of a weight gradient;
+          // by expert its operands lie block by block, {128, N or K, block}.
+          const int x = MODE == WGRAD_RAGGED ? 0 : kb * kK, wg = MODE == WGRAD_RAGGED ? t.kb0 + kb : t.g;
+          const int c1 = MODE == EQUAL ? t.g : MODE == RAGGED ? 0 : mr, c2 = MODE == WGRAD || MODE == WGRAD_RAGGED ? wg : mr;
           if (PAIR) {
             tma_load_3d_pair(dst, &tmW, fb, x, t.n0, wg);
             tma_load_3d_pair(dst + 128 * kK, &tmT, fb, x, c1, c2);
@@ -328,12 +316,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < t.nkb; kb += 4) {
         uint32_t w[12];
         // Rows past the end take the last one's: their products are not stored.
+        auto word = [&](const uint8_t* e, int row, long long pitch) {
+          if (MODE != WGRAD_RAGGED) return *reinterpret_cast<const uint32_t*>(e + (size_t)row * pitch + kb);
+          uint32_t v = 0;  // [block][row]
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          w[c] = four_bytes(we + (size_t)min(t.n0 + 32 * c + lane, p.N - 1) * p.we_row, t.kb0 + kb, (int)p.we_row);
+          for (int i = 0; i < 4; ++i)
+            if (kb + i < t.nkb) v |= (uint32_t)e[(size_t)(t.kb0 + kb + i) * pitch + row] << (8 * i);
+          return v;
+        };
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          w[4 + c] = 32 * c < p.nt ? four_bytes(te + (size_t)min(t.m0 + 32 * c + lane, p.rows_end - 1) * p.te_row, t.kb0 + kb, (int)p.we_row) : 0u;
+        for (int c = 0; c < 4; ++c) w[c] = word(we, min(t.n0 + 32 * c + lane, p.N - 1), p.we_row);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[4 + c] = 32 * c < p.nt ? word(te, min(t.m0 + 32 * c + lane, p.rows_end - 1), p.te_row) : 0u;
         if (!wait_warp<CROSS>(exp_empty(slot), ph ^ 1u, ERRBIT_WAIT_ROWS, wc)) {
           ok = false;
           break;
@@ -482,7 +476,7 @@ bool plan(const LinearF8& d, Params& p, bool& pair, long long& tiles) {
   if (tiles > (1ll << 30)) return false;
   p.num_tiles = (int)tiles;
   // Strides of a tensor map: below 2^40 bytes.
-  const long long pitch = mode == WGRAD_RAGGED ? (long long)ragged_blocks(d.M, d.G) * kF8Block : (long long)p.nkb * kK;
+  const long long pitch = mode == WGRAD_RAGGED ? kK : (long long)p.nkb * kK;
   const long long most = d.K > d.N && d.wgrad ? d.K : d.N;
   if (pitch > (1ll << 30) || pitch * most >= (1ll << 39) || pitch * d.G >= (1ll << 39)) return false;
   p.stage_bytes = (128 + p.ntc) * kK;
@@ -520,17 +514,12 @@ cudaError_t launch_linear_f8(const LinearF8& d, unsigned int* err, cudaStream_t 
   p.err = err;
   p.wait_ns = kWaitLimitNs;
   const uint64_t M = d.M, G = d.G, K = d.K, N = d.N;
-  uint64_t pitch, exps;  // of a row of either operand
-  if (mode == WGRAD_RAGGED) {
-    const int blocks = ragged_blocks(d.M, d.G);
-    pitch = (uint64_t)blocks * kF8Block;
-    exps = (uint64_t)(blocks + 3) / 4 * 4;
-  } else {
-    pitch = f8_pitch(d.wgrad ? d.M : d.K);
-    exps = f8_exps(d.wgrad ? d.M : d.K);
-  }
+  // Bytes of a row of either operand, and how many matrices of rows there are.
+  const bool blocks = mode == WGRAD_RAGGED;
+  const uint64_t pitch = blocks ? kF8Block : f8_pitch(d.wgrad ? d.M : d.K), exps = f8_exps(d.wgrad ? d.M : d.K);
+  const uint64_t mats = blocks ? ragged_blocks(d.M, d.G) : G;
   CUtensorMap w, t;
-  bool ok = make_tensor_map_rows8(&w, d.w, pitch, N, mode == WGRAD_RAGGED ? 1 : G, pitch, N * pitch, 128, 1);
+  bool ok = make_tensor_map_rows8(&w, d.w, pitch, N, mats, pitch, N * pitch, 128, 1);
   p.we_row = p.te_row = (long long)exps;
   p.we_group = (long long)(N * exps);
   p.rows_end = p.M;
@@ -552,7 +541,9 @@ cudaError_t launch_linear_f8(const LinearF8& d, unsigned int* err, cudaStream_t 
       p.out_group = (long long)(K * N);
       break;
     default:
-      ok = ok && make_tensor_map_rows8(&t, d.t, pitch, K, 1, pitch, K * pitch, (uint32_t)p.ntc, 1);
+      ok = ok && make_tensor_map_rows8(&t, d.t, pitch, K, mats, pitch, K * pitch, (uint32_t)p.ntc, 1);
+      p.we_row = (long long)N;
+      p.te_row = (long long)K;
       p.out_group = (long long)(K * N);
   }
   if (!ok) return cudaErrorInvalidValue;

@@ -213,10 +213,12 @@ __global__ void __launch_bounds__(256) k_dequant_f8(long long total, int bpr, in
 }
 
 // ---------------------------------------------------------------- rows and columns
-// A CTA takes 128 rows of a group by 128 columns through shared memory: the
-// row pass gives eight lanes a row, the column pass a thread two columns of 32
-// rows (its words in a row of shared memory are its neighbours', without bank
-// conflicts), four threads a column.
+// A CTA takes 128 rows of a group by 128 columns at a time, `tpc` neighbouring
+// tiles of columns, through shared memory.  Row pass: eight lanes a row, straight
+// from the loads (the next tile's are issued before this one's column pass).
+// Column pass: a thread two columns of 32 rows, held in registers between the
+// maximum and the conversion; its words in a row of shared memory are its
+// neighbours', without bank conflicts, and it writes whole 32-byte sectors.
 constexpr int kTile = 128, kThreads = 256;
 
 template <typename T> struct Pair2;
@@ -232,9 +234,27 @@ template <> struct Pair2<f16> {
   using W = uint32_t;
   static __device__ __forceinline__ float2 pair(W w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 };
+// Bits of the larger magnitudes, kept per column of the pair: 16-bit types in
+// the halves of m0, float32 in m0 and m1.
+__device__ __forceinline__ void pair_top(float2 w, uint32_t& m0, uint32_t& m1) {
+  m0 = max(m0, __float_as_uint(w.x) & 0x7fffffffu);
+  m1 = max(m1, __float_as_uint(w.y) & 0x7fffffffu);
+}
+__device__ __forceinline__ void pair_top(uint32_t w, uint32_t& m0, uint32_t&) { m0 = __vmaxu2(m0, w & 0x7fff7fffu); }
+template <typename T> __device__ __forceinline__ uint32_t half_bits(uint32_t h) {
+  if (std::is_same<T, bf16>::value) return h << 16;
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
+}
+// 32 bytes to one sector.
+__device__ __forceinline__ void st_sector(uint8_t* p, const uint32_t (&o)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]),
+               "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+               : "memory");
+}
 
 template <typename T, bool VEC, bool E5>
-__global__ void __launch_bounds__(kThreads) k_quant_groups(const QuantGroups a, const int ctiles, const int EP) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+    k_quant_groups(const QuantGroups a, const int ctiles, const int tpc, const int EP) {
   pdl_enter();
   extern __shared__ uint4 smem_q[];
   T* tile = reinterpret_cast<T*>(smem_q);  // [128][128]
@@ -242,9 +262,9 @@ __global__ void __launch_bounds__(kThreads) k_quant_groups(const QuantGroups a, 
   int* before = first + a.G + 1;
   __shared__ uint32_t ctop[4][kTile];
   __shared__ float csum[4][kTile];
-  const int blk = blockIdx.x / ctiles, c0 = (blockIdx.x - blk * ctiles) * kTile;
-  // The block's group, its first row and how many rows it has, where its column
-  // blocks go.
+  const int runs = (ctiles + tpc - 1) / tpc;
+  const int blk = blockIdx.x / runs, ct0 = (blockIdx.x - blk * runs) * tpc, ct1 = min(ct0 + tpc, ctiles);
+  // The block's group, its first row and how many rows it has.
   int g, b, rows;
   long long row0;
   if (a.offsets) {
@@ -262,32 +282,42 @@ __global__ void __launch_bounds__(kThreads) k_quant_groups(const QuantGroups a, 
     row0 = b * kTile;
   }
   const T* x = static_cast<const T*>(a.x) + (size_t)g * a.group_stride + (size_t)row0 * a.row_stride;
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, l = t & 7;
+  const int cp = t & 63, quarter = t >> 6, r0 = quarter * 32;
 
-  // In: zeros outside.
-  if constexpr (VEC) {
-    constexpr int V = 16 / (int)sizeof(T), PER = kTile / V;  // 16-byte vectors of a row
-    for (int i = t; i < kTile * PER; i += kThreads) {
-      const int r = i / PER, c = (i - r * PER) * V;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rows && c0 + c < a.C) v = *reinterpret_cast<const uint4*>(x + (size_t)r * a.row_stride + c0 + c);
-      *reinterpret_cast<uint4*>(tile + r * kTile + c) = v;
-    }
-  } else {
-    for (int i = t; i < kTile * kTile; i += kThreads) {
-      const int r = i >> 7, c = i & 127;
-      tile[i] = r < rows && c0 + c < a.C ? x[(size_t)r * a.row_stride + c0 + c] : from_f<T>(0.f);
-    }
-  }
-  __syncthreads();
-
-  if (a.q) {
-    const int l = t & 7;
-    for (int r = t >> 3; r < kTile; r += kThreads / 8) {
-      Chunk<T> k[2];
+  Chunk<T> k[4][2];  // rows t / 8 + 32 i, columns 8 l and 64 + 8 l
+  auto load = [&](int c0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) k[h] = load_chunk<T, 32, true>(tile + r * kTile, 64 * h + 8 * l, kTile);
-      uint32_t m = top_max<T>(top_of(k[0]), top_of(k[1]));
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = (t >> 3) + 32 * i;
+        k[i][h] = load_chunk<T, 32, true>(x + (size_t)r * a.row_stride + c0, 64 * h + 8 * l, r < rows ? a.C - c0 : 0);
+      }
+  };
+  if constexpr (VEC) load(ct0 * kTile);
+  for (int ct = ct0; ct < ct1; ++ct) {
+    const int c0 = ct * kTile;
+    if constexpr (!VEC) {
+      for (int i = t; i < kTile * kTile; i += kThreads) {
+        const int r = i >> 7, c = i & 127;
+        tile[i] = r < rows && c0 + c < a.C ? x[(size_t)r * a.row_stride + c0 + c] : from_f<T>(0.f);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) k[i][h] = load_chunk<T, 32, true>(tile + ((t >> 3) + 32 * i) * kTile, 64 * h + 8 * l, kTile);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (t >> 3) + 32 * i;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<Chunk<T>*>(tile + r * kTile + 64 * h + 8 * l) = k[i][h];
+      }
+      if (!a.q) continue;
+      uint32_t m = top_max<T>(top_of(k[i][0]), top_of(k[i][1]));
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) m = top_max<T>(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (r >= rows) continue;
@@ -298,70 +328,81 @@ __global__ void __launch_bounds__(kThreads) k_quant_groups(const QuantGroups a, 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float2 v[4];
-        to_pairs(k[h], v);
+        to_pairs(k[i][h], v);
         *reinterpret_cast<uint2*>(q + 64 * h + 8 * l) = to_f8x8<E5>(v, inv);
       }
       if (l == 0) {
         uint8_t* ex = a.e + qr * EP;
-        ex[c0 / kTile] = (uint8_t)e;
-        if (c0 + kTile >= a.C)
-          for (int i = ctiles; i < EP; ++i) ex[i] = 0;
+        ex[ct] = (uint8_t)e;
+        if (ct == ctiles - 1)
+          for (int j = ctiles; j < EP; ++j) ex[j] = 0;
       }
     }
-  }
-  if (!a.qt && !a.part) return;
-  using W = typename Pair2<T>::W;
-  const W* words = reinterpret_cast<const W*>(tile);  // [128][64]
-  const int cp = t & 63, quarter = t >> 6, r0 = quarter * 32;
-  {
+    __syncthreads();
+    if constexpr (VEC) {
+      if (ct + 1 < ct1) load(c0 + kTile);
+    }
+    if (!a.qt && !a.part) {
+      __syncthreads();
+      continue;
+    }
+    using W = typename Pair2<T>::W;
+    const W* words = reinterpret_cast<const W*>(tile) + r0 * 64 + cp;  // [128][64]
+    W w[32];
     uint32_t m0 = 0, m1 = 0;
-    float2 s = f2(0.f);
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      const float2 v = Pair2<T>::pair(words[(r0 + i) * 64 + cp]);
-      m0 = max(m0, __float_as_uint(v.x) & 0x7fffffffu);
-      m1 = max(m1, __float_as_uint(v.y) & 0x7fffffffu);
-      s = add2(s, v);
+      w[i] = words[i * 64];
+      pair_top(w[i], m0, m1);
     }
-    ctop[quarter][2 * cp] = m0;
-    ctop[quarter][2 * cp + 1] = m1;
-    csum[quarter][2 * cp] = s.x;
-    csum[quarter][2 * cp + 1] = s.y;
-  }
-  __syncthreads();
-  if (a.part && t < kTile && c0 + t < a.C)
-    a.part[(size_t)blk * a.C + c0 + t] = (csum[0][t] + csum[1][t]) + (csum[2][t] + csum[3][t]);
-  if (!a.qt) return;
-  // Where column c of group g keeps its blocks: at block b, or (ragged) at the
-  // block's own number.
-  const int kb = a.offsets ? blk : b;
+    if (sizeof(T) == 2) {
+      m1 = half_bits<T>(m0 >> 16);
+      m0 = half_bits<T>(m0 & 0xffffu);
+    }
+    *reinterpret_cast<uint2*>(&ctop[quarter][2 * cp]) = make_uint2(m0, m1);
+    if (a.part) {
+      float2 s = f2(0.f);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int cl = 2 * cp + h, c = c0 + cl;
-    const uint32_t top = max(max(ctop[0][cl], ctop[1][cl]), max(ctop[2][cl], ctop[3][cl]));
-    const int e = block_exp<E5>(top);
-    const float inv = block_inv(e);
-    uint32_t o[8];
+      for (int i = 0; i < 32; ++i) s = add2(s, Pair2<T>::pair(w[i]));
+      *reinterpret_cast<float2*>(&csum[quarter][2 * cp]) = s;
+    }
+    __syncthreads();  // (also: every word has been read before the next tile's are written)
+    if (a.part && t < kTile && c0 + t < a.C)
+      a.part[(size_t)blk * a.C + c0 + t] = (csum[0][t] + csum[1][t]) + (csum[2][t] + csum[3][t]);
+    if (!a.qt) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v[4];
+    for (int h = 0; h < 2; ++h) {
+      const int cl = 2 * cp + h, c = c0 + cl;
+      const uint32_t top = max(max(ctop[0][cl], ctop[1][cl]), max(ctop[2][cl], ctop[3][cl]));
+      const int e = block_exp<E5>(top);
+      const float inv = block_inv(e);
+      uint32_t o[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 p = Pair2<T>::pair(words[(r0 + 4 * i + j) * 64 + cp]);
-        v[j] = h ? p.y : p.x;
+      for (int i = 0; i < 8; ++i) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 p = Pair2<T>::pair(w[4 * i + j]);
+          v[j] = h ? p.y : p.x;
+        }
+        o[i] = inv == 0.f ? 0u : to_f8x2<E5>(v[0] * inv, v[1] * inv) | to_f8x2<E5>(v[2] * inv, v[3] * inv) << 16;
       }
-      o[i] = inv == 0.f ? 0u : to_f8x2<E5>(v[0] * inv, v[1] * inv) | to_f8x2<E5>(v[2] * inv, v[3] * inv) << 16;
-    }
-    if (c >= a.C) continue;
-    const size_t cr = a.offsets ? (size_t)c : (size_t)g * a.C + c;
-    uint4* q = reinterpret_cast<uint4*>(a.qt + cr * a.tp + (size_t)kb * kTile + r0);
-    q[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    q[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    if (quarter == 0) {
-      uint8_t* ex = a.et + cr * a.tep;
-      ex[kb] = (uint8_t)e;
-      if (!a.offsets && (b + 1) * kTile >= a.M)
-        for (int i = b + 1; i < a.tep; ++i) ex[i] = 0;
+      if (c >= a.C) continue;
+      if (a.offsets) {
+        // Block by block: [blocks][C][128] and [blocks][C].
+        const size_t at = (size_t)blk * a.C + c;
+        st_sector(a.qt + at * kTile + r0, o);
+        if (quarter == 0) a.et[at] = (uint8_t)e;
+      } else {
+        const size_t cr = (size_t)g * a.C + c;
+        st_sector(a.qt + cr * a.tp + (size_t)b * kTile + r0, o);
+        if (quarter == 0) {
+          uint8_t* ex = a.et + cr * a.tep;
+          ex[b] = (uint8_t)e;
+          if ((b + 1) * kTile >= a.M)
+            for (int i = b + 1; i < a.tep; ++i) ex[i] = 0;
+        }
+      }
     }
   }
 }
@@ -416,7 +457,15 @@ template <typename T, bool VEC, bool E5> cudaError_t quant_groups(const QuantGro
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kTile * kTile * (int)sizeof(T) + 2 * (kMaxExperts + 1) * (int)sizeof(int));
   if (e != cudaSuccess) return e;
-  return launch_k(k, dim3((unsigned)(a.blocks * ctiles)), dim3(kThreads), smem, st, 1, a, ctiles, f8_exps(a.C));
+  // Column tiles a CTA takes in turn: as many as still leave four CTAs for each
+  // place there is (three or two an SM).
+  const long long places = 4ll * sm_count() * (sizeof(T) == 2 ? 3 : 2);
+  long long tpc = (long long)a.blocks * ctiles / places;
+  tpc = tpc < 1 ? 1 : tpc > 8 ? 8 : tpc;
+  const int runs = (int)((ctiles + tpc - 1) / tpc);
+  tpc = (ctiles + runs - 1) / runs;
+  return launch_k(k, dim3((unsigned)((long long)a.blocks * ((ctiles + tpc - 1) / tpc))), dim3(kThreads), smem, st, 1, a, ctiles,
+                  (int)tpc, f8_exps(a.C));
 }
 
 #define BY_FORM(f, T, C, fmt, ...)                                                         \
