@@ -19,7 +19,7 @@
 // the next), then four places of 12 columns for exponents.
 //
 // Exponents in tensor memory: a 32-bit word holds a row's for four blocks of k,
-// byte i for block i; the word of row r is in lane r % 32 (the same in all four
+// byte i for block 4 j + i; the word of row r is in lane r % 32 (the same in all four
 // quarters), column r / 32.  The instruction names the byte.
 //
 // Groups are tokens of a per-token layer, or experts with rows given by offsets in
@@ -60,7 +60,8 @@ struct Params {
   const int32_t* offsets;
   int Mcap;                    // rows that offsets may reach
   const uint8_t *te, *we;
-  long long te_row, te_group, we_row, we_group;  // bytes
+  long long te_row, te_group, we_row, we_group;  // bytes between rows and groups
+  long long te_word, we_word;                    // and from four blocks' exponents to the next four's
   long long out_row, out_group;                  // elements
   const void *bias, *resid;
   void* out;
@@ -261,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t accumulate = 0;
 #pragma unroll 1
         for (int kb = 0; kb < t.nkb; ++kb) {
-          const uint32_t byte = (uint32_t)kb & 3u;
-          if (byte == 0 && !wait_one<CROSS>(exp_full(slot), eph, ERRBIT_WAIT_MMA, wc)) {
+          const uint32_t byte = (uint32_t)(t.kb0 + kb) & 3u;
+          if ((byte == 0 || kb == 0) && !wait_one<CROSS>(exp_full(slot), eph, ERRBIT_WAIT_MMA, wc)) {
             ok = false;
             break;
           }
@@ -304,6 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kFirstExp && warp < kFirstEpi) {
     // ------------------------------------------------------------ exponents
+    // A word of each row for every four blocks of k: the next four's are on
+    // their way while these wait for their place.
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kExpCol0;
     const uint32_t full0 = PAIR ? mapa_shared(exp_full(0), 0) : exp_full(0);
     int slot = 0, used = 0;
@@ -311,23 +314,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int tile = tile0; ok && tile < num_tiles; tile += stride) {
       const Tile t = tile_of(tile);
-      const uint8_t* we = p.we + (MODE == WGRAD_RAGGED ? 0 : (size_t)t.g * p.we_group);
-      const uint8_t* te = p.te + (MODE == WGRAD_RAGGED ? 0 : (size_t)t.g * p.te_group);
-      for (int kb = 0; kb < t.nkb; kb += 4) {
-        uint32_t w[12];
-        // Rows past the end take the last one's: their products are not stored.
-        auto word = [&](const uint8_t* e, int row, long long pitch) {
-          if (MODE != WGRAD_RAGGED) return *reinterpret_cast<const uint32_t*>(e + (size_t)row * pitch + kb);
-          uint32_t v = 0;  // [block][row]
+      // Rows past the end take the last one's: their products are not stored.
+      const uint8_t* row[12];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (kb + i < t.nkb) v |= (uint32_t)e[(size_t)(t.kb0 + kb + i) * pitch + row] << (8 * i);
-          return v;
-        };
+      for (int c = 0; c < 4; ++c)
+        row[c] = p.we + (MODE == WGRAD_RAGGED ? 0 : (size_t)t.g * p.we_group) + (size_t)min(t.n0 + 32 * c + lane, p.N - 1) * p.we_row;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = word(we, min(t.n0 + 32 * c + lane, p.N - 1), p.we_row);
+      for (int c = 0; c < 8; ++c)
+        row[4 + c] = p.te + (MODE == WGRAD_RAGGED ? 0 : (size_t)t.g * p.te_group) +
+                     (size_t)min(t.m0 + 32 * c + lane, p.rows_end - 1) * p.te_row;
+      const int q0 = t.kb0 >> 2, q1 = t.nkb > 0 ? (t.kb0 + t.nkb + 3) >> 2 : q0;
+      auto load = [&](int q, uint32_t (&w)[12]) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) w[4 + c] = 32 * c < p.nt ? word(te, min(t.m0 + 32 * c + lane, p.rows_end - 1), p.te_row) : 0u;
+        for (int c = 0; c < 12; ++c)
+          w[c] = c < 4 || 32 * (c - 4) < p.nt
+                     ? *reinterpret_cast<const uint32_t*>(row[c] + (size_t)q * (c < 4 ? p.we_word : p.te_word))
+                     : 0u;
+      };
+      uint32_t w[12], next[12];
+      if (q0 < q1) load(q0, w);
+      for (int q = q0; q < q1; ++q) {
+        if (q + 1 < q1) load(q + 1, next);
         if (!wait_warp<CROSS>(exp_empty(slot), ph ^ 1u, ERRBIT_WAIT_ROWS, wc)) {
           ok = false;
           break;
@@ -344,6 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           slot = 0;
           ph ^= 1u;
         }
+#pragma unroll
+        for (int c = 0; c < 12; ++c) w[c] = next[c];
       }
     }
     if (warp == kFirstExp) {
@@ -521,6 +530,7 @@ cudaError_t launch_linear_f8(const LinearF8& d, unsigned int* err, cudaStream_t 
   CUtensorMap w, t;
   bool ok = make_tensor_map_rows8(&w, d.w, pitch, N, mats, pitch, N * pitch, 128, 1);
   p.we_row = p.te_row = (long long)exps;
+  p.we_word = p.te_word = 4;
   p.we_group = (long long)(N * exps);
   p.rows_end = p.M;
   p.out_row = (long long)N;
@@ -542,8 +552,9 @@ cudaError_t launch_linear_f8(const LinearF8& d, unsigned int* err, cudaStream_t 
       break;
     default:
       ok = ok && make_tensor_map_rows8(&t, d.t, pitch, K, mats, pitch, K * pitch, (uint32_t)p.ntc, 1);
-      p.we_row = (long long)N;
-      p.te_row = (long long)K;
+      p.we_row = p.te_row = 4;
+      p.we_word = (long long)(4 * N);
+      p.te_word = (long long)(4 * K);
       p.out_group = (long long)(K * N);
   }
   if (!ok) return cudaErrorInvalidValue;

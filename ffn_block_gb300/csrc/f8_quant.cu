@@ -389,10 +389,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       }
       if (c >= a.C) continue;
       if (a.offsets) {
-        // Block by block: [blocks][C][128] and [blocks][C].
-        const size_t at = (size_t)blk * a.C + c;
-        st_sector(a.qt + at * kTile + r0, o);
-        if (quarter == 0) a.et[at] = (uint8_t)e;
+        // Block by block, [blocks][C][128], the exponents in fours, [blocks / 4][C][4].
+        st_sector(a.qt + ((size_t)blk * a.C + c) * kTile + r0, o);
+        if (quarter == 0) a.et[((size_t)(blk >> 2) * a.C + c) * 4 + (blk & 3)] = (uint8_t)e;
       } else {
         const size_t cr = (size_t)g * a.C + c;
         st_sector(a.qt + cr * a.tp + (size_t)b * kTile + r0, o);

@@ -563,9 +563,10 @@ typedef struct {
  *   qt, exps_t   its columns: row c of group g holds x[.., g, c] over the group's
  *                rows, in blocks of 128 of them.  TOKENS, GROUPS: [G, C,
  *                rmx_f8_pitch(M)] and [G, C, rmx_f8_exps(M)].  RAGGED: block by
- *                block, [NB, C, 128] and [NB, C] with NB = rmx_f8_ragged_pitch(M,
- *                G) / 128; every group starts on a new block, zeros behind its
- *                rows, blocks behind the last group's are left as they were.
+ *                block, [NB, C, 128], and four blocks' exponents together, [NB / 4
+ *                rounded up, C, 4], with NB = rmx_f8_ragged_pitch(M, G) / 128;
+ *                every group starts on a new block, zeros behind its rows, blocks
+ *                behind the last group's are left as they were.
  *   sums         [G, C] in the storage type: the sum over the group's rows (the
  *                bias gradient, where x is dy)
  * Each of the three may be null (q and exps together, qt and exps_t too); RAGGED

@@ -111,7 +111,7 @@ def test_rows_and_columns(order, dt, fmt, M, G, C):
     lead = x.shape[:-1]
     ragged = order == "ragged"
     TP = B.rmx_f8_ragged_pitch(M, G) if ragged else B.rmx_f8_pitch(M)
-    TE = TP // 128 if ragged else B.rmx_f8_exps(M)
+    TE = (TP // 128 + 3) // 4 * 4 if ragged else B.rmx_f8_exps(M)
     new = lambda: (full_of((*lead, P), torch.uint8, 7), full_of((*lead, EP), torch.uint8, 7),  # noqa: E731
                    full_of(((C, TP) if ragged else (G, C, TP)), torch.uint8, 7),
                    full_of(((C, TE) if ragged else (G, C, TE)), torch.uint8, 7), full_of((G, C), dt, 7.0))
@@ -135,12 +135,12 @@ def test_rows_and_columns(order, dt, fmt, M, G, C):
                 vq, ve = O.quant_rows(xg.T, fmt)
                 got = qt.reshape(TP // 128, C, 128)[kb : kb + nb].transpose(0, 1).reshape(C, nb * 128).contiguous()
                 assert np.array_equal(f8_values(got, fmt), vq)
-                assert np.array_equal(et.reshape(TP // 128, C).t().cpu().numpy()[:, kb : kb + nb], ve)
+                assert np.array_equal(et.reshape(-1, C, 4).transpose(0, 1).reshape(C, TE).cpu().numpy()[:, kb : kb + nb], ve)
             kb += nb
         else:
             _check_rows(qt[g], et[g], xg.T, fmt, M)
     if ragged:
-        assert torch.all(qt.reshape(TP // 128, C, 128)[kb:] == 7) and torch.all(et.reshape(TP // 128, C)[kb:] == 7)
+        assert torch.all(qt.reshape(TP // 128, C, 128)[kb:] == 7) and torch.all(et.reshape(-1, C, 4).transpose(0, 1).reshape(C, TE)[:, kb:] == 7)
     # each by itself is the same
     a, b = new(), new()
     ok(B.rmx_quant_f8_groups(gr, fmt, doff, dx, a[0], a[1], None, None, None, None, 0))
@@ -327,7 +327,7 @@ def test_weight_gradient(order, M, G, K, N, dt):
     forms = []
     for v, c, fmt in ((x, K, "e4m3"), (dy, N, "e5m2")):
         TP = B.rmx_f8_ragged_pitch(M, G) if ragged else B.rmx_f8_pitch(M)
-        TE = TP // 128 if ragged else B.rmx_f8_exps(M)
+        TE = (TP // 128 + 3) // 4 * 4 if ragged else B.rmx_f8_exps(M)
         qt = full_of((c, TP) if ragged else (G, c, TP), torch.uint8, 0x7F)
         et = full_of((c, TE) if ragged else (G, c, TE), torch.uint8, 255)
         ok(B.rmx_quant_f8_groups(B.make_groups(M, G, c, "f32", order), fmt, dev(off.astype(np.int32)) if ragged else None,
