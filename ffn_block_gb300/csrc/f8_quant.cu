@@ -45,8 +45,11 @@ template <bool E5> __device__ __forceinline__ uint2 to_f8x8(const float2 (&v)[4]
   if (inv == 0.f) return make_uint2(0, 0);
   uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = to_f8x2<E5>(v[i].x * inv, v[i].y * inv);
-  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = mul2(v[i], f2(inv));
+    h[i] = to_f8x2<E5>(u.x, u.y);
+  }
+  return make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
 }
 // Bits of the largest magnitude of eight values; NaN comes out above infinity
 // above every number.
@@ -213,9 +216,9 @@ __global__ void __launch_bounds__(256) k_dequant_f8(long long total, int bpr, in
 }
 
 // ---------------------------------------------------------------- rows and columns
-// A CTA takes 128 rows of a group by 128 columns at a time, `tpc` neighbouring
-// tiles of columns, through shared memory.  Row pass: eight lanes a row, straight
-// from the loads (the next tile's are issued before this one's column pass).
+// A CTA takes tiles of 128 rows of a group by 128 columns through shared memory; the grid is what fits at once.  Row pass: eight lanes a
+// row, straight from the loads (the next tile's are issued before this one's
+// column pass).
 // Column pass: a thread two columns of 32 rows, held in registers between the
 // maximum and the conversion; its words in a row of shared memory are its
 // neighbours', without bank conflicts, and it writes whole 32-byte sectors.
@@ -254,7 +257,7 @@ __device__ __forceinline__ void st_sector(uint8_t* p, const uint32_t (&o)[8]) {
 
 template <typename T, bool VEC, bool E5>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
-    k_quant_groups(const QuantGroups a, const int ctiles, const int tpc, const int EP) {
+    k_quant_groups(const QuantGroups a, const int ctiles, const int EP) {
   pdl_enter();
   extern __shared__ uint4 smem_q[];
   T* tile = reinterpret_cast<T*>(smem_q);  // [128][128]
@@ -262,43 +265,68 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
   int* before = first + a.G + 1;
   __shared__ uint32_t ctop[4][kTile];
   __shared__ float csum[4][kTile];
-  const int runs = (ctiles + tpc - 1) / tpc;
-  const int blk = blockIdx.x / runs, ct0 = (blockIdx.x - blk * runs) * tpc, ct1 = min(ct0 + tpc, ctiles);
-  // The block's group, its first row and how many rows it has.
-  int g, b, rows;
-  long long row0;
+  uint32_t blocks = (uint32_t)a.blocks;
   if (a.offsets) {
     ragged_scan<kThreads>(a.offsets, a.G, a.M, kTile, first, before);
-    if (blk >= before[a.G]) return;
-    g = ragged_group(before, a.G, blk);
-    b = blk - before[g];
-    rows = min(kTile, first[g + 1] - first[g] - b * kTile);
-    row0 = first[g] + b * kTile;
-  } else {
-    const int per = (a.M + kTile - 1) / kTile;
-    g = blk / per;
-    b = blk - g * per;
-    rows = min(kTile, a.M - b * kTile);
-    row0 = b * kTile;
+    blocks = (uint32_t)before[a.G];
   }
-  const T* x = static_cast<const T*>(a.x) + (size_t)g * a.group_stride + (size_t)row0 * a.row_stride;
+  // Tiles go to the CTAs in turn, so that what is read at one time lies together.
+  const uint32_t end = blocks * (uint32_t)ctiles;  // below 2^31
+  uint32_t at = blockIdx.x;
+  if (at >= end) return;
+  // A block of rows: its group, its number there, its first row, how many it has.
+  struct Block {
+    int blk, g, b, rows;
+    long long row0;
+  };
+  auto block_of = [&](int blk) {
+    Block k;
+    k.blk = blk;
+    if (a.offsets) {
+      k.g = ragged_group(before, a.G, blk);
+      k.b = blk - before[k.g];
+      k.rows = min(kTile, first[k.g + 1] - first[k.g] - k.b * kTile);
+      k.row0 = first[k.g] + k.b * kTile;
+    } else {
+      const int per = (a.M + kTile - 1) / kTile;
+      k.g = blk / per;
+      k.b = blk - k.g * per;
+      k.rows = min(kTile, a.M - k.b * kTile);
+      k.row0 = (long long)k.b * kTile;
+    }
+    return k;
+  };
+  Block cur = block_of((int)(at / (uint32_t)ctiles));
+  int ct = (int)at - cur.blk * ctiles;
   const int t = threadIdx.x, l = t & 7;
   const int cp = t & 63, quarter = t >> 6, r0 = quarter * 32;
 
   Chunk<T> k[4][2];  // rows t / 8 + 32 i, columns 8 l and 64 + 8 l
-  auto load = [&](int c0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = (t >> 3) + 32 * i;
-        k[i][h] = load_chunk<T, 32, true>(x + (size_t)r * a.row_stride + c0, 64 * h + 8 * l, r < rows ? a.C - c0 : 0);
-      }
+  const size_t x_step = 32 * (size_t)a.row_stride, q_pitch = (size_t)ctiles * kTile;
+  const size_t q_step = 32 * (size_t)a.q_row * q_pitch, e_step = 32 * (size_t)a.q_row * EP;
+  auto base = [&](const Block& k) {
+    return static_cast<const T*>(a.x) + (size_t)k.g * a.group_stride + (size_t)k.row0 * a.row_stride;
   };
-  if constexpr (VEC) load(ct0 * kTile);
-  for (int ct = ct0; ct < ct1; ++ct) {
-    const int c0 = ct * kTile;
+  auto load = [&](const Block& n, int c0) {
+    const T* p = base(n) + (size_t)(t >> 3) * a.row_stride + c0;
+    if (n.rows == kTile && c0 + kTile <= a.C) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) k[i][h] = *reinterpret_cast<const Chunk<T>*>(p + i * x_step + 64 * h + 8 * l);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          k[i][h] = load_chunk<T, 32, true>(p + i * x_step, 64 * h + 8 * l, (t >> 3) + 32 * i < n.rows ? a.C - c0 : 0);
+    }
+  };
+  if constexpr (VEC) load(cur, ct * kTile);
+  for (; at < end; at += gridDim.x) {
+    const int c0 = ct * kTile, g = cur.g, b = cur.b, blk = cur.blk, rows = cur.rows;
     if constexpr (!VEC) {
+      const T* x = base(cur);
       for (int i = t; i < kTile * kTile; i += kThreads) {
         const int r = i >> 7, c = i & 127;
         tile[i] = r < rows && c0 + c < a.C ? x[(size_t)r * a.row_stride + c0 + c] : from_f<T>(0.f);
@@ -309,6 +337,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
 #pragma unroll
         for (int h = 0; h < 2; ++h) k[i][h] = load_chunk<T, 32, true>(tile + ((t >> 3) + 32 * i) * kTile, 64 * h + 8 * l, kTile);
     }
+    const size_t qr0 = (size_t)g * a.q_group + (size_t)(cur.row0 + (t >> 3)) * a.q_row;
+    uint8_t* const pq = a.q + qr0 * q_pitch + 8 * l;
+    uint8_t* const pe = a.e + qr0 * EP;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = (t >> 3) + 32 * i;
@@ -323,24 +354,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       if (r >= rows) continue;
       const int e = block_exp<E5>(as_f32_bits<T>(m));
       const float inv = block_inv(e);
-      const size_t qr = (size_t)g * a.q_group + (size_t)(row0 + r) * a.q_row;
-      uint8_t* q = a.q + qr * ((size_t)ctiles * kTile) + c0;
+      uint8_t* const q = pq + i * q_step + c0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float2 v[4];
         to_pairs(k[i][h], v);
-        *reinterpret_cast<uint2*>(q + 64 * h + 8 * l) = to_f8x8<E5>(v, inv);
+        *reinterpret_cast<uint2*>(q + 64 * h) = to_f8x8<E5>(v, inv);
       }
       if (l == 0) {
-        uint8_t* ex = a.e + qr * EP;
-        ex[ct] = (uint8_t)e;
-        if (ct == ctiles - 1)
+        uint8_t* ex = pe + i * e_step;
+        ex[c0 / kTile] = (uint8_t)e;
+        if (c0 + kTile >= a.C)
           for (int j = ctiles; j < EP; ++j) ex[j] = 0;
       }
     }
     __syncthreads();
-    if constexpr (VEC) {
-      if (ct + 1 < ct1) load(c0 + kTile);
+    const uint32_t next = at + gridDim.x;
+    if (next < end) {
+      cur = block_of((int)(next / (uint32_t)ctiles));
+      ct = (int)next - cur.blk * ctiles;
+      if constexpr (VEC) load(cur, ct * kTile);
     }
     if (!a.qt && !a.part) {
       __syncthreads();
@@ -370,22 +403,32 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     if (a.part && t < kTile && c0 + t < a.C)
       a.part[(size_t)blk * a.C + c0 + t] = (csum[0][t] + csum[1][t]) + (csum[2][t] + csum[3][t]);
     if (!a.qt) continue;
+    // Both columns at once.
+    int ex2[2];
+    float2 inv2;
+    {
+      const uint2 q0 = *reinterpret_cast<const uint2*>(&ctop[0][2 * cp]), q1 = *reinterpret_cast<const uint2*>(&ctop[1][2 * cp]),
+                  q2 = *reinterpret_cast<const uint2*>(&ctop[2][2 * cp]), q3 = *reinterpret_cast<const uint2*>(&ctop[3][2 * cp]);
+      ex2[0] = block_exp<E5>(max(max(q0.x, q1.x), max(q2.x, q3.x)));
+      ex2[1] = block_exp<E5>(max(max(q0.y, q1.y), max(q2.y, q3.y)));
+      inv2 = make_float2(block_inv(ex2[0]), block_inv(ex2[1]));
+    }
+    uint32_t o2[2][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float2 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = mul2(Pair2<T>::pair(w[4 * i + j]), inv2);
+      o2[0][i] = __byte_perm(to_f8x2<E5>(v[0].x, v[1].x), to_f8x2<E5>(v[2].x, v[3].x), 0x5410);
+      o2[1][i] = __byte_perm(to_f8x2<E5>(v[0].y, v[1].y), to_f8x2<E5>(v[2].y, v[3].y), 0x5410);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int cl = 2 * cp + h, c = c0 + cl;
-      const uint32_t top = max(max(ctop[0][cl], ctop[1][cl]), max(ctop[2][cl], ctop[3][cl]));
-      const int e = block_exp<E5>(top);
-      const float inv = block_inv(e);
-      uint32_t o[8];
+      const int c = c0 + 2 * cp + h, e = ex2[h];
+      uint32_t (&o)[8] = o2[h];
+      if (e == kNaNExp) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 p = Pair2<T>::pair(w[4 * i + j]);
-          v[j] = h ? p.y : p.x;
-        }
-        o[i] = inv == 0.f ? 0u : to_f8x2<E5>(v[0] * inv, v[1] * inv) | to_f8x2<E5>(v[2] * inv, v[3] * inv) << 16;
+        for (int i = 0; i < 8; ++i) o[i] = 0;
       }
       if (c >= a.C) continue;
       if (a.offsets) {
@@ -456,15 +499,8 @@ template <typename T, bool VEC, bool E5> cudaError_t quant_groups(const QuantGro
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kTile * kTile * (int)sizeof(T) + 2 * (kMaxExperts + 1) * (int)sizeof(int));
   if (e != cudaSuccess) return e;
-  // Column tiles a CTA takes in turn: as many as still leave four CTAs for each
-  // place there is (three or two an SM).
-  const long long places = 4ll * sm_count() * (sizeof(T) == 2 ? 3 : 2);
-  long long tpc = (long long)a.blocks * ctiles / places;
-  tpc = tpc < 1 ? 1 : tpc > 8 ? 8 : tpc;
-  const int runs = (int)((ctiles + tpc - 1) / tpc);
-  tpc = (ctiles + runs - 1) / runs;
-  return launch_k(k, dim3((unsigned)((long long)a.blocks * ((ctiles + tpc - 1) / tpc))), dim3(kThreads), smem, st, 1, a, ctiles,
-                  (int)tpc, f8_exps(a.C));
+  const long long tiles = (long long)a.blocks * ctiles, fit = (sizeof(T) == 2 ? 3ll : 2ll) * sm_count();
+  return launch_k(k, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kThreads), smem, st, 1, a, ctiles, f8_exps(a.C));
 }
 
 #define BY_FORM(f, T, C, fmt, ...)                                                         \
