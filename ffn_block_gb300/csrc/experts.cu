@@ -2,17 +2,19 @@
 // experts' rows added up at their tokens, and the backward of that.
 //
 // The sort counts.  A warp takes its slots in order, 32 at a time: lanes with
-// the same expert find one another (match), so a slot's place among them is a
+// the same expert find one another by votes, so a slot's place among them is a
 // population count, and the first of them moves the warp's own counter on.  No
-// atomics: the order is the slots' own.  Few slots are sorted by one CTA in one
-// launch; many by three: each warp counts its share, each expert's counts are
-// summed over the warps, and each warp places its share.
+// atomics: the order is the slots' own.  Up to 8192 slots are sorted by one CTA,
+// up to 262,144 by a cluster of eight, whose CTAs read one another's counts, in one
+// launch; more by three launches: each warp counts its share, each expert's counts
+// are summed over the warps, and each warp places its share.
 
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
 #include "q8_rows.cuh"
 #include "sparse.h"
+#include "tcgen05.cuh"
 
 namespace rmx {
 namespace {
@@ -26,34 +28,59 @@ __device__ __forceinline__ int expert_of(const int32_t* expert, long long slot, 
   const int e = slot < end ? expert[slot] : -1;
   return (uint32_t)e < (uint32_t)E ? e : -1;
 }
+// The lanes with this lane's expert (of 2^bits), one vote a bit: 131,072 slots to 64
+// experts take 33 us with the match instruction, RMX_SORT with votes.
+__device__ __forceinline__ uint32_t same_expert(int e, int bits) {
+  uint32_t same = __ballot_sync(0xffffffffu, e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (e >> b) & 1;
+    const uint32_t ones = __ballot_sync(0xffffffffu, one);
+    same &= one ? ones : ~ones;
+  }
+  return same;  // (of no meaning where e < 0)
+}
+__device__ __forceinline__ int expert_bits(int E) { return 32 - __clz(E - 1); }
+// Loads of a warp in flight at a time.
+constexpr int kAhead = 4;
 // Slots [begin, end) of a warp (32 at a time, all lanes together) counted into
 // its own hist[E].
 __device__ __forceinline__ void count_slots(const int32_t* expert, long long begin, long long end, int E, int* hist) {
-  const int lane = threadIdx.x & 31;
-  for (long long s = begin; s < end; s += 32) {
-    const int e = expert_of(expert, s + lane, end, E);
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && (same & lanes_below()) == 0) hist[e] += __popc(same);
-    __syncwarp();
+  const int lane = threadIdx.x & 31, bits = expert_bits(E);
+  for (long long s0 = begin; s0 < end; s0 += 32 * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) id[i] = expert_of(expert, s0 + 32 * i + lane, end, E);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const uint32_t same = same_expert(id[i], bits);
+      if (id[i] >= 0 && (same & lanes_below()) == 0) hist[id[i]] += __popc(same);
+      __syncwarp();
+    }
   }
 }
 // The same slots given their places: hist[e] is the warp's next place of expert e.
 __device__ __forceinline__ void place_slots(const int32_t* expert, long long begin, long long end, int E, int* hist,
                                             int32_t* position, int32_t* source) {
-  const int lane = threadIdx.x & 31;
-  for (long long s = begin; s < end; s += 32) {
-    const long long slot = s + lane;
-    const int e = expert_of(expert, slot, end, E);
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    const uint32_t below = same & lanes_below();
-    const int first = e >= 0 ? hist[e] : 0;
-    __syncwarp();
-    if (e >= 0 && below == 0) hist[e] = first + __popc(same);
-    __syncwarp();
-    if (slot < end) {
-      const int at = e >= 0 ? first + __popc(below) : -1;
-      position[slot] = at;
-      if (e >= 0) source[at] = (int32_t)slot;
+  const int lane = threadIdx.x & 31, bits = expert_bits(E);
+  for (long long s0 = begin; s0 < end; s0 += 32 * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) id[i] = expert_of(expert, s0 + 32 * i + lane, end, E);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const long long slot = s0 + 32 * i + lane;
+      const int e = id[i];
+      const uint32_t same = same_expert(e, bits);
+      const uint32_t below = same & lanes_below();
+      const int first = e >= 0 ? hist[e] : 0;
+      __syncwarp();
+      if (e >= 0 && below == 0) hist[e] = first + __popc(same);
+      __syncwarp();
+      if (slot < end) {
+        const int at = e >= 0 ? first + __popc(below) : -1;
+        position[slot] = at;
+        if (e >= 0) source[at] = (int32_t)slot;
+      }
     }
   }
 }
@@ -85,39 +112,66 @@ __device__ __forceinline__ int block_prefix(int v, int* tmp, int& total) {
   return tmp[warp] + inc - v;
 }
 
-constexpr int kOneWarps = 32;
-constexpr int kOneSlots = 8192;  // up to here one CTA sorts by itself
+constexpr int kWarps = 32;             // of a CTA that sorts, at most
+constexpr int kOneSlots = 8192;        // up to here one CTA sorts by itself
+constexpr int kCluster = 8, kClusterSlots = 262144;
 
-__global__ void __launch_bounds__(32 * kOneWarps) k_sort_one(int S, int E, const int32_t* expert, int32_t* offsets,
-                                                             int32_t* position, int32_t* source) {
+__device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// CTAS: 1, or a cluster of kCluster, each CTA with the next kWarps shares.
+// blockDim.x >= E, and at least 32 * warps.
+template <int CTAS>
+__global__ void __launch_bounds__(32 * kWarps) k_sort(int S, int E, int warps, int share, const int32_t* expert,
+                                                      int32_t* offsets, int32_t* position, int32_t* source) {
   pdl_enter();
-  extern __shared__ int hist[];  // [warps][E]
+  extern __shared__ int hist[];  // [warps][E], then this CTA's count of each expert [E]
   __shared__ int tmp[33];
-  const int warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < kOneWarps * E; i += 32 * kOneWarps) hist[i] = 0;
+  int* mine = hist + warps * E;
+  const int warp = threadIdx.x >> 5, rank = CTAS > 1 ? (int)cluster_rank() : 0;
+  for (int i = threadIdx.x; i < warps * E; i += blockDim.x) hist[i] = 0;
   __syncthreads();
-  const int share = ((S + kOneWarps - 1) / kOneWarps + 31) / 32 * 32;
-  const int begin = min(S, warp * share), end = min(S, begin + share);
-  count_slots(expert, begin, end, E, hist + warp * E);
+  const long long begin = min((long long)S, (long long)(rank * warps + warp) * share), end = min((long long)S, begin + share);
+  if (warp < warps) count_slots(expert, begin, end, E, hist + warp * E);
   __syncthreads();
   int n = 0;
-  const int e = threadIdx.x;  // E <= 1024 threads
-  if (e < E)
-    for (int w = 0; w < kOneWarps; ++w) {
+  const int e = threadIdx.x;
+  if (e < E) {
+    for (int w = 0; w < warps; ++w) {
       const int c = hist[w * E + e];
       hist[w * E + e] = n;
       n += c;
     }
-  int total;
-  const int off = block_prefix(n, tmp, total);
-  if (e < E) {
-    offsets[e] = off;
-    for (int w = 0; w < kOneWarps; ++w) hist[w * E + e] += off;
+    mine[e] = n;
   }
-  if (threadIdx.x == 0) offsets[E] = total;
+  int all = n, base = 0;
+  if (CTAS > 1) {
+    cluster_barrier();
+    if (e < E) {
+      const uint32_t at = smem_u32(mine + e);
+      all = 0;
+#pragma unroll
+      for (int r = 0; r < CTAS; ++r) {
+        const int c = ld_cluster_s32(mapa_shared(at, (uint32_t)r));
+        base += r < rank ? c : 0;
+        all += c;
+      }
+    }
+    cluster_barrier();  // none leaves, or goes on to count, while another reads
+  }
+  int total;
+  const int off = block_prefix(e < E ? all : 0, tmp, total);
+  if (e < E) {
+    if (rank == 0) offsets[e] = off;
+    for (int w = 0; w < warps; ++w) hist[w * E + e] += off + base;
+  }
+  if (rank == 0 && threadIdx.x == 0) offsets[E] = total;
   __syncthreads();
-  place_slots(expert, begin, end, E, hist + warp * E, position, source);
-  for (int i = total + threadIdx.x; i < S; i += 32 * kOneWarps) source[i] = -1;
+  if (warp < warps) place_slots(expert, begin, end, E, hist + warp * E, position, source);
+  for (long long i = total + (long long)rank * blockDim.x + threadIdx.x; i < S; i += CTAS * blockDim.x) source[i] = -1;
 }
 
 // ws: counts [warps][E], then totals [E].
@@ -296,6 +350,80 @@ __global__ void __launch_bounds__(256) k_combine(const Units u, int S, int k, in
   }
 }
 
+// The same for rows of more than 512 columns: a warp has a segment of NCH blocks of
+// a token's row and two experts' rows of it on their way at a time, and knows the
+// next token's rows before it is done with this one.
+template <typename T, int NCH, bool VEC>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1)
+    k_combine_rows(int tokens, int S, int k, int C, const int segs, const int32_t* position, const float* weight, const T* y,
+                   T* out) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const uint32_t units = (uint32_t)tokens * (uint32_t)segs;  // segments of 1.5 KB and more: far below 2^31
+  const uint32_t step = gridDim.x * 8;
+  uint32_t u = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (u >= units) return;
+  struct Slot {
+    int p;
+    float w;
+  };
+  auto slot = [&](uint32_t t, int j) {
+    Slot s{-1, 1.f};
+    if (j < k) {
+      s.p = position[(size_t)t * k + j];
+      if (weight) s.w = weight[(size_t)t * k + j];
+    }
+    return s;
+  };
+  uint32_t t = u / (uint32_t)segs;
+  Slot a = slot(t, 0), b = slot(t, 1);
+  while (true) {
+    const int seg0 = (int)(u - t * (uint32_t)segs) * NCH;
+    const uint32_t nu = u + step, nt = nu < units ? nu / (uint32_t)segs : 0;
+    float2 acc[NCH][4];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = f2(0.f);
+    for (int j = 0; j < k; j += 2) {
+      Chunk<T> ca[NCH], cb[NCH];
+      const bool la = (uint32_t)a.p < (uint32_t)S, lb = (uint32_t)b.p < (uint32_t)S;
+      if (la) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) ca[i] = load_chunk<T, 32, VEC>(y + (size_t)a.p * C, col0<32, VEC>(seg0 + i, lane), C);
+      }
+      if (lb) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) cb[i] = load_chunk<T, 32, VEC>(y + (size_t)b.p * C, col0<32, VEC>(seg0 + i, lane), C);
+      }
+      const float wa = a.w, wb = b.w;
+      if (j + 2 < k) {
+        a = slot(t, j + 2);
+        b = slot(t, j + 3);
+      } else if (nu < units) {
+        a = slot(nt, 0);
+        b = slot(nt, 1);
+      }
+      auto add = [&](const Chunk<T> (&c)[NCH], float w) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          float2 v[4];
+          to_pairs(c[i], v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] = fma2(v[e], f2(w), acc[i][e]);
+        }
+      };
+      if (la) add(ca, wa);
+      if (lb) add(cb, wb);
+    }
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) store_chunk<T, 32, VEC>(out + (size_t)t * C, col0<32, VEC>(seg0 + i, lane), C, acc[i]);
+    if (nu >= units) return;
+    u = nu;
+    t = nt;
+  }
+}
+
 // A token belongs to L lanes of W warps with NCH blocks each, dout's row in
 // registers while its k rows of y pass.
 template <typename T, int L, int NCH, bool VEC>
@@ -379,6 +507,14 @@ cudaError_t combine(const Routes& r, const int32_t* position, const float* weigh
                     (T*)out);
   };
   if (r.C <= 64) return go(k_combine<T, 8, VEC>, units_of<8>(r.T, r.C), 32);
+  const int blocks = (r.C + 255) / 256;
+  if (blocks > 2) {
+    const int segs = (blocks + 4) / 5, nch = (blocks + segs - 1) / segs;
+    auto k = nch == 3 ? k_combine_rows<T, 3, VEC> : nch == 4 ? k_combine_rows<T, 4, VEC> : k_combine_rows<T, 5, VEC>;
+    const long long want = ((long long)r.T * segs + 7) / 8, fit = (sizeof(T) == 2 ? 2ll : 1ll) * sm_count();
+    return launch_k(k, dim3((unsigned)(want < fit ? want : fit)), dim3(256), 0, st, 1, r.T, r.S, r.k, r.C, segs, position,
+                    weight, (const T*)y, (T*)out);
+  }
   return go(k_combine<T, 32, VEC>, units_of<32>(r.T, r.C), 8);
 }
 template <typename T, bool VEC>
@@ -403,7 +539,7 @@ cudaError_t combine_bwd(const Routes& r, const int32_t* position, const float* w
 
 int sort_warps(int S, int E) {
   (void)E;
-  if (S <= kOneSlots) return 0;
+  if (S <= kClusterSlots) return 0;
   const int share = share_of(S);
   return (int)(((long long)S + share - 1) / share);
 }
@@ -412,11 +548,18 @@ cudaError_t launch_expert_sort(const Routes& r, const int32_t* expert, int32_t* 
                                int32_t* source, int32_t* ws, int pass, cudaStream_t st) {
   const int warps = sort_warps(r.S, r.E), E = r.E;
   if (warps == 0) {
-    const int smem = kOneWarps * E * (int)sizeof(int);  // 128 KB at most
-    cudaError_t e = cudaFuncSetAttribute(k_sort_one, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kOneWarps * kMaxExperts * (int)sizeof(int));
+    const bool one = r.S <= kOneSlots;
+    // A warp to every 32 slots, up to what the CTAs have.
+    const int most = (r.S + 31) / 32, nw = !one ? kWarps : most < 1 ? 1 : most < kWarps ? most : kWarps;
+    const int all = one ? nw : kCluster * kWarps, share = ((r.S + all - 1) / all + 31) / 32 * 32;
+    const int threads = 32 * nw > (E + 31) / 32 * 32 ? 32 * nw : (E + 31) / 32 * 32;
+    const int smem = (nw + 1) * E * (int)sizeof(int);  // 132 KB at most
+    auto k = one ? k_sort<1> : k_sort<kCluster>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (kWarps + 1) * kMaxExperts * (int)sizeof(int));
     if (e != cudaSuccess) return e;
-    return launch_k(k_sort_one, dim3(1), dim3(32 * kOneWarps), smem, st, 1, r.S, E, expert, offsets, position, source);
+    return launch_k(k, dim3(one ? 1 : kCluster), dim3(threads), smem, st, one ? 1 : kCluster, r.S, E, nw, share, expert, offsets,
+                    position, source);
   }
   const int share = share_of(r.S), ctas = (warps + kManyWarps - 1) / kManyWarps;
   int32_t* totals = ws + (size_t)warps * E;
