@@ -31,14 +31,14 @@ __device__ __forceinline__ DropBits drop_bits(const Drop& d) {
 }
 
 // The eight columns 8 * grp .. 8 * grp + 7 of a row: 16 bits each, two to a word,
-// the lower half first.  N groups, 32 apart, round by round: a round of one
-// depends on the one before, and the groups fill one another's latency.
+// the lower half first.  N groups, round by round: they share the keys, and fill
+// one another's latency.
 template <int N>
-__device__ __forceinline__ void bits8(const DropBits& b, long long row, int grp, uint32_t (&c)[N][4]) {
+__device__ __forceinline__ void bits8(const DropBits& b, const long long (&row)[N], const int (&grp)[N], uint32_t (&c)[N][4]) {
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    c[n][0] = (uint32_t)(grp + 32 * n) | (uint32_t)(row >> 32) << 24;
-    c[n][1] = (uint32_t)row;
+    c[n][0] = (uint32_t)grp[n] | (uint32_t)(row[n] >> 32) << 24;
+    c[n][1] = (uint32_t)row[n];
     c[n][2] = b.o0;
     c[n][3] = b.o1;
   }
@@ -69,24 +69,16 @@ __device__ __forceinline__ uint32_t keep_mask(const DropBits& b, const uint32_t 
 // Which of one group's are kept, a bit each.
 __device__ __forceinline__ uint32_t keep8(const DropBits& b, long long row, int grp) {
   uint32_t w[1][4];
-  bits8<1>(b, row, grp, w);
+  bits8<1>(b, {row}, {grp}, w);
   return keep_mask(b, w[0]);
 }
-// v * scale where kept, exactly 0 elsewhere, by the words or the bits.
+// v * scale where kept, exactly 0 elsewhere.
 __device__ __forceinline__ void drop_by_words(const DropBits& b, float scale, const uint32_t (&w)[4], float2 (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 s = mul2(v[i], f2(scale));
     v[i].x = (w[i] << 16) >= b.lim ? s.x : 0.f;
     v[i].y = w[i] >= b.lim ? s.y : 0.f;
-  }
-}
-__device__ __forceinline__ void drop_by_mask(uint32_t keep, float scale, float2 (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 s = mul2(v[i], f2(scale));
-    v[i].x = keep & (1u << (2 * i)) ? s.x : 0.f;
-    v[i].y = keep & (2u << (2 * i)) ? s.y : 0.f;
   }
 }
 
@@ -104,7 +96,7 @@ __device__ __forceinline__ void drop_values(const DropBits& b, float scale, long
   }
   if constexpr (VEC) {
     uint32_t w[1][4];
-    bits8<1>(b, row, c0 >> 3, w);
+    bits8<1>(b, {row}, {c0 >> 3}, w);
     drop_by_words(b, scale, w[0], v);
   } else {
     const int sub = threadIdx.x & 7;

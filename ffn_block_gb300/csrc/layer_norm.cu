@@ -53,7 +53,7 @@ template <int L, bool VEC> __device__ __forceinline__ void mask_end(float2 (&v)[
 // kUnits units at a time, so that their loads are in flight together.
 constexpr int kUnits = 4;
 template <typename T, int L, bool VEC>
-__global__ void __launch_bounds__(256) k_dropout(long long row0, uint32_t units, int bpr, int C, const Drop d,
+__global__ void __launch_bounds__(256) k_dropout(long long row0, uint32_t units, int bpr, int step_row, int step_blk, int C, const Drop d,
                                                  const T* x, const T* r, T* out) {
   pdl_enter();
   const int lane = threadIdx.x & (L - 1);
@@ -64,13 +64,16 @@ __global__ void __launch_bounds__(256) k_dropout(long long row0, uint32_t units,
   long long row[kUnits];
   int c0[kUnits];
   bool live[kUnits];
+  // One division; from unit to unit PER blocks on.
+  uint32_t ur = u0 / (uint32_t)bpr, blk = u0 - ur * (uint32_t)bpr;
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
-    const uint32_t u = u0 + (uint32_t)(j * PER);
-    live[j] = u < units;
-    const uint32_t ur = live[j] ? u / (uint32_t)bpr : 0u;
-    row[j] = row0 + ur;
-    c0[j] = col0<L, VEC>(live[j] ? (int)(u - ur * (uint32_t)bpr) : 0, lane);
+    live[j] = u0 + (uint32_t)(j * PER) < units;
+    row[j] = live[j] ? row0 + ur : row0;
+    c0[j] = col0<L, VEC>(live[j] ? (int)blk : 0, lane);
+    blk += (uint32_t)step_blk;
+    ur += (uint32_t)step_row + (blk >= (uint32_t)bpr ? 1u : 0u);
+    blk -= blk >= (uint32_t)bpr ? (uint32_t)bpr : 0u;
     const int end = live[j] ? C : 0;
     cx[j] = load_chunk<T, L, VEC>(x + (size_t)row[j] * C, c0[j], end);
     if (r) cr[j] = load_chunk<T, L, VEC>(r + (size_t)row[j] * C, c0[j], end);
@@ -100,7 +103,7 @@ cudaError_t dropout(long long R, int C, const Drop& d, const void* x, const void
     const uint32_t units = (uint32_t)(rows * bpr);
     const uint32_t per = 256 / L * kUnits;
     cudaError_t e = launch_k(k_dropout<T, L, VEC>, dim3((units + per - 1) / per), dim3(256), 0, st, 1, row0, units, bpr,
-                             C, d, (const T*)x, (const T*)r, (T*)out);
+                             256 / L / bpr, 256 / L % bpr, C, d, (const T*)x, (const T*)r, (T*)out);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -109,50 +112,73 @@ template <typename T>
 cudaError_t dropout_t(long long R, int C, const Drop& d, const void* x, const void* r, void* out, cudaStream_t st) {
   const bool vec = rows_aligned(C, sizeof(T));
   if (C <= 64) return vec ? dropout<T, 8, true>(R, C, d, x, r, out, st) : dropout<T, 8, false>(R, C, d, x, r, out, st);
+  if (C <= 128) return vec ? dropout<T, 16, true>(R, C, d, x, r, out, st) : dropout<T, 16, false>(R, C, d, x, r, out, st);
   return vec ? dropout<T, 32, true>(R, C, d, x, r, out, st) : dropout<T, 32, false>(R, C, d, x, r, out, st);
 }
 
 // ---------------------------------------------------------------- rows through shared memory
-// Rows of whole 16-byte vectors longer than 512 columns.  A warp has a segment
-// of NCH blocks of 256 columns of a row (rows of up to 1280 columns belong to
-// one warp) and brings its rows in with bulk copies into shared memory of its
-// own, `depth` rows ahead: what is in flight takes no registers, which hold the
-// row's values and (backward) the column sums, 16 a block.  Warps meet only where
-// a row has several.
+// Rows longer than 512 columns.  A warp has a segment of NCH blocks of 256 columns
+// of a row (rows of up to 1280 columns belong to one warp) and brings its rows in
+// with bulk copies into shared memory of its own, `depth` rows ahead: what is in
+// flight takes no registers, which hold the row's values and (backward) the column
+// sums, 16 a block.  Warps meet only where a row has several.
+//
+// VEC: rows start on 16-byte boundaries.  Else a copy brings the 16-byte vectors
+// that a segment lies in, and the segment starts inside the first of them; of the
+// tensor's last vector, where it is not a whole one, the elements are loaded one
+// by one.
 constexpr int kRingSmem = 200 * 1024, kRingMaxDepth = 3, kRingParams = 24 * 1024;
 constexpr uint64_t kDrainNs = 50ull * 1000ull * 1000ull;
-template <typename T, int SEG> struct RowRing {
-  T* base;            // [depth][nt][SEG]
+template <typename T, bool VEC> constexpr int ring_pitch(int nch) { return nch * 256 + (VEC ? 0 : 32 / (int)sizeof(T)); }
+template <typename T, int NCH, bool VEC> struct RowRing {
+  static constexpr int SEG = NCH * 256, PITCH = ring_pitch<T, VEC>(NCH);
+  T* base;            // [depth][nt][PITCH]
   uint32_t bar0;      // depth barriers
   const T* src[3];
-  int nt, depth, seg0, C;
-  uint32_t bytes;     // of a segment
+  int nt, depth, seg0, seg, C;
   long long R, step;
   int s;              // the stage of the row at hand, and its parity
   uint32_t ph;
   bool failed;
 
+  // The bytes of a segment that copies bring, from its first vector on.
+  __device__ __forceinline__ void range(long long row, size_t& from, uint32_t& bytes) const {
+    const size_t b0 = ((size_t)row * C + seg0) * sizeof(T), b1 = b0 + (size_t)seg * sizeof(T);
+    from = VEC ? b0 : b0 & ~(size_t)15;
+    const size_t all = (size_t)R * C * sizeof(T) & ~(size_t)15, up = (b1 + 15) & ~(size_t)15;
+    bytes = (uint32_t)((VEC ? b1 : up < all ? up : all) - from);
+  }
   __device__ __forceinline__ void issue(long long row, int stage) const {
     if ((threadIdx.x & 31) != 0 || row >= R) return;
-    const uint32_t bar = bar0 + 8u * (uint32_t)stage, dst = smem_u32(base + (size_t)stage * nt * SEG);
-    const size_t at = (size_t)row * C + seg0;
+    const uint32_t bar = bar0 + 8u * (uint32_t)stage, dst = smem_u32(base + (size_t)stage * nt * PITCH);
+    size_t from;
+    uint32_t bytes;
+    range(row, from, bytes);
     mbar_arrive_expect_tx(bar, bytes * (uint32_t)nt);
 #pragma unroll
     for (int i = 0; i < 3; ++i)
-      if (i < nt) bulk_g2s(dst + (uint32_t)(i * SEG * (int)sizeof(T)), src[i] + at, bytes, bar);
+      if (i < nt)
+        bulk_g2s(dst + (uint32_t)(i * PITCH * (int)sizeof(T)), reinterpret_cast<const char*>(src[i]) + from, bytes, bar);
   }
-  // Eight values of the row at hand (its segment's columns past the row's end are
-  // zeros, written once).
-  static __device__ __forceinline__ Chunk<T> load(const T* p) {
+  // Eight values of a tensor of the row at hand, block j of the segment; zeros past
+  // its end (VEC: written once, by init).
+  __device__ __forceinline__ Chunk<T> load(const T* row, int tensor, int j) const {
+    const int lane = threadIdx.x & 31;
+    const T* p = row + tensor * PITCH;
+    if constexpr (VEC) return whole(p + j * 256 + lane * 8);
+    else return load_chunk<T, 32, false>(p, j * 256 + lane, seg);
+  }
+  static __device__ __forceinline__ Chunk<T> whole(const T* p) {
     Chunk<T> k;
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(&k)[i] = reinterpret_cast<const uint4*>(p)[i];
     return k;
   }
   // The warp's barriers; before the block meets.
-  __device__ __forceinline__ void init(int seg) {
-    for (int i = 0; i < depth * nt; ++i)
-      for (int c = seg + (int)(threadIdx.x & 31); c < SEG; c += 32) base[i * SEG + c] = from_f<T>(0.f);
+  __device__ __forceinline__ void init() {
+    if (VEC)
+      for (int i = 0; i < depth * nt; ++i)
+        for (int c = seg + (int)(threadIdx.x & 31); c < SEG; c += 32) base[i * PITCH + c] = from_f<T>(0.f);
     if ((threadIdx.x & 31) == 0) {
       for (int i = 0; i < depth; ++i) mbar_init(bar0 + 8u * (uint32_t)i, 1);
       fence_mbar_init();
@@ -164,15 +190,31 @@ template <typename T, int SEG> struct RowRing {
   __device__ __forceinline__ void start(long long row0) const {
     for (int i = 0; i < depth; ++i) issue(row0 + i * step, i);
   }
-  // Waits for the row at hand.  A wait that gives up leaves the block's barriers
-  // in step: the warp goes on (with what it finds), waits no more and issues
-  // nothing.
-  __device__ __forceinline__ const T* wait(unsigned long long limit, unsigned int* err, volatile int* abort) {
+  // Waits for the row at hand, and returns where its segment starts.  A wait that
+  // gives up leaves the block's barriers in step: the warp goes on (with what it
+  // finds), waits no more and issues nothing.
+  __device__ __forceinline__ const T* wait(long long row, unsigned long long limit, unsigned int* err, volatile int* abort) {
     if (!failed) {
       const bool ok = mbar_wait_bounded(bar0 + 8u * (uint32_t)s, ph, limit, err, ERRBIT_WAIT_ROWS, abort);
       failed = !__all_sync(0xffffffffu, ok);
     }
-    return base + (size_t)s * nt * SEG;
+    T* stage = base + (size_t)s * nt * PITCH;
+    if constexpr (VEC) return stage;
+    size_t from;
+    uint32_t bytes;
+    range(row, from, bytes);
+    const size_t b0 = ((size_t)row * C + seg0) * sizeof(T);
+    T* in = stage + (b0 - from) / sizeof(T);
+    const int there = (int)((from + bytes - b0) / sizeof(T)), lane = threadIdx.x & 31;
+    if (there < seg) {
+      if (there + lane < seg) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (i < nt) in[i * PITCH + there + lane] = src[i][b0 / sizeof(T) + there + lane];
+      }
+      __syncwarp();
+    }
+    return in;
   }
   // The row has been read: its stage takes the one `depth` rows on.  The copy is of
   // the async proxy: a proxy fence orders the warp's reads before its writes.
@@ -210,7 +252,7 @@ RingSpread ring_spread(long long R, int C, int dtype, int nt, int threads) {
   const int blocks = (C + 255) / 256;
   s.W = (blocks + 4) / 5;
   s.nch = (blocks + s.W - 1) / s.W;
-  const int row_bytes = nt * s.nch * 256 * (dtype == 0 ? 4 : 2);
+  const int e = dtype == 0 ? 4 : 2, row_bytes = nt * (s.nch * 256 * e + (rows_aligned(C, e) ? 0 : 32));
   int warps = kRingSmem / (2 * row_bytes);
   if (warps > threads / 32) warps = threads / 32;
   s.rpb = warps / s.W;
@@ -225,7 +267,7 @@ RingSpread ring_spread(long long R, int C, int dtype, int nt, int threads) {
 
 // ---------------------------------------------------------------- forward
 constexpr int kFwdRingThreads = 512, kBwdRingThreads = 256;
-template <typename T, int NCH>
+template <typename T, int NCH, bool VEC>
 __global__ void __launch_bounds__(kFwdRingThreads, 1)
     k_layer_norm_ring(const LnFwd a, const int W, const int rpb, const int depth, const bool staged, unsigned int* err,
                       const unsigned long long limit) {
@@ -237,20 +279,20 @@ __global__ void __launch_bounds__(kFwdRingThreads, 1)
   __shared__ int abort_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rib = warp / W, w = warp - rib * W;
   const int seg0 = w * SEG, seg = min(SEG, a.C - seg0);
-  RowRing<T, SEG> ring;
+  RowRing<T, NCH, VEC> ring;
   ring.nt = a.r ? 2 : 1;
   ring.depth = depth;
-  ring.base = reinterpret_cast<T*>(ring_smem) + (size_t)warp * (depth * ring.nt * SEG);
+  ring.base = reinterpret_cast<T*>(ring_smem) + (size_t)warp * (depth * ring.nt * ring.PITCH);
   ring.bar0 = smem_u32(bars + kRingMaxDepth * warp);
   ring.src[0] = static_cast<const T*>(a.x);
   ring.src[1] = static_cast<const T*>(a.r);
   ring.src[2] = nullptr;
   ring.seg0 = seg0;
   ring.C = a.C;
-  ring.bytes = (uint32_t)(seg * (int)sizeof(T));
+  ring.seg = seg;
   ring.R = a.R;
   ring.step = (long long)gridDim.x * rpb;
-  ring.init(seg);
+  ring.init();
   if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
   pdl_wait();
@@ -260,36 +302,38 @@ __global__ void __launch_bounds__(kFwdRingThreads, 1)
   const float inv_n = 1.f / (float)a.C;
   float* my_red = red + rib * 2 * W;
   // gamma and beta in shared memory behind the ring, where they fit.
-  T* const held = reinterpret_cast<T*>(ring_smem) + (size_t)rpb * W * (depth * ring.nt * SEG);
+  T* const held = reinterpret_cast<T*>(ring_smem) + (size_t)rpb * W * (depth * ring.nt * ring.PITCH);
   const int pitch = W * SEG;
   if (staged) {
-    for (int c = 8 * (int)threadIdx.x; c < a.C; c += 8 * (int)blockDim.x) {
-      if (a.gamma) *reinterpret_cast<Chunk<T>*>(held + c) = load_chunk<T, 32, true>(static_cast<const T*>(a.gamma), c, a.C);
-      if (a.beta) *reinterpret_cast<Chunk<T>*>(held + pitch + c) = load_chunk<T, 32, true>(static_cast<const T*>(a.beta), c, a.C);
+    constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;
+    using U = typename std::conditional<VEC, uint4, T>::type;
+    for (int c = V * (int)threadIdx.x; c < a.C; c += V * (int)blockDim.x) {
+      if (a.gamma) *reinterpret_cast<U*>(held + c) = *reinterpret_cast<const U*>(static_cast<const T*>(a.gamma) + c);
+      if (a.beta) *reinterpret_cast<U*>(held + pitch + c) = *reinterpret_cast<const U*>(static_cast<const T*>(a.beta) + c);
     }
     __syncthreads();
   }
   auto param = [&](const void* p, int i, int c) {
-    return staged ? ring.load(held + i * pitch + c) : load_chunk<T, 32, true>(static_cast<const T*>(p), c, a.C);
+    return load_chunk<T, 32, VEC>(staged ? held + i * pitch : static_cast<const T*>(p), c, a.C);
   };
   long long gave_up = row0;
   for (long long row = row0; row < a.R; row += ring.step) {
-    const T* in = ring.wait(limit, err, &abort_flag);
+    const T* in = ring.wait(row, limit, err, &abort_flag);
     if (!ring.failed) gave_up = row + ring.step;
     const size_t at = (size_t)row * a.C;
     float2 v[NCH][4], s2 = f2(0.f);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int c = j * 256 + lane * 8, c0 = seg0 + c;
-      to_pairs(ring.load(in + c), v[j]);
-      drop_values<32, true>(bits, a.drop.scale, row, c0, v[j]);
+      const int c0 = seg0 + col0<32, VEC>(j, lane);
+      to_pairs(ring.load(in, 0, j), v[j]);
+      drop_values<32, VEC>(bits, a.drop.scale, row, c0, v[j]);
       if (a.r) {
         float2 r[4];
-        to_pairs(ring.load(in + SEG + c), r);
+        to_pairs(ring.load(in, 1, j), r);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], r[i]);
       }
-      if (a.h) store_chunk<T, 32, true>(static_cast<T*>(a.h) + at, c0, a.C, v[j]);
+      if (a.h) store_chunk<T, 32, VEC>(static_cast<T*>(a.h) + at, c0, a.C, v[j]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s2 = add2(s2, v[j][i]);
     }
@@ -302,7 +346,7 @@ __global__ void __launch_bounds__(kFwdRingThreads, 1)
     for (int j = 0; j < NCH; ++j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], f2(-mean));
-      if (seg != SEG) mask_end<32, true>(v[j], seg0 + j * 256 + lane * 8, a.C);
+      if (seg != SEG) mask_end<32, VEC>(v[j], seg0 + col0<32, VEC>(j, lane), a.C);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s2 = fma2(v[j][i], v[j][i], s2);
     }
@@ -319,24 +363,25 @@ __global__ void __launch_bounds__(kFwdRingThreads, 1)
       for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], f2(rstd));
       float2 g[4], b[4];
       if (a.gamma) {
-        to_pairs(param(a.gamma, 0, seg0 + j * 256 + lane * 8), g);
+        to_pairs(param(a.gamma, 0, seg0 + col0<32, VEC>(j, lane)), g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], g[i]);
       }
       if (a.beta) {
-        to_pairs(param(a.beta, 1, seg0 + j * 256 + lane * 8), b);
+        to_pairs(param(a.beta, 1, seg0 + col0<32, VEC>(j, lane)), b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], b[i]);
       }
-      store_chunk<T, 32, true>(static_cast<T*>(a.y) + at, seg0 + j * 256 + lane * 8, a.C, v[j]);
+      store_chunk<T, 32, VEC>(static_cast<T*>(a.y) + at, seg0 + col0<32, VEC>(j, lane), a.C, v[j]);
     }
   }
   ring.drain(gave_up, err);
 }
-template <typename T> cudaError_t layer_norm_ring(const LnFwd& a, const RingSpread& s, cudaStream_t st) {
-  auto k = s.nch == 3 ? k_layer_norm_ring<T, 3> : s.nch == 4 ? k_layer_norm_ring<T, 4> : k_layer_norm_ring<T, 5>;
+template <typename T, bool VEC> cudaError_t layer_norm_ring(const LnFwd& a, const RingSpread& s, cudaStream_t st) {
+  auto k = s.nch == 3 ? k_layer_norm_ring<T, 3, VEC> : s.nch == 4 ? k_layer_norm_ring<T, 4, VEC> : k_layer_norm_ring<T, 5, VEC>;
   const int params = 2 * s.W * s.nch * 256 * (int)sizeof(T);
-  const bool staged = (a.gamma || a.beta) && params <= kRingParams;
+  // (Worth its wait where a warp has several rows.)
+  const bool staged = (a.gamma || a.beta) && params <= kRingParams && a.R > 4ll * s.rpb * sm_count();
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem + kRingParams);
   if (e != cudaSuccess) return e;
   const long long want = (a.R + s.rpb - 1) / s.rpb;
@@ -344,82 +389,104 @@ template <typename T> cudaError_t layer_norm_ring(const LnFwd& a, const RingSpre
                   s.smem + (staged ? params : 0), st, 1, a, s.W, s.rpb, s.depth, staged, device_error_word(), (unsigned long long)kWaitLimitNs);
 }
 
-// Other rows: a row belongs to L lanes of W warps (W > 1 only with L = 32), with NCH blocks
-// of 8 * L columns each; rpb rows at a time to a thread block.
-// One block after another on an SM's resident ones starts each with its loads
+// Other rows: a row belongs to L lanes of W warps (W > 1 only with L = 32), with
+// NCH blocks of 8 * L columns each; rpb rows at a time to a thread block, RB of
+// them to each thread (W = 1), whose loads and shuffles are in flight together.
+// One block after another on an SM's resident ones would start each with its loads
 // exposed: the grid is what fits at once, and blocks go through the rows.
-template <int NCH> constexpr int fwd_blocks = NCH == 1 ? 6 : NCH == 2 ? 4 : 2;
-template <typename T, int L, int NCH, bool VEC, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? fwd_blocks<NCH> : 1) k_layer_norm(const LnFwd a, const int W, const int rpb) {
+constexpr int kFwdBlocks = 2;  // an SM (three, four or six of them spill and are slower)
+template <typename T, int L, int NCH, int RB, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? kFwdBlocks : 1) k_layer_norm(const LnFwd a, const int W, const int rpb) {
   pdl_enter();
   __shared__ float red[64];
   const int lane = threadIdx.x & (L - 1), part = threadIdx.x / L, rib = part / W, w = part - rib * W;
   const DropBits bits = drop_bits(a.drop);
   const float inv_n = 1.f / (float)a.C;
-  float* my_red = red + rib * 2 * W;
+  float* my_red = red + rib * 2 * RB * W;
   const long long step = (long long)gridDim.x * rpb;
-  const int first_of_warp = L == 32 ? rib : (threadIdx.x >> 5) * (32 / L);
   auto c_of = [&](int j) { return col0<L, VEC>(w + j * W, lane); };
-  for (long long row = (long long)blockIdx.x * rpb + rib; row - rib + first_of_warp < a.R; row += step) {
-    const bool live = L == 32 || row < a.R;
-    const size_t at = (size_t)(live ? row : 0) * a.C;
-    const int C = live ? a.C : 0;
-    Chunk<T> cx[NCH], cr[NCH];
+  // Parts of a warp stay in the loop together (their shuffles take every lane).
+  const int first_of_warp = L == 32 ? rib : (threadIdx.x >> 5) * (32 / L);
+  for (long long row0 = (long long)blockIdx.x * rpb + rib; row0 - rib + first_of_warp < a.R; row0 += RB * step) {
+    Chunk<T> cx[RB][NCH], cr[RB][NCH];
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      cx[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.x) + at, c_of(j), C);
-      if (a.r) cr[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.r) + at, c_of(j), C);
-    }
-    float2 v[NCH][4], s2 = f2(0.f);
+    for (int r = 0; r < RB; ++r) {
+      const long long row = row0 + r * step;
+      const bool live = row < a.R;
+      const size_t at = (size_t)(live ? row : 0) * a.C;
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      to_pairs(cx[j], v[j]);
-      drop_values<L, VEC>(bits, a.drop.scale, row, c_of(j), v[j]);
-      if (a.r) {
-        float2 r[4];
-        to_pairs(cr[j], r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], r[i]);
+      for (int j = 0; j < NCH; ++j) {
+        cx[r][j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.x) + at, c_of(j), live ? a.C : 0);
+        if (a.r) cr[r][j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.r) + at, c_of(j), live ? a.C : 0);
       }
-      if (a.h && live) store_chunk<T, L, VEC>(static_cast<T*>(a.h) + at, c_of(j), a.C, v[j]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s2 = add2(s2, v[j][i]);
     }
-    float s[1] = {s2.x + s2.y};
-    row_sums<L, 1>(s, my_red, 0, w, W, 1 + rib);
-    const float mean = s[0] * inv_n;
-    s2 = f2(0.f);
+    float2 v[RB][NCH][4];
+    float s[RB], mean[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const long long row = row0 + r * step;
+      float2 s2 = f2(0.f);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        float2(&u)[4] = v[r][j];
+        to_pairs(cx[r][j], u);
+        drop_values<L, VEC>(bits, a.drop.scale, row, c_of(j), u);
+        if (a.r) {
+          float2 t[4];
+          to_pairs(cr[r][j], t);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[i] = add2(u[i], t[i]);
+        }
+        if (a.h && row < a.R) store_chunk<T, L, VEC>(static_cast<T*>(a.h) + (size_t)row * a.C, c_of(j), a.C, u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s2 = add2(s2, u[i]);
+      }
+      s[r] = s2.x + s2.y;
+    }
+    row_sums<L, RB>(s, my_red, 0, w, W, 1 + rib);
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      mean[r] = s[r] * inv_n;
+      float2 s2 = f2(0.f);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        float2(&u)[4] = v[r][j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = add2(u[i], f2(-mean[r]));
+        mask_end<L, VEC>(u, c_of(j), a.C);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s2 = fma2(u[i], u[i], s2);
+      }
+      s[r] = s2.x + s2.y;
+    }
+    row_sums<L, RB>(s, my_red, 1, w, W, 1 + rib);
+    float rstd[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const long long row = row0 + r * step;
+      rstd[r] = 1.f / sqrtf(s[r] * inv_n + a.eps);
+      if (row < a.R && w == 0 && lane == 0) {
+        if (a.mean) a.mean[row] = mean[r];
+        if (a.rstd) a.rstd[row] = rstd[r];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
+      float2 g[4], b[4];
+      if (a.gamma) to_pairs(load_chunk<T, L, VEC>(static_cast<const T*>(a.gamma), c_of(j), a.C), g);
+      if (a.beta) to_pairs(load_chunk<T, L, VEC>(static_cast<const T*>(a.beta), c_of(j), a.C), b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], f2(-mean));
-      mask_end<L, VEC>(v[j], c_of(j), a.C);
+      for (int r = 0; r < RB; ++r) {
+        const long long row = row0 + r * step;
+        float2(&u)[4] = v[r][j];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s2 = fma2(v[j][i], v[j][i], s2);
-    }
-    s[0] = s2.x + s2.y;
-    row_sums<L, 1>(s, my_red, 1, w, W, 1 + rib);
-    const float rstd = 1.f / sqrtf(s[0] * inv_n + a.eps);
-    if (live && w == 0 && lane == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
-    }
-#pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], f2(rstd));
-      float2 g[4];
-      if (a.gamma) {
-        to_pairs(load_chunk<T, L, VEC>(static_cast<const T*>(a.gamma), c_of(j), a.C), g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], g[i]);
+        for (int i = 0; i < 4; ++i) {
+          u[i] = mul2(u[i], f2(rstd[r]));
+          if (a.gamma) u[i] = mul2(u[i], g[i]);
+          if (a.beta) u[i] = add2(u[i], b[i]);
+        }
+        if (row < a.R) store_chunk<T, L, VEC>(static_cast<T*>(a.y) + (size_t)row * a.C, c_of(j), a.C, u);
       }
-      if (a.beta) {
-        to_pairs(load_chunk<T, L, VEC>(static_cast<const T*>(a.beta), c_of(j), a.C), g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], g[i]);
-      }
-      if (live) store_chunk<T, L, VEC>(static_cast<T*>(a.y) + at, c_of(j), a.C, v[j]);
     }
   }
 }
@@ -427,118 +494,139 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? fwd_blocks<NCH> : 1) k_lay
 struct Spread {
   int L, W, nch, rpb, threads;
 };
-// Up to 1280 columns a warp (or a part of it) has the row to itself, without a
-// barrier; above, as few warps as hold it with four blocks each.
+// Up to 512 columns a warp (or a part of it) has the row to itself, without a
+// barrier; above (the rows that the rings do not hold), warps with four blocks each.
 Spread fwd_spread(int C) {
   Spread s;
   const int blocks = (C + 255) / 256;
   s.L = C <= 64 ? 8 : C <= 128 ? 16 : 32;
-  s.nch = blocks <= 1 ? 1 : blocks == 2 ? 2 : blocks == 5 ? 5 : 4;
+  s.nch = blocks <= 2 ? blocks : 4;
   s.W = (blocks + s.nch - 1) / s.nch;
   s.rpb = s.W == 1 ? 256 / s.L : s.W < 8 ? 8 / s.W : 1;
   s.threads = s.L * s.W * s.rpb;
   return s;
 }
 template <typename T, bool VEC> cudaError_t layer_norm(const LnFwd& a, cudaStream_t st) {
-  if constexpr (VEC) {
+  if (a.C > 512) {
     const RingSpread r = ring_spread(a.R, a.C, a.dtype, a.r ? 2 : 1, kFwdRingThreads);
-    if (a.C > 512 && r.rpb >= 1 && r.W <= 16) return layer_norm_ring<T>(a, r, st);
+    if (r.rpb >= 1) return layer_norm_ring<T, VEC>(a, r, st);
   }
   const Spread s = fwd_spread(a.C);
-  auto go = [&](auto k, int per_sm) {
-    const long long want = (a.R + s.rpb - 1) / s.rpb, most = (long long)sm_count() * per_sm;
-    return launch_k(k, dim3((unsigned)(want < most ? want : most)), dim3(s.threads), 0, st, 1, a, s.W, s.rpb);
+  auto go = [&](auto k, int rb) {
+    const long long share = (long long)s.rpb * rb, want = (a.R + share - 1) / share, most = (long long)sm_count() * kFwdBlocks;
+    // Few rows: as many blocks as there are rows to give them.
+    const long long few = (a.R + s.rpb - 1) / s.rpb, least = few < sm_count() ? few : sm_count();
+    const long long grid = want < least ? least : want < most ? want : most;
+    return launch_k(k, dim3((unsigned)grid), dim3(s.threads), 0, st, 1, a, s.W, s.rpb);
   };
-  if (s.L == 8) return go(k_layer_norm<T, 8, 1, VEC, 256>, fwd_blocks<1>);
-  if (s.L == 16) return go(k_layer_norm<T, 16, 1, VEC, 256>, fwd_blocks<1>);
-  if (s.nch == 1) return go(k_layer_norm<T, 32, 1, VEC, 256>, fwd_blocks<1>);
-  if (s.nch == 2) return go(k_layer_norm<T, 32, 2, VEC, 256>, fwd_blocks<2>);
-  if (s.nch == 5) return go(k_layer_norm<T, 32, 5, VEC, 256>, fwd_blocks<5>);
-  if (s.threads <= 256) return go(k_layer_norm<T, 32, 4, VEC, 256>, fwd_blocks<4>);
-  return go(k_layer_norm<T, 32, 4, VEC, 512>, 1);
+  if (s.L == 8) return go(k_layer_norm<T, 8, 1, 4, VEC, 256>, 4);
+  if (s.L == 16) return go(k_layer_norm<T, 16, 1, 4, VEC, 256>, 4);
+  if (s.nch == 1) return go(k_layer_norm<T, 32, 1, 4, VEC, 256>, 4);
+  if (s.nch == 2) return go(k_layer_norm<T, 32, 2, 2, VEC, 256>, 2);
+  return go(k_layer_norm<T, 32, 4, 1, VEC, 512>, 1);
 }
 
 // ---------------------------------------------------------------- backward
-template <typename T, int L, int NCH, bool VEC>
-__global__ void __launch_bounds__(512) k_layer_norm_bwd(const LnBwd a, const int W, const int rpb) {
+// Other rows, as in the forward.
+template <typename T, int L, int NCH, int RB, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_layer_norm_bwd(const LnBwd a, const int W, const int rpb) {
   pdl_enter();
-  __shared__ float red[128];
+  __shared__ float red[64];
   extern __shared__ float cols[];  // partials of the block's sets of warps, [sets - 1][2][C]
   const int lane = threadIdx.x & (L - 1), part = threadIdx.x / L, rib = part / W, w = part - rib * W;
   const DropBits bits = drop_bits(a.drop);
   const float inv_n = 1.f / (float)a.C;
-  float* my_red = red + rib * 4 * W;
+  float* my_red = red + rib * 4 * RB * W;
   auto c_of = [&](int j) { return col0<L, VEC>(w + j * W, lane); };
   float2 ag[NCH][4], ab[NCH][4];
+  Chunk<T> gm[NCH];
 #pragma unroll
-  for (int j = 0; j < NCH; ++j)
+  for (int j = 0; j < NCH; ++j) {
+    if (a.gamma) gm[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.gamma), c_of(j), a.C);
 #pragma unroll
     for (int i = 0; i < 4; ++i) ag[j][i] = ab[j][i] = f2(0.f);
+  }
   const long long step = (long long)gridDim.x * rpb;
   int slot = 0;
   const int first_of_warp = L == 32 ? rib : (threadIdx.x >> 5) * (32 / L);
-  for (long long row = (long long)blockIdx.x * rpb + rib; row - rib + first_of_warp < a.R; row += step, slot ^= 1) {
-    const bool live = L == 32 || row < a.R;
-    const size_t at = (size_t)(live ? row : 0) * a.C;
-    const int C = live ? a.C : 0;
-    Chunk<T> cy[NCH], ch[NCH], cd[NCH];
+  for (long long row0 = (long long)blockIdx.x * rpb + rib; row0 - rib + first_of_warp < a.R; row0 += RB * step, slot ^= 1) {
+    Chunk<T> cy[RB][NCH], ch[RB][NCH], cd[RB][NCH];
+    float rstd[RB], shift[RB];
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      cy[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.dy) + at, c_of(j), C);
-      ch[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.h) + at, c_of(j), C);
-      if (a.dh) cd[j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.dh) + at, c_of(j), C);
+    for (int r = 0; r < RB; ++r) {
+      const long long row = row0 + r * step;
+      const bool live = row < a.R;
+      const size_t at = (size_t)(live ? row : 0) * a.C;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        cy[r][j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.dy) + at, c_of(j), live ? a.C : 0);
+        ch[r][j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.h) + at, c_of(j), live ? a.C : 0);
+        if (a.dh) cd[r][j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.dh) + at, c_of(j), live ? a.C : 0);
+      }
+      rstd[r] = live ? a.rstd[row] : 0.f;
+      shift[r] = live ? -a.mean[row] * rstd[r] : 0.f;
     }
-    const float rstd = live ? a.rstd[row] : 0.f, shift = live ? -a.mean[row] * rstd : 0.f;
-    auto both = [&](int j, float2 (&xh)[4], float2 (&t)[4]) {
-      to_pairs(ch[j], xh);
-      to_pairs(cy[j], t);
+    auto both = [&](int r, int j, float2 (&xh)[4], float2 (&t)[4]) {
+      to_pairs(ch[r][j], xh);
+      to_pairs(cy[r][j], t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xh[i] = fma2(xh[i], f2(rstd), f2(shift));
+      for (int i = 0; i < 4; ++i) xh[i] = fma2(xh[i], f2(rstd[r]), f2(shift[r]));
     };
     auto weigh = [&](int j, float2 (&t)[4]) {
       if (!a.gamma) return;
       float2 g[4];
-      to_pairs(load_chunk<T, L, VEC>(static_cast<const T*>(a.gamma), c_of(j), a.C), g);
+      to_pairs(gm[j], g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) t[i] = mul2(t[i], g[i]);
     };
-    float2 m1 = f2(0.f), m2 = f2(0.f);
+    float m[2 * RB];
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      float2 xh[4], t[4];
-      both(j, xh, t);
+    for (int r = 0; r < RB; ++r) {
+      float2 m1 = f2(0.f), m2 = f2(0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ag[j][i] = fma2(t[i], xh[i], ag[j][i]);
-        ab[j][i] = add2(t[i], ab[j][i]);
+      for (int j = 0; j < NCH; ++j) {
+        float2 xh[4], t[4];
+        both(r, j, xh, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ag[j][i] = fma2(t[i], xh[i], ag[j][i]);
+          ab[j][i] = add2(t[i], ab[j][i]);
+        }
+        weigh(j, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          m1 = add2(m1, t[i]);
+          m2 = fma2(t[i], xh[i], m2);
+        }
       }
-      weigh(j, t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        m1 = add2(m1, t[i]);
-        m2 = fma2(t[i], xh[i], m2);
-      }
+      m[2 * r] = m1.x + m1.y;
+      m[2 * r + 1] = m2.x + m2.y;
     }
-    float m[2] = {m1.x + m1.y, m2.x + m2.y};
-    row_sums<L, 2>(m, my_red, slot, w, W, 1 + rib);
-    const float2 c1 = f2(-m[0] * inv_n), c2 = f2(-m[1] * inv_n), rs = f2(rstd);
+    row_sums<L, 2 * RB>(m, my_red, slot, w, W, 1 + rib);
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      float2 xh[4], t[4];
-      both(j, xh, t);
-      weigh(j, t);
+    for (int r = 0; r < RB; ++r) {
+      const long long row = row0 + r * step;
+      const bool live = row < a.R;
+      const size_t at = (size_t)(live ? row : 0) * a.C;
+      const float2 c1 = f2(-m[2 * r] * inv_n), c2 = f2(-m[2 * r + 1] * inv_n), rs = f2(rstd[r]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t[i] = mul2(fma2(xh[i], c2, add2(t[i], c1)), rs);
-      if (a.dh) {
-        float2 d[4];
-        to_pairs(cd[j], d);
+      for (int j = 0; j < NCH; ++j) {
+        float2 xh[4], t[4];
+        both(r, j, xh, t);
+        weigh(j, t);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = add2(t[i], d[i]);
-      }
-      if (live) store_chunk<T, L, VEC>(static_cast<T*>(a.dr) + at, c_of(j), a.C, t);
-      if (a.dx) {
-        drop_values<L, VEC>(bits, a.drop.scale, row, c_of(j), t);
-        if (live) store_chunk<T, L, VEC>(static_cast<T*>(a.dx) + at, c_of(j), a.C, t);
+        for (int i = 0; i < 4; ++i) t[i] = mul2(fma2(xh[i], c2, add2(t[i], c1)), rs);
+        if (a.dh) {
+          float2 d[4];
+          to_pairs(cd[r][j], d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = add2(t[i], d[i]);
+        }
+        if (live) store_chunk<T, L, VEC>(static_cast<T*>(a.dr) + at, c_of(j), a.C, t);
+        if (a.dx) {
+          drop_values<L, VEC>(bits, a.drop.scale, row, c_of(j), t);
+          if (live) store_chunk<T, L, VEC>(static_cast<T*>(a.dx) + at, c_of(j), a.C, t);
+        }
       }
     }
   }
@@ -585,7 +673,7 @@ __global__ void __launch_bounds__(512) k_layer_norm_bwd(const LnBwd a, const int
   });
 }
 
-template <typename T, int NCH>
+template <typename T, int NCH, bool VEC>
 __global__ void __launch_bounds__(kBwdRingThreads, 1)
     k_layer_norm_bwd_ring(const LnBwd a, const int W, const int rpb, const int depth, unsigned int* err,
                           const unsigned long long limit) {
@@ -597,20 +685,20 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
   __shared__ int abort_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rib = warp / W, w = warp - rib * W;
   const int seg0 = w * SEG, seg = min(SEG, a.C - seg0);
-  RowRing<T, SEG> ring;
+  RowRing<T, NCH, VEC> ring;
   ring.nt = a.dh ? 3 : 2;
   ring.depth = depth;
-  ring.base = reinterpret_cast<T*>(ring_smem) + (size_t)warp * (depth * ring.nt * SEG);
+  ring.base = reinterpret_cast<T*>(ring_smem) + (size_t)warp * (depth * ring.nt * ring.PITCH);
   ring.bar0 = smem_u32(bars + kRingMaxDepth * warp);
   ring.src[0] = static_cast<const T*>(a.dy);
   ring.src[1] = static_cast<const T*>(a.h);
   ring.src[2] = static_cast<const T*>(a.dh);
   ring.seg0 = seg0;
   ring.C = a.C;
-  ring.bytes = (uint32_t)(seg * (int)sizeof(T));
+  ring.seg = seg;
   ring.R = a.R;
   ring.step = (long long)gridDim.x * rpb;
-  ring.init(seg);
+  ring.init();
   if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
   pdl_wait();
@@ -622,7 +710,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
   Chunk<T> gm[NCH];
   if (a.gamma) {
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) gm[j] = load_chunk<T, 32, true>(static_cast<const T*>(a.gamma), seg0 + j * 256 + lane * 8, a.C);
+    for (int j = 0; j < NCH; ++j) gm[j] = load_chunk<T, 32, VEC>(static_cast<const T*>(a.gamma), seg0 + col0<32, VEC>(j, lane), a.C);
   }
   float2 ag[NCH][4], ab[NCH][4];
 #pragma unroll
@@ -638,13 +726,13 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
       next_rstd = a.rstd[row + ring.step];
       next_mean = a.mean[row + ring.step];
     }
-    const T* in = ring.wait(limit, err, &abort_flag);
+    const T* in = ring.wait(row, limit, err, &abort_flag);
     if (!ring.failed) gave_up = row + ring.step;
     float2 m1 = f2(0.f), m2 = f2(0.f), xh[NCH][4], t[NCH][4];
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      to_pairs(ring.load(in + j * 256 + lane * 8), t[j]);
-      to_pairs(ring.load(in + SEG + j * 256 + lane * 8), xh[j]);
+      to_pairs(ring.load(in, 0, j), t[j]);
+      to_pairs(ring.load(in, 1, j), xh[j]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         xh[j][i] = fma2(xh[j][i], f2(rstd), f2(shift));
@@ -669,19 +757,19 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
     const size_t at = (size_t)row * a.C;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int c0 = seg0 + j * 256 + lane * 8;
+      const int c0 = seg0 + col0<32, VEC>(j, lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i) t[j][i] = mul2(fma2(xh[j][i], c2, add2(t[j][i], c1)), rs);
       if (a.dh) {
         float2 d[4];
-        to_pairs(ring.load(in + 2 * SEG + j * 256 + lane * 8), d);
+        to_pairs(ring.load(in, 2, j), d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[j][i] = add2(t[j][i], d[i]);
       }
-      store_chunk<T, 32, true>(static_cast<T*>(a.dr) + at, c0, a.C, t[j]);
+      store_chunk<T, 32, VEC>(static_cast<T*>(a.dr) + at, c0, a.C, t[j]);
       if (a.dx) {
-        drop_values<32, true>(bits, a.drop.scale, row, c0, t[j]);
-        store_chunk<T, 32, true>(static_cast<T*>(a.dx) + at, c0, a.C, t[j]);
+        drop_values<32, VEC>(bits, a.drop.scale, row, c0, t[j]);
+        store_chunk<T, 32, VEC>(static_cast<T*>(a.dx) + at, c0, a.C, t[j]);
       }
     }
     ring.next(row);
@@ -696,7 +784,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
     for (int j = 0; j < NCH; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int c = seg0 + j * 256 + lane * 8 + i;
+        const int c = col<32, VEC>(seg0 + col0<32, VEC>(j, lane), i);
         if (c < a.C) f(i & 1 ? ag[j][i / 2].y : ag[j][i / 2].x, i & 1 ? ab[j][i / 2].y : ab[j][i / 2].x, c);
       }
   };
@@ -720,9 +808,11 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
 }
 
 RingSpread bwd_ring_spread(const LnBwd& a) { return ring_spread(a.R, a.C, a.dtype, a.dh ? 3 : 2, kBwdRingThreads); }
-template <typename T> cudaError_t layer_norm_bwd_ring(const LnBwd& a, cudaStream_t st) {
+template <typename T, bool VEC> cudaError_t layer_norm_bwd_ring(const LnBwd& a, cudaStream_t st) {
   const RingSpread s = bwd_ring_spread(a);
-  auto k = s.nch == 3 ? k_layer_norm_bwd_ring<T, 3> : s.nch == 4 ? k_layer_norm_bwd_ring<T, 4> : k_layer_norm_bwd_ring<T, 5>;
+  auto k = s.nch == 3   ? k_layer_norm_bwd_ring<T, 3, VEC>
+           : s.nch == 4 ? k_layer_norm_bwd_ring<T, 4, VEC>
+                        : k_layer_norm_bwd_ring<T, 5, VEC>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
   if (e != cudaSuccess) return e;
   return launch_k(k, dim3((unsigned)ln_bwd_rows_blocks(a)), dim3(32 * s.W * s.rpb), s.smem, st, 1, a, s.W, s.rpb, s.depth,
@@ -730,28 +820,31 @@ template <typename T> cudaError_t layer_norm_bwd_ring(const LnBwd& a, cudaStream
 }
 // The longest rows need more warps than share a block's registers.
 bool ring_takes(const LnBwd& a) {
-  return a.C > 512 && rows_aligned(a.C, a.dtype == 0 ? 4 : 2) && bwd_ring_spread(a).rpb >= 1;
+  return a.C > 512 && bwd_ring_spread(a).rpb >= 1;
 }
 
+template <typename T> constexpr int kBwdRows = sizeof(T) == 2 ? 4 : 2;  // rows of one block at a time
 Spread bwd_spread(int C) {
   Spread s;
   const int blocks = (C + 255) / 256;
   s.L = C <= 64 ? 8 : C <= 128 ? 16 : 32;
-  s.nch = blocks <= 16 ? 1 : blocks <= 32 ? 2 : 4;
+  s.nch = blocks <= 2 ? blocks : 4;
   s.W = (blocks + s.nch - 1) / s.nch;
-  s.rpb = s.W == 1 ? 256 / s.L : s.W < 10 ? 10 / s.W : 1;
+  s.rpb = s.W == 1 ? 256 / s.L : s.W < 8 ? 8 / s.W : 1;
   s.threads = s.L * s.W * s.rpb;
   return s;
 }
 template <typename T, bool VEC> cudaError_t layer_norm_bwd(const LnBwd& a, cudaStream_t st) {
+  if (ring_takes(a)) return layer_norm_bwd_ring<T, VEC>(a, st);
   const Spread s = bwd_spread(a.C);
   const int sets = s.L == 32 ? s.rpb : s.threads / 32;
-  const size_t smem = (size_t)(sets - 1) * 2 * a.C * sizeof(float);  // 18 KB at most
-  auto k = s.L == 8     ? k_layer_norm_bwd<T, 8, 1, VEC>
-           : s.L == 16  ? k_layer_norm_bwd<T, 16, 1, VEC>
-           : s.nch == 1 ? k_layer_norm_bwd<T, 32, 1, VEC>
-           : s.nch == 2 ? k_layer_norm_bwd<T, 32, 2, VEC>
-                        : k_layer_norm_bwd<T, 32, 4, VEC>;
+  const size_t smem = (size_t)(sets - 1) * 2 * a.C * sizeof(float);  // 28 KB at most
+  constexpr int RB = kBwdRows<T>;
+  auto k = s.L == 8     ? k_layer_norm_bwd<T, 8, 1, RB, VEC, 256>
+           : s.L == 16  ? k_layer_norm_bwd<T, 16, 1, RB, VEC, 256>
+           : s.nch == 1 ? k_layer_norm_bwd<T, 32, 1, RB, VEC, 256>
+           : s.nch == 2 ? k_layer_norm_bwd<T, 32, 2, RB / 2, VEC, 256>
+                        : k_layer_norm_bwd<T, 32, 4, 1, VEC, 512>;
   return launch_k(k, dim3((unsigned)ln_bwd_rows_blocks(a)), dim3(s.threads), smem, st, 1, a, s.W, s.rpb);
 }
 
@@ -770,14 +863,13 @@ int ln_bwd_rows_blocks(const LnBwd& a) {
     const long long want = (a.R + rpb - 1) / rpb;
     return (int)(want < sm_count() ? want : sm_count());
   }
+  // As many as are resident at once (two an SM, one where the row has 16 warps);
+  // few rows: as many as there are.
   const Spread s = bwd_spread(a.C);
-  const long long want = (a.R + s.rpb - 1) / s.rpb;
-  long long most = (long long)sm_count() * 3;
-  if (most > kLnBwdMaxBlocks) most = kLnBwdMaxBlocks;
+  const long long want = (a.R + s.rpb - 1) / s.rpb, most = (long long)sm_count() * (s.threads > 256 ? 1 : 2);
   return (int)(want < most ? want : most);
 }
 cudaError_t launch_layer_norm_bwd(const LnBwd& a, cudaStream_t st) {
-  if (ring_takes(a)) { RMX_BY_DTYPE(a.dtype, return layer_norm_bwd_ring<T>(a, st)) }
   RMX_BY_DTYPE(a.dtype,
                return rows_aligned(a.C, sizeof(T)) ? layer_norm_bwd<T, true>(a, st) : layer_norm_bwd<T, false>(a, st))
 }
