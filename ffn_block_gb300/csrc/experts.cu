@@ -4,8 +4,8 @@
 // The sort counts.  A warp takes its slots in order, 32 at a time: lanes with
 // the same expert find one another by votes, so a slot's place among them is a
 // population count, and the first of them moves the warp's own counter on.  No
-// atomics: the order is the slots' own.  Up to 8192 slots are sorted by one CTA,
-// up to 262,144 by a cluster of eight, whose CTAs read one another's counts, in one
+// atomics: the order is the slots' own.  Up to 2048 slots are sorted by one CTA, up
+// to 49,152 by a cluster of eight, whose CTAs read one another's counts, in one
 // launch; more by three launches: each warp counts its share, each expert's counts
 // are summed over the warps, and each warp places its share.
 
@@ -113,8 +113,10 @@ __device__ __forceinline__ int block_prefix(int v, int* tmp, int& total) {
 }
 
 constexpr int kWarps = 32;             // of a CTA that sorts, at most
-constexpr int kOneSlots = 8192;        // up to here one CTA sorts by itself
-constexpr int kCluster = 8, kClusterSlots = 262144;
+// Slots that one CTA sorts by itself, and that a cluster does.  us for 64 experts, a
+// CTA / a cluster / three launches: 2048 slots 7.1 / - / -, 8192 11.9 / 7.8 / -,
+// 32,768 - / 8.6 / 10.8, 65,536 - / 12.9 / 11.7, 131,072 - / 21.4 / 13.1.
+constexpr int kOneSlots = 2048, kCluster = 8, kClusterSlots = 49152;
 
 __device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_addr) {
   int v;
@@ -243,10 +245,11 @@ __global__ void __launch_bounds__(32 * kManyWarps) k_sort_place(int S, int E, in
   for (long long i = run + (long long)blockIdx.x * blockDim.x + threadIdx.x; i < S; i += (long long)gridDim.x * blockDim.x)
     source[i] = -1;
 }
-// A warp's share of the slots: 512, or what keeps the warps at 4096.
+// A warp's share of the slots: 256 (128 or 512: 131,072 slots in 14.6 and 15.8 us, not
+// 13.1), or what keeps the warps at 4096.
 int share_of(int S) {
   const int least = (int)(((long long)S + 4095) / 4096);
-  return least <= 512 ? 512 : (least + 31) / 32 * 32;
+  return least <= 256 ? 256 : (least + 31) / 32 * 32;
 }
 
 // ---------------------------------------------------------------- rows

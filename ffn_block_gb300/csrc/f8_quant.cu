@@ -78,24 +78,13 @@ template <typename T> __device__ __forceinline__ uint32_t as_f32_bits(uint32_t m
   return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
 }
 
-// A block belongs to eight lanes: lane l has columns 8 l .. 8 l + 7 and 64 + 8 l
-// .. (so that neighbouring lanes' accesses are neighbours).
-template <typename T, bool VEC> struct Load {
-  static __device__ __forceinline__ Chunk<T> chunk(const T* row, int c0, int C) {
-    if constexpr (VEC) {
-      return load_chunk<T, 32, true>(row, c0, C);
-    } else {
-      Chunk<T> k;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) k.v[i] = c0 + i < C ? row[c0 + i] : from_f<T>(0.f);
-      return k;
-    }
-  }
-};
-
-// Blocks of 128 columns at a time to each eight lanes.
-constexpr int kBatch = 2;
-template <typename T, bool VEC, bool E5, bool GATHER>
+// Rows of whole 16-byte vectors: a block belongs to eight lanes, lane l has columns
+// 8 l .. 8 l + 7 and 64 + 8 l .. (so that neighbouring lanes' accesses are
+// neighbours).
+// Blocks of 128 columns at a time to each eight lanes, and pairs of them to each
+// warp where rows are odd.
+constexpr int kBatch = 2, kOddBatch = 4;
+template <typename T, bool E5, bool GATHER>
 __global__ void __launch_bounds__(256) k_quant_f8(const QuantRows a, const int bpr, const int EP, const long long total) {
   pdl_enter();
   const int l = threadIdx.x & 7;
@@ -125,7 +114,7 @@ __global__ void __launch_bounds__(256) k_quant_f8(const QuantRows a, const int b
       const T* p = x + (size_t)from * a.C;
       const int C = row[j] >= 0 ? a.C : 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) k[j][h] = Load<T, VEC>::chunk(p, blk[j] * 128 + 64 * h + 8 * l, C);
+      for (int h = 0; h < 2; ++h) k[j][h] = load_chunk<T, 32, true>(p, blk[j] * 128 + 64 * h + 8 * l, C);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -141,22 +130,86 @@ __global__ void __launch_bounds__(256) k_quant_f8(const QuantRows a, const int b
         float2 v[4];
         to_pairs(k[j][h], v);
         *reinterpret_cast<uint2*>(a.q + (size_t)row[j] * (bpr * 128) + c0) = to_f8x8<E5>(v, inv);
-        if (GATHER && a.out) {
-          T* o = static_cast<T*>(a.out) + (size_t)row[j] * a.C;
-          if constexpr (VEC) {
-            store_chunk<T, 32, true>(o, c0, a.C, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c0 + i < a.C) o[c0 + i] = k[j][h].v[i];
-          }
-        }
+        if (GATHER && a.out) store_chunk<T, 32, true>(static_cast<T*>(a.out) + (size_t)row[j] * a.C, c0, a.C, v);
       }
       if (l == 0) {
         uint8_t* ex = a.e + (size_t)row[j] * EP;
         ex[blk[j]] = (uint8_t)e;
         if (blk[j] == bpr - 1)
           for (int i = bpr; i < EP; ++i) ex[i] = 0;
+      }
+    }
+  }
+}
+
+// Other rows: a warp takes two blocks, a lane four neighbouring columns of each.
+template <typename T, bool E5, bool GATHER>
+__global__ void __launch_bounds__(256) k_quant_f8_odd(const QuantRows a, const int bpr, const int EP, const int wpr,
+                                                      const long long total) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const long long step = (long long)gridDim.x * 8 * kOddBatch;
+  const T* x = static_cast<const T*>(a.x);
+  for (long long w0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kOddBatch; w0 < total; w0 += step) {
+    Chunk<T> k[kOddBatch];
+    long long row[kOddBatch];
+    int c0[kOddBatch];
+#pragma unroll
+    for (int j = 0; j < kOddBatch; ++j) {
+      const long long b = w0 + j;
+      row[j] = -1;
+      c0[j] = 0;
+      long long from = 0;
+      if (b < total) {
+        const long long r = total < (1ll << 31) ? (long long)((uint32_t)b / (uint32_t)wpr) : b / wpr;
+        c0[j] = (int)(b - r * wpr) * 256;
+        row[j] = from = r;
+        if (GATHER) {
+          const int s = a.source[r];
+          if ((uint32_t)s < (uint32_t)a.R) from = (uint32_t)s / (uint32_t)a.k;
+          else row[j] = -1;
+        }
+      }
+      const T* p = x + (size_t)from * a.C;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0[j] + 128 * (i / 4) + 4 * lane + i % 4;
+        k[j].v[i] = row[j] >= 0 && c < a.C ? p[c] : from_f<T>(0.f);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kOddBatch; ++j) {
+      uint32_t m[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i / 4] = max(m[i / 4], __float_as_uint(to_f(k[j].v[i])) & 0x7fffffffu);
+      m[0] = __reduce_max_sync(0xffffffffu, m[0]);
+      m[1] = __reduce_max_sync(0xffffffffu, m[1]);
+      if (row[j] < 0) continue;
+      uint8_t* q = a.q + (size_t)row[j] * (bpr * 128);
+      uint8_t* ex = a.e + (size_t)row[j] * EP;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int blk = c0[j] / 128 + h;
+        if (blk >= bpr) break;
+        const int e = block_exp<E5>(m[h]);
+        const float inv = block_inv(e);
+        const T* v = k[j].v + 4 * h;
+        const uint32_t w = __byte_perm(to_f8x2<E5>(to_f(v[0]) * inv, to_f(v[1]) * inv),
+                                       to_f8x2<E5>(to_f(v[2]) * inv, to_f(v[3]) * inv), 0x5410);
+        *reinterpret_cast<uint32_t*>(q + blk * 128 + 4 * lane) = inv == 0.f ? 0u : w;
+        if (lane == 0) {
+          ex[blk] = (uint8_t)e;
+          if (blk == bpr - 1)
+            for (int i = bpr; i < EP; ++i) ex[i] = 0;
+        }
+      }
+      if (GATHER && a.out) {
+        T* o = static_cast<T*>(a.out) + (size_t)row[j] * a.C;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = c0[j] + 128 * (i / 4) + 4 * lane + i % 4;
+          if (c < a.C) o[c] = k[j].v[i];
+        }
       }
     }
   }
@@ -185,7 +238,7 @@ template <typename T> __device__ __forceinline__ float read_back(float q, float 
   return fabsf(v) > Largest<T>::value ? copysignf(Largest<T>::value, v) : v;  // (a NaN step stays NaN)
 }
 
-template <typename T, bool VEC, bool E5>
+template <typename T, bool E5>
 __global__ void __launch_bounds__(256) k_dequant_f8(long long total, int bpr, int EP, int C, const uint8_t* q,
                                                     const uint8_t* e, T* x) {
   pdl_enter();
@@ -203,15 +256,34 @@ __global__ void __launch_bounds__(256) k_dequant_f8(long long total, int bpr, in
                      from_f8x2<E5>(w.y >> 16)};
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = make_float2(read_back<T>(v[i].x, s), read_back<T>(v[i].y, s));
-      T* o = x + (size_t)row * C;
-      if constexpr (VEC) {
-        store_chunk<T, 32, true>(o, c0, C, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c0 + i < C) o[c0 + i] = from_f<T>(i & 1 ? v[i / 2].y : v[i / 2].x);
-      }
+      store_chunk<T, 32, true>(x + (size_t)row * C, c0, C, v);
     }
+  }
+}
+// Other rows, as in the quantisation.
+template <typename T, bool E5>
+__global__ void __launch_bounds__(256) k_dequant_f8_odd(long long total, int bpr, int EP, int wpr, int C, const uint8_t* q,
+                                                        const uint8_t* e, T* x) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const long long step = (long long)gridDim.x * 8;
+  for (long long b = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); b < total; b += step) {
+    const long long row = total < (1ll << 31) ? (long long)((uint32_t)b / (uint32_t)wpr) : b / wpr;
+    const int c0 = (int)(b - row * wpr) * 256;
+    const uint8_t* p = q + (size_t)row * (bpr * 128);
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = c0 + 32 * i < C ? p[c0 + 32 * i + lane] : 0u;
+    float s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = c0 + 128 * h < C ? block_step(e[(size_t)row * EP + c0 / 128 + h]) : 0.f;
+    float2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = from_f8x2<E5>(w[2 * i] | w[2 * i + 1] << 8);
+      v[i] = make_float2(read_back<T>(v[i].x, s[i / 2]), read_back<T>(v[i].y, s[i / 2]));
+    }
+    store_chunk<T, 32, false>(x + (size_t)row * C, c0 + lane, C, v);
   }
 }
 
@@ -255,8 +327,10 @@ __device__ __forceinline__ void st_sector(uint8_t* p, const uint32_t (&o)[8]) {
                : "memory");
 }
 
-template <typename T, bool VEC, bool E5>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+// Resident CTAs an SM.
+template <typename T, bool SUMS> constexpr int quant_blocks = sizeof(T) == 2 && !SUMS ? 3 : 2;
+template <typename T, bool VEC, bool E5, bool SUMS>
+__global__ void __launch_bounds__(kThreads, (quant_blocks<T, SUMS>))
     k_quant_groups(const QuantGroups a, const int ctiles, const int EP) {
   pdl_enter();
   extern __shared__ uint4 smem_q[];
@@ -327,9 +401,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     const int c0 = ct * kTile, g = cur.g, b = cur.b, blk = cur.blk, rows = cur.rows;
     if constexpr (!VEC) {
       const T* x = base(cur);
-      for (int i = t; i < kTile * kTile; i += kThreads) {
-        const int r = i >> 7, c = i & 127;
-        tile[i] = r < rows && c0 + c < a.C ? x[(size_t)r * a.row_stride + c0 + c] : from_f<T>(0.f);
+      // A warp takes 16 rows, four at a time, neighbours' columns one run.
+      const int lane = t & 31;
+#pragma unroll 1
+      for (int r = (t >> 5) * 4; r < kTile; r += kThreads / 8) {
+        T v[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[i][j] = r + i < rows && c0 + 32 * j + lane < a.C ? x[(size_t)(r + i) * a.row_stride + c0 + 32 * j + lane] : from_f<T>(0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tile[(r + i) * kTile + 32 * j + lane] = v[i][j];
       }
       __syncthreads();
 #pragma unroll
@@ -375,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       ct = (int)next - cur.blk * ctiles;
       if constexpr (VEC) load(cur, ct * kTile);
     }
-    if (!a.qt && !a.part) {
+    if (!SUMS && !a.qt) {
       __syncthreads();
       continue;
     }
@@ -393,16 +478,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       m0 = half_bits<T>(m0 & 0xffffu);
     }
     *reinterpret_cast<uint2*>(&ctop[quarter][2 * cp]) = make_uint2(m0, m1);
-    if (a.part) {
-      float2 s = f2(0.f);
+    if constexpr (SUMS) {
+      float2 sum = f2(0.f);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s = add2(s, Pair2<T>::pair(w[i]));
-      *reinterpret_cast<float2*>(&csum[quarter][2 * cp]) = s;
+      for (int i = 0; i < 32; ++i) sum = add2(sum, Pair2<T>::pair(w[i]));
+      *reinterpret_cast<float2*>(&csum[quarter][2 * cp]) = sum;
     }
     __syncthreads();  // (also: every word has been read before the next tile's are written)
-    if (a.part && t < kTile && c0 + t < a.C)
-      a.part[(size_t)blk * a.C + c0 + t] = (csum[0][t] + csum[1][t]) + (csum[2][t] + csum[3][t]);
-    if (!a.qt) continue;
+    if constexpr (SUMS) {
+      if (t < kTile && c0 + t < a.C) a.part[(size_t)blk * a.C + c0 + t] = (csum[0][t] + csum[1][t]) + (csum[2][t] + csum[3][t]);
+      if (!a.qt) continue;
+    }
     // Both columns at once.
     int ex2[2];
     float2 inv2;
@@ -418,7 +504,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     for (int i = 0; i < 8; ++i) {
       float2 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = mul2(Pair2<T>::pair(w[4 * i + j]), inv2);
+      for (int j = 0; j < 4; ++j) {
+        v[j] = mul2(Pair2<T>::pair(w[4 * i + j]), inv2);
+      }
       o2[0][i] = __byte_perm(to_f8x2<E5>(v[0].x, v[1].x), to_f8x2<E5>(v[2].x, v[3].x), 0x5410);
       o2[1][i] = __byte_perm(to_f8x2<E5>(v[0].y, v[1].y), to_f8x2<E5>(v[2].y, v[3].y), 0x5410);
     }
@@ -482,24 +570,37 @@ unsigned grid_of(long long units, int per_block) {
 
 template <typename T, bool VEC, bool E5> cudaError_t quant(const QuantRows& a, cudaStream_t st) {
   const int bpr = f8_blocks(a.C), EP = f8_exps(a.C);
-  const long long total = a.R * bpr;
-  auto k = a.source ? k_quant_f8<T, VEC, E5, true> : k_quant_f8<T, VEC, E5, false>;
-  return launch_k(k, dim3(grid_of(total, 32 * kBatch)), dim3(256), 0, st, 1, a, bpr, EP, total);
+  if constexpr (VEC) {
+    const long long total = a.R * bpr;
+    auto k = a.source ? k_quant_f8<T, E5, true> : k_quant_f8<T, E5, false>;
+    return launch_k(k, dim3(grid_of(total, 32 * kBatch)), dim3(256), 0, st, 1, a, bpr, EP, total);
+  } else {
+    const int wpr = (bpr + 1) / 2;
+    const long long total = a.R * wpr;
+    auto k = a.source ? k_quant_f8_odd<T, E5, true> : k_quant_f8_odd<T, E5, false>;
+    return launch_k(k, dim3(grid_of(total, 8 * kOddBatch)), dim3(256), 0, st, 1, a, bpr, EP, wpr, total);
+  }
 }
 template <typename T, bool VEC, bool E5>
 cudaError_t dequant(long long R, int C, const uint8_t* q, const uint8_t* e, void* x, cudaStream_t st) {
-  const long long total = R * f8_blocks(C);
-  return launch_k(k_dequant_f8<T, VEC, E5>, dim3(grid_of(total, 32)), dim3(256), 0, st, 1, total, f8_blocks(C), f8_exps(C), C,
-                  q, e, (T*)x);
+  const int bpr = f8_blocks(C), EP = f8_exps(C);
+  if constexpr (VEC) {
+    const long long total = R * bpr;
+    return launch_k(k_dequant_f8<T, E5>, dim3(grid_of(total, 32)), dim3(256), 0, st, 1, total, bpr, EP, C, q, e, (T*)x);
+  } else {
+    const int wpr = (bpr + 1) / 2;
+    const long long total = R * wpr;
+    return launch_k(k_dequant_f8_odd<T, E5>, dim3(grid_of(total, 8)), dim3(256), 0, st, 1, total, bpr, EP, wpr, C, q, e, (T*)x);
+  }
 }
 template <typename T, bool VEC, bool E5> cudaError_t quant_groups(const QuantGroups& a, cudaStream_t st) {
   const int ctiles = f8_blocks(a.C);
   const int smem = kTile * kTile * (int)sizeof(T) + (a.offsets ? 2 * (a.G + 1) * (int)sizeof(int) : 0);
-  auto k = k_quant_groups<T, VEC, E5>;
+  auto k = a.part ? k_quant_groups<T, VEC, E5, true> : k_quant_groups<T, VEC, E5, false>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kTile * kTile * (int)sizeof(T) + 2 * (kMaxExperts + 1) * (int)sizeof(int));
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)a.blocks * ctiles, fit = (sizeof(T) == 2 ? 3ll : 2ll) * sm_count();
+  const long long tiles = (long long)a.blocks * ctiles, fit = (long long)sm_count() * (a.part ? quant_blocks<T, true> : quant_blocks<T, false>);
   return launch_k(k, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kThreads), smem, st, 1, a, ctiles, f8_exps(a.C));
 }
 

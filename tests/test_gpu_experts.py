@@ -29,9 +29,10 @@ def _check_sort(ids, E):
     return got
 
 
-# both sides of the single CTA's limit (8192 slots) and of a warp's share, experts up to 1024
+# both sides of the limits of one CTA (2048 slots) and of a cluster (49152), and of a warp's share; experts up to 1024
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 64, 3), (5, 2, 7), (31, 1, 2), (33, 3, 1024), (64, 2, 32), (1024, 8, 64),
-                                   (8191, 1, 5), (8193, 1, 5), (4097, 2, 1024), (1229, 7, 33), (65536, 2, 64), (20000, 8, 200)])
+                                   (2048, 1, 5), (2049, 1, 5), (8193, 1, 5), (4097, 2, 1024), (1229, 7, 33), (49152, 1, 64),
+                                   (49153, 1, 64), (12289, 4, 1024), (65536, 2, 64), (20000, 8, 200)])
 def test_sort(T, k, E):
     rng = np.random.default_rng(T)
     _check_sort(rng.integers(0, E, (T, k)), E)

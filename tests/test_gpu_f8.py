@@ -363,3 +363,21 @@ def test_products_repeat_bit_for_bit():
         ok(B.rmx_linear_f8(B.make_layer_f8(M, G, K, N, "bf16"), None, qa, ea, qw, ew, None, None, o))
     sync()
     assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+def test_sums_of_faulty_columns():
+    """A column's sum holds its infinities and NaN, its neighbours' do not; tiny and huge values sum as they are."""
+    M, G, C = 200, 1, 64
+    x = torch.randn((M, C), device="cuda")
+    x[3, 5], x[150, 6] = float("inf"), float("nan")
+    x[:, 8] = 2.0 ** -140
+    x[:, 9] = 2.0 ** 120
+    gr = B.make_groups(M, G, C, "f32", "groups")
+    nws = B.rmx_quant_f8_groups_workspace_bytes(gr)
+    sums = empty((G, C), "f32")
+    ok(B.rmx_quant_f8_groups(gr, "e4m3", None, x, None, None, None, None, sums, empty((nws,), torch.uint8), nws))
+    got, v = f64(sums)[0], f64(x)
+    assert np.isposinf(got[5]) and np.isnan(got[6])
+    fine = np.ones(C, bool)
+    fine[5:7] = False
+    within(got[fine], v.sum(0)[fine], 136 * E32 * np.abs(v).sum(0)[fine])
