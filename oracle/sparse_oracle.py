@@ -147,7 +147,7 @@ def quant_rows(x, fmt):
 def row_values(q, e, cols):
     """What 8-bit rows stand for."""
     step = np.where(e == 255, np.nan, 2.0 ** (e.astype(np.float64) - 127))
-    return (q.reshape(q.shape[0], -1, 128) * step[..., None]).reshape(q.shape)[:, :cols]
+    return (q.reshape(q.shape[0], e.shape[1], 128) * step[..., None]).reshape(q.shape)[:, :cols]
 
 
 def round_rows(x, fmt):
