@@ -272,8 +272,8 @@ __device__ __forceinline__ long long row_of(const Units& u, long long i, int& bl
 
 constexpr int kBatch = 4;
 template <typename T, int L, bool VEC>
-__global__ void __launch_bounds__(256) k_gather(const Units u, int S, int k, int C, const int32_t* source, const T* x,
-                                                T* out) {
+__global__ void __launch_bounds__(256) k_gather(const Units u, int S, int k, int C, const bool stream, const int32_t* source,
+                                                const T* x, T* out) {
   pdl_enter();
   constexpr int PER = 256 / L;
   const int lane = threadIdx.x & (L - 1);
@@ -302,7 +302,11 @@ __global__ void __launch_bounds__(256) k_gather(const Units u, int S, int k, int
           const uint4* s = reinterpret_cast<const uint4*>(&c[j]);
 #pragma unroll
           for (int i = 0; i < 8 / V; ++i)
-            if (c0[j] + i * V < C) reinterpret_cast<uint4*>(o + c0[j])[i] = s[i];
+            if (c0[j] + i * V < C) {
+              uint4* q = reinterpret_cast<uint4*>(o + c0[j]) + i;
+              if (stream) __stcs(q, s[i]);
+              else *q = s[i];
+            }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -496,7 +500,10 @@ unsigned grid_of(long long units, int per_block) {
 template <typename T, bool VEC>
 cudaError_t gather(const Routes& r, const int32_t* source, const void* x, void* out, cudaStream_t st) {
   auto go = [&](auto k, const Units& u, int per) {
-    return launch_k(k, dim3(grid_of(u.total, per * kBatch)), dim3(256), 0, st, 1, u, r.S, r.k, r.C, source, (const T*)x,
+    // A token's row is read again for its next expert: outputs that would push it out
+    // of L2 leave first (65536 x 2 rows of 1280 16-bit columns 105 us, 95 like this).
+    const bool stream = (long long)r.S * r.C * (int)sizeof(T) > (64ll << 20);
+    return launch_k(k, dim3(grid_of(u.total, per * kBatch)), dim3(256), 0, st, 1, u, r.S, r.k, r.C, stream, source, (const T*)x,
                     (T*)out);
   };
   if (r.C <= 64) return go(k_gather<T, 8, VEC>, units_of<8>(r.S, r.C), 32);

@@ -78,13 +78,25 @@ template <typename T> __device__ __forceinline__ uint32_t as_f32_bits(uint32_t m
   return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
 }
 
-// Rows of whole 16-byte vectors: a block belongs to eight lanes, lane l has columns
-// 8 l .. 8 l + 7 and 64 + 8 l .. (so that neighbouring lanes' accesses are
-// neighbours).
-// Blocks of 128 columns at a time to each eight lanes, and pairs of them to each
-// warp where rows are odd.
-constexpr int kBatch = 2, kOddBatch = 4;
-template <typename T, bool E5, bool GATHER>
+// A block belongs to eight lanes: lane l has columns 8 l .. 8 l + 7 and 64 + 8 l
+// .. (so that neighbouring lanes' accesses are neighbours).  Rows that are not whole
+// 16-byte vectors (not VEC) come value by value: 65,536 rows of 1001 16-bit columns
+// 47 us; four neighbouring columns of a block to each of 32 lanes 59; the two vectors
+// that eight columns lie in, shifted into place, 59.
+template <typename T, bool VEC> __device__ __forceinline__ Chunk<T> load_eight(const T* row, int c0, int C) {
+  if constexpr (VEC) {
+    return load_chunk<T, 32, true>(row, c0, C);
+  } else {
+    Chunk<T> k;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k.v[i] = c0 + i < C ? row[c0 + i] : from_f<T>(0.f);
+    return k;
+  }
+}
+
+// Blocks of 128 columns at a time to each eight lanes.
+constexpr int kBatch = 2;
+template <typename T, bool VEC, bool E5, bool GATHER>
 __global__ void __launch_bounds__(256) k_quant_f8(const QuantRows a, const int bpr, const int EP, const long long total) {
   pdl_enter();
   const int l = threadIdx.x & 7;
@@ -114,7 +126,7 @@ __global__ void __launch_bounds__(256) k_quant_f8(const QuantRows a, const int b
       const T* p = x + (size_t)from * a.C;
       const int C = row[j] >= 0 ? a.C : 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) k[j][h] = load_chunk<T, 32, true>(p, blk[j] * 128 + 64 * h + 8 * l, C);
+      for (int h = 0; h < 2; ++h) k[j][h] = load_eight<T, VEC>(p, blk[j] * 128 + 64 * h + 8 * l, C);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -130,86 +142,22 @@ __global__ void __launch_bounds__(256) k_quant_f8(const QuantRows a, const int b
         float2 v[4];
         to_pairs(k[j][h], v);
         *reinterpret_cast<uint2*>(a.q + (size_t)row[j] * (bpr * 128) + c0) = to_f8x8<E5>(v, inv);
-        if (GATHER && a.out) store_chunk<T, 32, true>(static_cast<T*>(a.out) + (size_t)row[j] * a.C, c0, a.C, v);
+        if (GATHER && a.out) {
+          T* o = static_cast<T*>(a.out) + (size_t)row[j] * a.C;
+          if constexpr (VEC) {
+            store_chunk<T, 32, true>(o, c0, a.C, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c0 + i < a.C) o[c0 + i] = k[j][h].v[i];
+          }
+        }
       }
       if (l == 0) {
         uint8_t* ex = a.e + (size_t)row[j] * EP;
         ex[blk[j]] = (uint8_t)e;
         if (blk[j] == bpr - 1)
           for (int i = bpr; i < EP; ++i) ex[i] = 0;
-      }
-    }
-  }
-}
-
-// Other rows: a warp takes two blocks, a lane four neighbouring columns of each.
-template <typename T, bool E5, bool GATHER>
-__global__ void __launch_bounds__(256) k_quant_f8_odd(const QuantRows a, const int bpr, const int EP, const int wpr,
-                                                      const long long total) {
-  pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const long long step = (long long)gridDim.x * 8 * kOddBatch;
-  const T* x = static_cast<const T*>(a.x);
-  for (long long w0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kOddBatch; w0 < total; w0 += step) {
-    Chunk<T> k[kOddBatch];
-    long long row[kOddBatch];
-    int c0[kOddBatch];
-#pragma unroll
-    for (int j = 0; j < kOddBatch; ++j) {
-      const long long b = w0 + j;
-      row[j] = -1;
-      c0[j] = 0;
-      long long from = 0;
-      if (b < total) {
-        const long long r = total < (1ll << 31) ? (long long)((uint32_t)b / (uint32_t)wpr) : b / wpr;
-        c0[j] = (int)(b - r * wpr) * 256;
-        row[j] = from = r;
-        if (GATHER) {
-          const int s = a.source[r];
-          if ((uint32_t)s < (uint32_t)a.R) from = (uint32_t)s / (uint32_t)a.k;
-          else row[j] = -1;
-        }
-      }
-      const T* p = x + (size_t)from * a.C;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = c0[j] + 128 * (i / 4) + 4 * lane + i % 4;
-        k[j].v[i] = row[j] >= 0 && c < a.C ? p[c] : from_f<T>(0.f);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kOddBatch; ++j) {
-      uint32_t m[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m[i / 4] = max(m[i / 4], __float_as_uint(to_f(k[j].v[i])) & 0x7fffffffu);
-      m[0] = __reduce_max_sync(0xffffffffu, m[0]);
-      m[1] = __reduce_max_sync(0xffffffffu, m[1]);
-      if (row[j] < 0) continue;
-      uint8_t* q = a.q + (size_t)row[j] * (bpr * 128);
-      uint8_t* ex = a.e + (size_t)row[j] * EP;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int blk = c0[j] / 128 + h;
-        if (blk >= bpr) break;
-        const int e = block_exp<E5>(m[h]);
-        const float inv = block_inv(e);
-        const T* v = k[j].v + 4 * h;
-        const uint32_t w = __byte_perm(to_f8x2<E5>(to_f(v[0]) * inv, to_f(v[1]) * inv),
-                                       to_f8x2<E5>(to_f(v[2]) * inv, to_f(v[3]) * inv), 0x5410);
-        *reinterpret_cast<uint32_t*>(q + blk * 128 + 4 * lane) = inv == 0.f ? 0u : w;
-        if (lane == 0) {
-          ex[blk] = (uint8_t)e;
-          if (blk == bpr - 1)
-            for (int i = bpr; i < EP; ++i) ex[i] = 0;
-        }
-      }
-      if (GATHER && a.out) {
-        T* o = static_cast<T*>(a.out) + (size_t)row[j] * a.C;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = c0[j] + 128 * (i / 4) + 4 * lane + i % 4;
-          if (c < a.C) o[c] = k[j].v[i];
-        }
       }
     }
   }
@@ -260,7 +208,9 @@ __global__ void __launch_bounds__(256) k_dequant_f8(long long total, int bpr, in
     }
   }
 }
-// Other rows, as in the quantisation.
+// Other rows: a warp takes 256 columns, a lane columns lane, lane + 32, ..., so that
+// neighbours write one run (65,536 rows of 1001 16-bit columns 53 us; with eight
+// neighbouring columns a lane, as above, 204).
 template <typename T, bool E5>
 __global__ void __launch_bounds__(256) k_dequant_f8_odd(long long total, int bpr, int EP, int wpr, int C, const uint8_t* q,
                                                         const uint8_t* e, T* x) {
@@ -570,16 +520,9 @@ unsigned grid_of(long long units, int per_block) {
 
 template <typename T, bool VEC, bool E5> cudaError_t quant(const QuantRows& a, cudaStream_t st) {
   const int bpr = f8_blocks(a.C), EP = f8_exps(a.C);
-  if constexpr (VEC) {
-    const long long total = a.R * bpr;
-    auto k = a.source ? k_quant_f8<T, E5, true> : k_quant_f8<T, E5, false>;
-    return launch_k(k, dim3(grid_of(total, 32 * kBatch)), dim3(256), 0, st, 1, a, bpr, EP, total);
-  } else {
-    const int wpr = (bpr + 1) / 2;
-    const long long total = a.R * wpr;
-    auto k = a.source ? k_quant_f8_odd<T, E5, true> : k_quant_f8_odd<T, E5, false>;
-    return launch_k(k, dim3(grid_of(total, 8 * kOddBatch)), dim3(256), 0, st, 1, a, bpr, EP, wpr, total);
-  }
+  const long long total = a.R * bpr;
+  auto k = a.source ? k_quant_f8<T, VEC, E5, true> : k_quant_f8<T, VEC, E5, false>;
+  return launch_k(k, dim3(grid_of(total, 32 * kBatch)), dim3(256), 0, st, 1, a, bpr, EP, total);
 }
 template <typename T, bool VEC, bool E5>
 cudaError_t dequant(long long R, int C, const uint8_t* q, const uint8_t* e, void* x, cudaStream_t st) {

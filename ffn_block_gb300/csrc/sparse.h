@@ -74,9 +74,8 @@ inline int f8_pitch(int cols) { return f8_blocks(cols) * kF8Block; }
 // Blocks of 128 rows that M rows in G groups take at most.
 inline int ragged_blocks(int M, int G) { return M / kF8Block + (G < M ? G : M); }
 
-// source (may be null): row i is x[source[i] / k], rows with no source in
-// [0, rows) are left out; x_rows bounds the index.  out (may be null): the
-// gathered row itself.
+// source (may be null): row i is x[source[i] / k], rows with no source in [0, R)
+// are left out.  out (may be null): the gathered row itself.
 struct QuantRows {
   long long R;
   int C, dtype, format;
