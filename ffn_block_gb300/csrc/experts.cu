@@ -8,6 +8,10 @@
 // to 49,152 by a cluster of eight, whose CTAs read one another's counts, in one
 // launch; more by three launches: each warp counts its share, each expert's counts
 // are summed over the warps, and each warp places its share.
+//
+// The rows are bound by HBM.  65,536 tokens to two of 64 experts, 1280 bf16 columns:
+// sort 13 us, gather 95 us (336 MB written: 84 us at the rate of pure writes, 4.0
+// TB/s), combination 76 us (6.6 TB/s), its backward 139 us (6.0 TB/s).
 
 #include "common.cuh"
 #include "kernels.h"

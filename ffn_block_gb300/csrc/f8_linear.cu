@@ -25,6 +25,18 @@
 // Groups are tokens of a per-token layer, or experts with rows given by offsets in
 // device memory; the weight gradient contracts over a group's rows, whose columns
 // then lie in blocks of 128 rows, each group's from a block of its own on.
+//
+// Measured (GB300): 8192 tokens through 4096 -> 4096 74 us (3.7 PFLOP/s), 1024 x 64
+// tokens through 1280 -> 5120 371 us (2.3 PFLOP/s), 32,768 rows of 32 experts through
+// 1280 -> 2560 80 us (2.7), the weight gradient of that 93 us (2.3), one sample x 64
+// tokens through 1280 -> 5120 66 us (6.3 TB/s, 95% of the copy rate).  A tile of N
+// tokens takes as long as N + 118 columns would at the tensor cores' best, so tiles
+// are as wide as tensor memory allows (32,768 rows as above: 224 tokens 85 us, 192
+// 86, 160 95, 128 107).  Products of few k are bound by their outputs: a plain fill
+// writes 3.5 to 4.0 TB/s (16,384 tokens 256 -> 2560 27 us, of which 25 for 84 MB).
+// Not kept: outputs in 16-byte pieces of eight tokens (the 371 us 434), through
+// shared memory as whole rows (447), more epilogue warps (366 to 377), the next
+// tile's operands prefetched to L2 (372).
 
 #include <cuda.h>
 

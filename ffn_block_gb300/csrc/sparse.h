@@ -46,7 +46,7 @@ struct LnBwd {
   void *dr, *dx;            // dx may be null
   float *pg, *pb;
 };
-constexpr int kLnBwdMaxBlocks = 912;
+constexpr int kLnBwdMaxBlocks = 512;
 int ln_bwd_rows_blocks(const LnBwd& a);
 cudaError_t launch_layer_norm_bwd(const LnBwd& a, cudaStream_t st);
 
