@@ -53,6 +53,13 @@ template <int L, bool VEC> __device__ __forceinline__ void mask_end(float2 (&v)[
     if (col<L, VEC>(c0, i) >= C) (i & 1 ? v[i / 2].y : v[i / 2].x) = 0.f;
 }
 
+// A lane's eight column sums to a row of partials (rows of it start anywhere).
+template <int L, bool VEC> __device__ __forceinline__ void store_partial(float* row, int c0, int C, const float2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (col<L, VEC>(c0, i) < C) row[col<L, VEC>(c0, i)] = i & 1 ? v[i / 2].y : v[i / 2].x;
+}
+
 // ---------------------------------------------------------------- dropout
 // A unit is a block of 8 * L columns of a row, a lane takes eight of them;
 // kUnits units at a time, so that their loads are in flight together.  (The units'
@@ -134,7 +141,8 @@ cudaError_t dropout_t(long long R, int C, const Drop& d, const void* x, const vo
 // that a segment lies in, and the segment starts inside the first of them; of the
 // tensor's last vector, where it is not a whole one, the elements are loaded one
 // by one.
-constexpr int kRingSmem = 200 * 1024, kRingMaxDepth = 3, kRingParams = 24 * 1024;
+constexpr int kRingSmem = 200 * 1024, kRingParams = 24 * 1024;  // forward
+constexpr int kBwdRingSmem = 220 * 1024, kRingMaxDepth = 3;
 constexpr uint64_t kDrainNs = 50ull * 1000ull * 1000ull;
 template <typename T, bool VEC> constexpr int ring_pitch(int nch) { return nch * 256 + (VEC ? 0 : 32 / (int)sizeof(T)); }
 template <typename T, int NCH, bool VEC> struct RowRing {
@@ -254,19 +262,21 @@ template <typename T, int NCH, bool VEC> struct RowRing {
 struct RingSpread {
   int W, nch, rpb, depth, smem;
 };
-RingSpread ring_spread(long long R, int C, int dtype, int nt, int threads) {
+// `few`: the number of blocks to stay at as long as a warp has no second row (0: no
+// such wish).
+RingSpread ring_spread(long long R, int C, int dtype, int nt, int threads, int smem, long long few = 0) {
   RingSpread s;
   const int blocks = (C + 255) / 256;
   s.W = (blocks + 4) / 5;
   s.nch = (blocks + s.W - 1) / s.W;
   const int e = dtype == 0 ? 4 : 2, row_bytes = nt * (s.nch * 256 * e + (rows_aligned(C, e) ? 0 : 32));
-  int warps = kRingSmem / (2 * row_bytes);
+  int warps = smem / (2 * row_bytes);
   if (warps > threads / 32) warps = threads / 32;
   s.rpb = warps / s.W;
   // Few rows: on as many SMs as there are.
-  const long long share = (R + sm_count() - 1) / sm_count();
+  const long long on = few && R <= few * s.rpb ? few : sm_count(), share = (R + on - 1) / on;
   if (s.rpb > share) s.rpb = (int)share;
-  s.depth = s.rpb > 0 ? kRingSmem / (s.rpb * s.W * row_bytes) : 0;
+  s.depth = s.rpb > 0 ? smem / (s.rpb * s.W * row_bytes) : 0;
   if (s.depth > kRingMaxDepth) s.depth = kRingMaxDepth;
   s.smem = s.rpb * s.W * s.depth * row_bytes;
   return s;
@@ -520,7 +530,7 @@ Spread fwd_spread(int C) {
 }
 template <typename T, bool VEC> cudaError_t layer_norm(const LnFwd& a, cudaStream_t st) {
   if (a.C > 512) {
-    const RingSpread r = ring_spread(a.R, a.C, a.dtype, a.r ? 2 : 1, kFwdRingThreads);
+    const RingSpread r = ring_spread(a.R, a.C, a.dtype, a.r ? 2 : 1, kFwdRingThreads, kRingSmem);
     if (r.rpb >= 1) return layer_norm_ring<T, VEC>(a, r, st);
   }
   const Spread s = fwd_spread(a.C);
@@ -544,7 +554,7 @@ template <typename T, int L, int NCH, int RB, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_layer_norm_bwd(const LnBwd a, const int W, const int rpb) {
   pdl_enter();
   __shared__ float red[64];
-  extern __shared__ float cols[];  // partials of the block's sets of warps, [sets - 1][2][C]
+  extern __shared__ float cols[];  // partials of the block's sets of warps
   const int lane = threadIdx.x & (L - 1), part = threadIdx.x / L, rib = part / W, w = part - rib * W;
   const DropBits bits = drop_bits(a.drop);
   const float inv_n = 1.f / (float)a.C;
@@ -645,44 +655,39 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_layer_norm_bwd(co
   // The block's partials: parts of a warp in a tree of shuffles, then the sets
   // of warps in order, the first adding the others' to its own.
   const int sets = L == 32 ? rpb : blockDim.x / 32, set = L == 32 ? rib : threadIdx.x >> 5;
+  const int set_size = 2 * W * NCH * 8 * L;  // [2][W][NCH][8][L]
+  float* mine = cols + w * (NCH * 8 * L) + lane;
   auto each = [&](auto f) {
 #pragma unroll
     for (int j = 0; j < NCH; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = col<L, VEC>(c_of(j), i);
-        f(i & 1 ? ag[j][i / 2].y : ag[j][i / 2].x, i & 1 ? ab[j][i / 2].y : ab[j][i / 2].x, c);
-      }
+      for (int i = 0; i < 8; ++i)
+        f(i & 1 ? ag[j][i / 2].y : ag[j][i / 2].x, i & 1 ? ab[j][i / 2].y : ab[j][i / 2].x, (j * 8 + i) * L);
   };
-  each([&](float& g, float& b, int c) {
+  each([&](float& g, float& b, int at) {
 #pragma unroll
     for (int o = L; o < 32; o <<= 1) {
       g += __shfl_xor_sync(0xffffffffu, g, o);
       b += __shfl_xor_sync(0xffffffffu, b, o);
     }
-    if (set > 0 && c < a.C) {
-      cols[(2 * (set - 1)) * a.C + c] = g;
-      cols[(2 * (set - 1) + 1) * a.C + c] = b;
+    if (set > 0) {  // (the parts of a warp write the same values)
+      mine[(set - 1) * set_size + at] = g;
+      mine[(set - 1) * set_size + set_size / 2 + at] = b;
     }
   });
   if (sets > 1) __syncthreads();
   if (set > 0) return;
 #pragma unroll 1
-  for (int r = 1; r < sets; ++r)
-    each([&](float& g, float& b, int c) {
-      if (c < a.C) {
-        g += cols[(2 * (r - 1)) * a.C + c];
-        b += cols[(2 * (r - 1) + 1) * a.C + c];
-      }
+  for (int r = 0; r < sets - 1; ++r)
+    each([&](float& g, float& b, int at) {
+      g += mine[r * set_size + at];
+      b += mine[r * set_size + set_size / 2 + at];
     });
-  float* pg = a.pg + (size_t)blockIdx.x * a.C;
-  float* pb = a.pb + (size_t)blockIdx.x * a.C;
-  each([&](float& g, float& b, int c) {
-    if (c < a.C) {
-      pg[c] = g;
-      pb[c] = b;
-    }
-  });
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    store_partial<L, VEC>(a.pg + (size_t)blockIdx.x * a.C, c_of(j), a.C, ag[j]);
+    store_partial<L, VEC>(a.pb + (size_t)blockIdx.x * a.C, c_of(j), a.C, ab[j]);
+  }
 }
 
 template <typename T, int NCH, bool VEC>
@@ -789,43 +794,51 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
   ring.drain(gave_up, err);
   __syncthreads();
   // The block's partials: the rows' sets of warps in order, the first adding the
-  // others' to its own.
-  float* cols = reinterpret_cast<float*>(ring_smem);  // [rpb - 1][2][C]
+  // others' to its own.  Each lane's values lie with its neighbours' (in the order of
+  // the columns, eight a lane, they would share banks: 500 rows of 1280 14.6 us, like
+  // this 10.0.)
+  float* cols = reinterpret_cast<float*>(ring_smem);  // [rpb - 1][2][W][NCH][8][32]
+  const int set_size = 2 * W * SEG;
+  float* mine = cols + w * SEG + lane;
   auto each = [&](auto f) {
 #pragma unroll
     for (int j = 0; j < NCH; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = col<32, VEC>(seg0 + col0<32, VEC>(j, lane), i);
-        if (c < a.C) f(i & 1 ? ag[j][i / 2].y : ag[j][i / 2].x, i & 1 ? ab[j][i / 2].y : ab[j][i / 2].x, c);
-      }
+      for (int i = 0; i < 8; ++i)
+        f(i & 1 ? ag[j][i / 2].y : ag[j][i / 2].x, i & 1 ? ab[j][i / 2].y : ab[j][i / 2].x, (j * 8 + i) * 32);
   };
   if (rib > 0)
-    each([&](float& g, float& b, int c) {
-      cols[(2 * (rib - 1)) * a.C + c] = g;
-      cols[(2 * (rib - 1) + 1) * a.C + c] = b;
+    each([&](float& g, float& b, int at) {
+      mine[(rib - 1) * set_size + at] = g;
+      mine[(rib - 1) * set_size + W * SEG + at] = b;
     });
   __syncthreads();
   if (rib > 0) return;
 #pragma unroll 1
-  for (int r = 1; r < rpb; ++r)
-    each([&](float& g, float& b, int c) {
-      g += cols[(2 * (r - 1)) * a.C + c];
-      b += cols[(2 * (r - 1) + 1) * a.C + c];
+  for (int r = 0; r < rpb - 1; ++r)
+    each([&](float& g, float& b, int at) {
+      g += mine[r * set_size + at];
+      b += mine[r * set_size + W * SEG + at];
     });
-  each([&](float& g, float& b, int c) {
-    a.pg[(size_t)blockIdx.x * a.C + c] = g;
-    a.pb[(size_t)blockIdx.x * a.C + c] = b;
-  });
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    const int c0 = seg0 + col0<32, VEC>(j, lane);
+    store_partial<32, VEC>(a.pg + (size_t)blockIdx.x * a.C, c0, a.C, ag[j]);
+    store_partial<32, VEC>(a.pb + (size_t)blockIdx.x * a.C, c0, a.C, ab[j]);
+  }
 }
 
-RingSpread bwd_ring_spread(const LnBwd& a) { return ring_spread(a.R, a.C, a.dtype, a.dh ? 3 : 2, kBwdRingThreads); }
+// As long as a warp has no second row, the partials stay at this many rows.
+constexpr long long kFewBlocks = 64;
+RingSpread bwd_ring_spread(const LnBwd& a) {
+  return ring_spread(a.R, a.C, a.dtype, a.dh ? 3 : 2, kBwdRingThreads, kBwdRingSmem, kFewBlocks);
+}
 template <typename T, bool VEC> cudaError_t layer_norm_bwd_ring(const LnBwd& a, cudaStream_t st) {
   const RingSpread s = bwd_ring_spread(a);
   auto k = s.nch == 3   ? k_layer_norm_bwd_ring<T, 3, VEC>
            : s.nch == 4 ? k_layer_norm_bwd_ring<T, 4, VEC>
                         : k_layer_norm_bwd_ring<T, 5, VEC>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdRingSmem);
   if (e != cudaSuccess) return e;
   return launch_k(k, dim3((unsigned)ln_bwd_rows_blocks(a)), dim3(32 * s.W * s.rpb), s.smem, st, 1, a, s.W, s.rpb, s.depth,
                   device_error_word(), (unsigned long long)kWaitLimitNs);
@@ -850,7 +863,7 @@ template <typename T, bool VEC> cudaError_t layer_norm_bwd(const LnBwd& a, cudaS
   if (ring_takes(a)) return layer_norm_bwd_ring<T, VEC>(a, st);
   const Spread s = bwd_spread(a.C);
   const int sets = s.L == 32 ? s.rpb : s.threads / 32;
-  const size_t smem = (size_t)(sets - 1) * 2 * a.C * sizeof(float);  // 28 KB at most
+  const size_t smem = (size_t)(sets - 1) * 2 * s.W * s.nch * 8 * s.L * sizeof(float);  // 28 KB at most
   constexpr int RB = kBwdRows<T>;
   auto k = s.L == 8     ? k_layer_norm_bwd<T, 8, 1, RB, VEC, 256>
            : s.L == 16  ? k_layer_norm_bwd<T, 16, 1, RB, VEC, 256>
@@ -881,7 +894,10 @@ int ln_bwd_rows_blocks(const LnBwd& a) {
   // As many as are resident at once (two an SM, one where the row has 16 warps);
   // few rows: as many as there are.
   const Spread s = bwd_spread(a.C);
-  return at_most((a.R + s.rpb - 1) / s.rpb, (long long)sm_count() * (s.threads > 256 ? 1 : 2));
+  const int rows = s.nch == 4 ? 1 : (a.dtype == 0 ? 2 : 4) / s.nch;  // of a thread at a time
+  const long long all = (a.R + s.rpb - 1) / s.rpb;
+  if (all > kFewBlocks && a.R <= kFewBlocks * s.rpb * rows) return (int)kFewBlocks;
+  return at_most(all, (long long)sm_count() * (s.threads > 256 ? 1 : 2));
 }
 cudaError_t launch_layer_norm_bwd(const LnBwd& a, cudaStream_t st) {
   RMX_BY_DTYPE(a.dtype,
