@@ -15,6 +15,8 @@
 //   warps 4-7   exponents: 512 k of them at a time from global into tensor
 //               memory, a warp to each quarter of its lanes
 //   warps 8-15  epilogue: a channel a thread, 16 tokens at a time
+// Few tiles with many steps of k: a cluster of two, four or eight CTAs shares a tile's
+// steps and adds the sums up through distributed shared memory (split_of).
 // TMEM: two accumulators of up to 224 columns (the epilogue of one tile overlaps
 // the next), then four places of 12 columns for exponents.
 //
@@ -54,7 +56,7 @@ namespace {
 constexpr int kFirstExp = 4, kFirstEpi = 8, kEpiWarps = 8, kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kK = 128;                // k of a stage: a block of exponents, a 128-byte row
 constexpr int kMaxStages = 8, kSlots = 4, kSlotCols = 12;
-constexpr int kMaxNT = 224;
+constexpr int kMaxNT = 224, kMaxSplit = 8;
 constexpr int kTmemCols = 512, kAccCols = kMaxNT, kExpCol0 = 2 * kAccCols;
 constexpr int kBarBytes = 256;
 constexpr int kSmemMax = 226 * 1024;  // and a little static shared memory
@@ -66,6 +68,7 @@ struct Params {
   int nkb;                     // blocks of k (weight gradient with offsets: by group)
   int nt, ntc;                 // tokens of a tile, and a CTA's share
   int stage_bytes, stages;
+  int split;                   // CTAs that share a tile's blocks of k (SPLIT)
   int tiles_m, tiles_n, num_tiles;  // (tiles_m, num_tiles: without offsets, or weight gradient)
   int rows_end;                // last row + 1 of the token operand, for the exponents
   uint32_t idesc;
@@ -111,7 +114,16 @@ __device__ __forceinline__ void tmem_st_32x8(uint32_t addr, const uint32_t* r) {
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-template <typename T, bool PAIR, int MODE>
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// SPLIT: the CTAs of a cluster each take a share of one tile's blocks of k and leave
+// their sums in shared memory; then each adds up every p.split-th token's, in the
+// order of the shares, and stores them.  A cluster has one tile.
+template <typename T, bool PAIR, int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT, const Params p) {
   pdl_trigger();
@@ -137,8 +149,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)cluster_rank() : 0;
-  const int tile0 = PAIR ? (int)cluster_id_x() : (int)blockIdx.x;
-  const int stride = PAIR ? (int)num_clusters_x() : (int)gridDim.x;
+  const int tile0 = PAIR || SPLIT ? (int)cluster_id_x() : (int)blockIdx.x;
+  const int stride = PAIR || SPLIT ? (int)num_clusters_x() : (int)gridDim.x;
+  const int share = SPLIT ? (int)cluster_rank() : 0;
   constexpr int CTAS = PAIR ? 2 : 1;
   constexpr Order CROSS = PAIR ? TENSOR : LOCAL;
   constexpr bool OFFSETS = MODE == RAGGED || MODE == WGRAD_RAGGED;
@@ -201,6 +214,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.n0 = tn * 128 * CTAS + rank * 128;
     t.kb0 = MODE == WGRAD_RAGGED ? before[t.g] : 0;
     t.nkb = MODE == WGRAD_RAGGED ? before[t.g + 1] - before[t.g] : p.nkb;
+    if (SPLIT) {
+      const int k0 = (int)((long long)t.nkb * share / p.split);
+      t.nkb = (int)((long long)t.nkb * (share + 1) / p.split) - k0;
+      t.kb0 += k0;
+    }
     return t;
   };
 
@@ -223,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = sRing + (uint32_t)(s * p.stage_bytes), fb = full0 + 8u * (uint32_t)s;
           // Channels {k, N, G}; tokens {k, G, M}, or {k, K, G} of a weight gradient;
           // by expert its operands lie block by block, {128, N or K, block}.
-          const int x = MODE == WGRAD_RAGGED ? 0 : kb * kK, wg = MODE == WGRAD_RAGGED ? t.kb0 + kb : t.g;
+          const int x = MODE == WGRAD_RAGGED ? 0 : (t.kb0 + kb) * kK, wg = MODE == WGRAD_RAGGED ? t.kb0 + kb : t.g;
           const int c1 = MODE == EQUAL ? t.g : MODE == RAGGED ? 0 : mr, c2 = MODE == WGRAD || MODE == WGRAD_RAGGED ? wg : mr;
           if (PAIR) {
             tma_load_3d_pair(dst, &tmW, fb, x, t.n0, wg);
@@ -390,6 +408,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_warp<CROSS>(d_full(acc), (uint32_t)(lt >> 1) & 1u, ERRBIT_WAIT_EPILOGUE, wc)) break;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kAccCols);
+      if constexpr (SPLIT) {
+        // Sums [token][128 channels], where the ring was: every copy has landed and
+        // been multiplied once the MMAs are done.
+#pragma unroll 1
+        for (int c0 = 16 * odd; c0 < t.live; c0 += 32) {
+          float v[16];
+          tmem_ld_32x16(d + c0, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sRing + (uint32_t)((c0 + i) * 512 + (q * 32 + lane) * 4)),
+                         "f"(t.nkb == 0 ? 0.f : v[i])
+                         : "memory");
+        }
+        continue;
+      }
       const size_t step = (size_t)p.out_row;
       size_t at = (size_t)(t.m0 + 16 * odd) * step + (MODE == RAGGED ? 0 : (size_t)t.g * p.out_group) + n;
       // Up to 16 tokens of this lane's channel (inlined twice: `cols` is 16 for
@@ -432,37 +465,104 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // Neither CTA of a pair leaves while the other may still read its shared
   // memory or signal its barriers; TMEM is freed by both together.
-  if (PAIR) cluster_barrier();
+  if (PAIR || SPLIT) cluster_barrier();
+  if constexpr (SPLIT) {
+    if (warp >= kFirstEpi) {
+      const Tile t = tile_of(tile0);
+      const int ch = (warp & 3) * 32 + lane, odd = (warp - kFirstEpi) >> 2, n = t.n0 + ch;
+      if (n < p.N) {
+        const float bias = p.bias ? to_f(static_cast<const T*>(p.bias)[(size_t)t.g * p.N + n]) : 0.f;
+        const size_t at = (size_t)t.m0 * p.out_row + (size_t)t.g * p.out_group + n;
+        uint32_t sums[kMaxSplit];  // this channel's of each share
+#pragma unroll
+        for (int k = 0; k < kMaxSplit; ++k) sums[k] = mapa_shared(sRing + 4u * (uint32_t)ch, k < p.split ? (uint32_t)k : 0u);
+        // Two tokens at a time (eight: a microsecond more for one token).
+        constexpr int TOK = 2;
+#pragma unroll 1
+        for (int c0 = share + p.split * odd; c0 < t.live; c0 += 2 * TOK * p.split) {
+          float x[TOK][kMaxSplit];
+#pragma unroll
+          for (int i = 0; i < TOK; ++i) {
+            const int c = c0 + 2 * i * p.split;
+#pragma unroll
+            for (int k = 0; k < kMaxSplit; ++k) {
+              x[i][k] = 0.f;
+              if (k < p.split && c < t.live) x[i][k] = ld_cluster_f32(sums[k] + (uint32_t)c * 512u);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < TOK; ++i) {
+            const int c = c0 + 2 * i * p.split;
+            if (c >= t.live) break;
+            float v = x[i][0];
+#pragma unroll
+            for (int k = 1; k < kMaxSplit; ++k) v += x[i][k];
+            v += bias;
+            const size_t o = at + (size_t)c * p.out_row;
+            if (p.resid) v += to_f(static_cast<const T*>(p.resid)[o]);
+            static_cast<T*>(p.out)[o] = from_f<T>(v);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    cluster_barrier();  // the others may still be reading this CTA's sums
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<PAIR>(tmem, kTmemCols);
   }
 }
 
-template <typename T, bool PAIR, int MODE>
+template <typename T, bool PAIR, int MODE, bool SPLIT>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& t, const Params& p, long long tiles, cudaStream_t st) {
-  auto k = k_linear_f8<T, PAIR, MODE>;
+  auto k = k_linear_f8<T, PAIR, MODE, SPLIT>;
   const int extra = kBarBytes + (MODE == RAGGED || MODE == WGRAD_RAGGED ? 2 * (p.G + 1) * (int)sizeof(int) : 0);
   const int smem = 1024 + p.stages * p.stage_bytes + extra;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
-  const int cluster = PAIR ? 2 : 1, slots = sm_count() / cluster;
-  const int n = tiles < slots ? (int)tiles : slots;
+  const int cluster = SPLIT ? p.split : PAIR ? 2 : 1;
+  const long long slots = SPLIT ? tiles : sm_count() / cluster;
+  const int n = (int)(tiles < slots ? tiles : slots);
   return launch_k(k, dim3(cluster * n), dim3(kThreads), smem, st, cluster, w, t, p);
 }
-template <typename T, bool PAIR>
-cudaError_t by_mode(int mode, const CUtensorMap& w, const CUtensorMap& t, const Params& p, long long tiles, cudaStream_t st) {
-  switch (mode) {
-    case EQUAL: return launch<T, PAIR, EQUAL>(w, t, p, tiles, st);
-    case RAGGED: return launch<T, PAIR, RAGGED>(w, t, p, tiles, st);
-    case WGRAD: return launch<T, PAIR, WGRAD>(w, t, p, tiles, st);
-    default: return launch<T, PAIR, WGRAD_RAGGED>(w, t, p, tiles, st);
+template <typename T, int MODE>
+cudaError_t by_size(bool pair, const CUtensorMap& w, const CUtensorMap& t, const Params& p, long long tiles, cudaStream_t st) {
+  if (pair) return launch<T, true, MODE, false>(w, t, p, tiles, st);
+  if constexpr (MODE != RAGGED) {
+    if (p.split > 1) return launch<T, false, MODE, true>(w, t, p, tiles, st);
   }
+  return launch<T, false, MODE, false>(w, t, p, tiles, st);
 }
 template <typename T>
 cudaError_t dispatch(bool pair, int mode, const CUtensorMap& w, const CUtensorMap& t, const Params& p, long long tiles,
                      cudaStream_t st) {
-  return pair ? by_mode<T, true>(mode, w, t, p, tiles, st) : by_mode<T, false>(mode, w, t, p, tiles, st);
+  switch (mode) {
+    case EQUAL: return by_size<T, EQUAL>(pair, w, t, p, tiles, st);
+    case RAGGED: return by_size<T, RAGGED>(pair, w, t, p, tiles, st);
+    case WGRAD: return by_size<T, WGRAD>(pair, w, t, p, tiles, st);
+    default: return by_size<T, WGRAD_RAGGED>(pair, w, t, p, tiles, st);
+  }
+}
+
+// CTAs to a tile of nt tokens and `steps` blocks of k (CTAs alone).  Few tiles leave
+// most SMs idle; a step takes about 0.23 us, and sharing costs about 0.6 us and, for
+// each token, 0.035, 0.022 or 0.016 us with two, four or eight CTAs (two cluster
+// barriers, and the sums' way through distributed shared memory).  36 clusters of
+// four, 76 of two and 15 of eight fit the GPU at once.  us, one CTA / two / four /
+// eight to a tile:
+//   15 tiles: 1 token 4096 -> 1920 11.4 / 9.2 / 7.5 / 6.2, 224 tokens 1024 -> 1920
+//   6.4 / 14.0 / 10.5 / 9.1, 4096 -> 1920 13.1 / 17.6 / 13.0 / 10.5
+//   32 tiles: 8 tokens 4096 -> 4096 11.3 / 9.3 / 7.8, 200 tokens 12.8 / 17.0 / 12.6
+//   71 tiles: 1 token 4096 -> 9088 11.4 / 9.4, 1024 -> 9088 5.8 / 6.1
+//   weight gradients: 23,770 rows, 1701 x 212 77 / 46 / 29, 65,536 rows, 224 x 1280
+//   282 / 131 / 67 / 38
+int split_of(long long tiles, int nt, long long steps) {
+  for (int s = kMaxSplit; s > 1; s /= 2) {
+    const long long fit = s == 8 ? 15 : s == 4 ? 36 : 72;
+    if (tiles <= fit && steps * 23 * (s - 1) > 60 * s + (long long)nt * (s + 5)) return s;
+  }
+  return 1;
 }
 
 int mode_of(const LinearF8& d) {
@@ -496,6 +596,9 @@ bool plan(const LinearF8& d, Params& p, bool& pair, long long& tiles) {
   tiles = mt * p.tiles_n;
   if (tiles > (1ll << 30)) return false;
   p.num_tiles = (int)tiles;
+  // Blocks of k of a tile: a group's share of them where they go by expert.
+  const long long steps = mode == WGRAD_RAGGED ? (f8_blocks(d.M) + d.G - 1) / d.G : p.nkb;
+  p.split = pair || mode == RAGGED ? 1 : split_of(tiles, p.nt, steps);
   // Strides of a tensor map: below 2^40 bytes.
   const long long pitch = mode == WGRAD_RAGGED ? kK : (long long)p.nkb * kK;
   const long long most = d.K > d.N && d.wgrad ? d.K : d.N;

@@ -248,6 +248,14 @@ def test_product_of_pairs(M, G, K, N, dt):
     _product(M, G, K, N, dt, "e4m3", "e5m2")
 
 
+# both sides of the rules on sharing a tile: eight, four and two CTAs to one, uneven shares, residuals
+@pytest.mark.parametrize("M,G,K,N", [(1, 1, 4096, 1920), (3, 1, 1100, 300), (7, 2, 4000, 900), (200, 1, 6000, 500), (30, 2, 2000, 2100),
+                                     (9, 3, 4099, 1300), (16, 1, 1025, 130), (2, 4, 5000, 2200), (224, 1, 8200, 129)])
+def test_product_of_shared_tiles(M, G, K, N):
+    _product(M, G, K, N, "f32", "e4m3", "e5m2", bias=True, resid=True, spread=1)
+    _product(M, G, K, N, "bf16", "e4m3", "e4m3", bias=False, spread=1)
+
+
 def test_product_in_place_of_the_residual():
     rng = np.random.default_rng(3)
     M, G, K, N = 90, 2, 256, 136
@@ -318,7 +326,8 @@ def test_product_by_expert_all_to_one():
 # ------------------------------------------------------------------ the weight gradient
 @pytest.mark.parametrize("order", ["tokens", "ragged"])
 @pytest.mark.parametrize("M,G,K,N,dt", [(1, 1, 1, 1, "f32"), (40, 2, 64, 130, "f32"), (300, 3, 200, 136, "bf16"), (129, 1, 257, 300, "f16"),
-                                        (1000, 6, 96, 72, "f32"), (700, 30, 300, 520, "bf16"), (520, 200, 40, 24, "f32")])
+                                        (1000, 6, 96, 72, "f32"), (700, 30, 300, 520, "bf16"), (520, 200, 40, 24, "f32"),
+                                        (9000, 1, 130, 140, "f32"), (12000, 3, 200, 300, "bf16"), (20001, 2, 24, 500, "f32")])
 def test_weight_gradient(order, M, G, K, N, dt):
     rng = np.random.default_rng(M + K)
     ragged = order == "ragged"
