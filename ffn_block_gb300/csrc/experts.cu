@@ -571,8 +571,7 @@ cudaError_t launch_expert_sort(const Routes& r, const int32_t* expert, int32_t* 
     const int threads = 32 * nw > (E + 31) / 32 * 32 ? 32 * nw : (E + 31) / 32 * 32;
     const int smem = (nw + 1) * E * (int)sizeof(int);  // 132 KB at most
     auto k = one ? k_sort<1> : k_sort<kCluster>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (kWarps + 1) * kMaxExperts * (int)sizeof(int));
+    cudaError_t e = allow_smem(k, smem, (kWarps + 1) * kMaxExperts * (int)sizeof(int));
     if (e != cudaSuccess) return e;
     return launch_k(k, dim3(one ? 1 : kCluster), dim3(threads), smem, st, one ? 1 : kCluster, r.S, E, nw, share, expert, offsets,
                     position, source);

@@ -540,8 +540,7 @@ template <typename T, bool VEC, bool E5> cudaError_t quant_groups(const QuantGro
   const int ctiles = f8_blocks(a.C);
   const int smem = kTile * kTile * (int)sizeof(T) + (a.offsets ? 2 * (a.G + 1) * (int)sizeof(int) : 0);
   auto k = a.part ? k_quant_groups<T, VEC, E5, true> : k_quant_groups<T, VEC, E5, false>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kTile * kTile * (int)sizeof(T) + 2 * (kMaxExperts + 1) * (int)sizeof(int));
+  cudaError_t e = allow_smem(k, smem, kTile * kTile * (int)sizeof(T) + 2 * (kMaxExperts + 1) * (int)sizeof(int));
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)a.blocks * ctiles, fit = (long long)sm_count() * (a.part ? quant_blocks<T, true> : quant_blocks<T, false>);
   return launch_k(k, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kThreads), smem, st, 1, a, ctiles, f8_exps(a.C));

@@ -53,4 +53,12 @@ cudaError_t launch_k(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cu
   return cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
 }
 
+// Allows a kernel `most` bytes of dynamic shared memory where a launch needs more than
+// every kernel may have (less a little static memory); the call costs the host about
+// as much as half a launch.
+template <typename K> cudaError_t allow_smem(K k, size_t need, int most) {
+  if (need <= 40 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 }  // namespace rmx

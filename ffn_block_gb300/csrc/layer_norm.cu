@@ -404,11 +404,12 @@ template <typename T, bool VEC> cudaError_t layer_norm_ring(const LnFwd& a, cons
   const int params = 2 * s.W * s.nch * 256 * (int)sizeof(T);
   // (Worth its wait where a warp has several rows.)
   const bool staged = (a.gamma || a.beta) && params <= kRingParams && a.R > 4ll * s.rpb * sm_count();
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem + kRingParams);
+  const size_t smem = s.smem + (staged ? params : 0);
+  cudaError_t e = allow_smem(k, smem, kRingSmem + kRingParams);
   if (e != cudaSuccess) return e;
   const long long want = (a.R + s.rpb - 1) / s.rpb;
   return launch_k(k, dim3((unsigned)(want < sm_count() ? want : sm_count())), dim3(32 * s.W * s.rpb),
-                  s.smem + (staged ? params : 0), st, 1, a, s.W, s.rpb, s.depth, staged, device_error_word(), (unsigned long long)kWaitLimitNs);
+                  smem, st, 1, a, s.W, s.rpb, s.depth, staged, device_error_word(), (unsigned long long)kWaitLimitNs);
 }
 
 // Other rows: a row belongs to L lanes of W warps (W > 1 only with L = 32), with
@@ -838,7 +839,7 @@ template <typename T, bool VEC> cudaError_t layer_norm_bwd_ring(const LnBwd& a, 
   auto k = s.nch == 3   ? k_layer_norm_bwd_ring<T, 3, VEC>
            : s.nch == 4 ? k_layer_norm_bwd_ring<T, 4, VEC>
                         : k_layer_norm_bwd_ring<T, 5, VEC>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdRingSmem);
+  cudaError_t e = allow_smem(k, s.smem, kBwdRingSmem);
   if (e != cudaSuccess) return e;
   return launch_k(k, dim3((unsigned)ln_bwd_rows_blocks(a)), dim3(32 * s.W * s.rpb), s.smem, st, 1, a, s.W, s.rpb, s.depth,
                   device_error_word(), (unsigned long long)kWaitLimitNs);
