@@ -278,7 +278,13 @@ RingSpread ring_spread(long long R, int C, int dtype, int nt, int threads, int s
   if (s.rpb > share) s.rpb = (int)share;
   s.depth = s.rpb > 0 ? smem / (s.rpb * s.W * row_bytes) : 0;
   if (s.depth > kRingMaxDepth) s.depth = kRingMaxDepth;
+  // No deeper than a warp has rows: with less shared memory a small launch starts sooner.
+  const long long at_once = (long long)sm_count() * s.rpb, rows = at_once > 0 ? (R + at_once - 1) / at_once : 0;
+  if (s.depth > rows) s.depth = (int)rows;
   s.smem = s.rpb * s.W * s.depth * row_bytes;
+  // The backward's partials take the ring's place at the end.
+  const int partials = (s.rpb - 1) * 2 * s.W * s.nch * 256 * (int)sizeof(float);
+  if (few && s.smem < partials) s.smem = partials;
   return s;
 }
 
@@ -874,8 +880,38 @@ template <typename T, bool VEC> cudaError_t layer_norm_bwd(const LnBwd& a, cudaS
   return launch_k(k, dim3((unsigned)ln_bwd_rows_blocks(a)), dim3(s.threads), smem, st, 1, a, s.W, s.rpb);
 }
 
+// ---------------------------------------------------------------- parameters
+// dgamma and dbeta from the blocks' partials: 32 columns a block, 16 warps each adding
+// up every 16th row of partials, then in order.
+constexpr int kParamWarps = 16;
+template <typename T>
+__global__ void __launch_bounds__(32 * kParamWarps) k_layer_norm_params(int P, int C, const float* pg, const float* pb, T* dgamma,
+                                                                        T* dbeta) {
+  pdl_enter();
+  __shared__ float sums[kParamWarps][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  T* out = blockIdx.y ? dbeta : dgamma;
+  if (!out) return;
+  const float* p = (blockIdx.y ? pb : pg) + c;
+  float s = 0.f;
+  if (c < C) {
+#pragma unroll 8
+    for (int r = warp; r < P; r += kParamWarps) s += p[(size_t)r * C];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp > 0 || c >= C) return;
+#pragma unroll
+  for (int w = 1; w < kParamWarps; ++w) s += sums[w][lane];
+  out[c] = from_f<T>(s);
+}
+
 }  // namespace
 
+cudaError_t launch_layer_norm_params(const LnBwd& a, void* dgamma, void* dbeta, cudaStream_t st) {
+  RMX_BY_DTYPE(a.dtype, return launch_k(k_layer_norm_params<T>, dim3((a.C + 31) / 32, 2), dim3(32 * kParamWarps), 0, st, 1,
+                                        ln_bwd_rows_blocks(a), a.C, (const float*)a.pg, (const float*)a.pb, (T*)dgamma, (T*)dbeta))
+}
 cudaError_t launch_dropout(long long R, int C, int dtype, const Drop& d, const void* x, const void* r, void* out,
                            cudaStream_t st) {
   RMX_BY_DTYPE(dtype, return dropout_t<T>(R, C, d, x, r, out, st))

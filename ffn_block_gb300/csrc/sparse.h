@@ -49,6 +49,8 @@ struct LnBwd {
 constexpr int kLnBwdMaxBlocks = 512;
 int ln_bwd_rows_blocks(const LnBwd& a);
 cudaError_t launch_layer_norm_bwd(const LnBwd& a, cudaStream_t st);
+// dgamma, dbeta (either may be null) from the partials.
+cudaError_t launch_layer_norm_params(const LnBwd& a, void* dgamma, void* dbeta, cudaStream_t st);
 
 // ---------------------------------------------------------------- routing
 constexpr int kMaxExperts = 1024;

@@ -140,14 +140,9 @@ rmx_status rmx_layer_norm_backward(const rmx_rows* shape, const rmx_drop* drop, 
     Launch l("layer_norm_backward", st);
     RMX_TRY(l.done(launch_layer_norm_bwd(a, st)));
   }
-  ColsumJob jobs[2];
-  int n = 0;
-  const int blocks = ln_bwd_rows_blocks(a);
-  if (dgamma) jobs[n++] = ColsumJob{pg, dgamma, blocks, shape->cols};
-  if (dbeta) jobs[n++] = ColsumJob{pb, dbeta, blocks, shape->cols};
-  if (n == 0) return RMX_OK;
+  if (!dgamma && !dbeta) return RMX_OK;
   Launch l("layer_norm_params", st);
-  return l.done(launch_colsums(jobs, n, shape->dtype, st));
+  return l.done(launch_layer_norm_params(a, dgamma, dbeta, st));
 }
 
 // ---------------------------------------------------------------- routing
