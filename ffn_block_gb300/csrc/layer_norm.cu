@@ -9,8 +9,8 @@
 // squared deviations), so a row far from zero loses nothing.
 //
 // Measured (GB300, 65,536 rows of 1280 bf16 columns, dropout and residual; a copy
-// moves 6.68 TB/s): forward 108 us (6.2 TB/s), backward 145 us with its column sums
-// (5.8 TB/s), dropout alone 76 us with a residual (6.6 TB/s) and 63 without (5.3:
+// moves 6.68 TB/s): forward 108 us (6.2 TB/s), backward 141 us with its column sums
+// (6.0 TB/s), dropout alone 76 us with a residual (6.6 TB/s) and 63 without (5.3:
 // there the generator's integer operations bound it).
 
 #include "common.cuh"
@@ -290,10 +290,10 @@ RingSpread ring_spread(long long R, int C, int dtype, int nt, int threads, int s
 
 // ---------------------------------------------------------------- forward
 // Forward: 16 warps of 128 registers two rows deep, gamma and beta in shared memory:
-// 117 us for 65,536 x 1280 (12 warps with them in registers 124, 20 or 24 warps,
-// which spill, 160 and 165; without a ring 130 to 200).  Backward: 8 warps of 255
-// registers, a row's values kept from its sums to its output: 145 us (12 warps that
-// work them out again 176, without a ring 350).
+// 108 us for 65,536 x 1280, when the choice was made 117 (12 warps with them in
+// registers 124, 20 or 24 warps, which spill, 160 and 165; without a ring 130 to
+// 200).  Backward: 8 warps of 255 registers, a row's values kept from its sums to its
+// output: 141 us, then 145 (12 warps that work them out again 176, without a ring 350).
 constexpr int kFwdRingThreads = 512, kBwdRingThreads = 256;
 template <typename T, int NCH, bool VEC>
 __global__ void __launch_bounds__(kFwdRingThreads, 1)
