@@ -178,3 +178,26 @@ def test_gather_to_8_bits(fmt, dt, T, k, C):
         ok(B.rmx_expert_gather(r, dev(src), x, out if beside else None, fmt, q2, e2))
         assert torch.equal(q, q2) and torch.equal(e, e2)
         assert not beside or torch.equal(out, rows)
+
+
+@pytest.mark.parametrize("T,k,E", [(500, 2, 40), (9000, 2, 64), (40000, 2, 64)])
+def test_sort_in_a_graph(T, k, E):
+    """One CTA, a cluster and three launches, captured and replayed with other experts."""
+    r = B.make_routes(T, k, E, 1, "f32")
+    nws = B.rmx_expert_sort_workspace_bytes(r)
+    ids, off, pos, src = (empty(n, torch.int32) for n in ((T, k), (E + 1,), (T, k), (T * k,)))
+    ws, st = empty((nws,), torch.uint8), torch.cuda.Stream()
+    ids.random_(0, E)
+    ok(B.rmx_expert_sort(r, ids, off, pos, src, ws, nws, st))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        ok(B.rmx_expert_sort(r, ids, off, pos, src, ws, nws, st))
+    for _ in range(2):
+        ids.random_(-1, E)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((off, pos, src), O.expert_sort(ids.cpu().numpy(), E)):
+            assert np.array_equal(a.cpu().numpy(), b)

@@ -327,3 +327,36 @@ def test_layer_norm_repeats_bit_for_bit():
         outs.append((dr, dg, db))
     assert all(torch.equal(a, b) for o in outs[1:] for a, b in zip(outs[0], o))
     sync()
+
+
+@pytest.mark.parametrize("C", [40, 333, 1001, 1280, 4104])
+def test_layer_norm_that_drops_everything(C):
+    """p = 1: the sum is the residual, whatever x holds, and no gradient reaches x."""
+    R = 200
+    s, d = B.make_rows(R, C, "bf16"), B.make_drop(1.0)
+    x, r, dy = full_of((R, C), "bf16", float("nan")), torch.randn((R, C), device="cuda").bfloat16(), torch.randn((R, C), device="cuda").bfloat16()
+    h, y, y2, mean, rstd = empty((R, C), "bf16"), empty((R, C), "bf16"), empty((R, C), "bf16"), empty((R,), "f32"), empty((R,), "f32")
+    ok(B.rmx_layer_norm(s, 1e-5, d, x, r, None, None, h, y, mean, rstd))
+    ok(B.rmx_layer_norm(s, 1e-5, None, r, None, None, None, None, y2, None, None))
+    assert torch.equal(h, r) and torch.equal(y, y2)
+    nws = B.rmx_layer_norm_backward_workspace_bytes(s)
+    dr, dr2, dx, ws = empty((R, C), "bf16"), empty((R, C), "bf16"), full_of((R, C), "bf16", 1.0), empty((nws,), torch.uint8)
+    ok(B.rmx_layer_norm_backward(s, d, dy, None, h, mean, rstd, None, dr, dx, None, None, ws, nws))
+    ok(B.rmx_layer_norm_backward(s, None, dy, None, h, mean, rstd, None, dr2, None, None, None, ws, nws))
+    assert not dx.any() and torch.equal(dr, dr2)
+
+
+@pytest.mark.parametrize("R", [3, 5000])
+@pytest.mark.parametrize("C", [72, 513, 1280])
+def test_layer_norm_with_one_parameter(R, C):
+    """gamma without beta and beta without gamma: as with ones and zeros in the other's place.  Either side rounds the
+    product twice and the sum once, or product and sum together: 2 |product| + |y| <= 3 |y| + 2 |beta| units each."""
+    s = B.make_rows(R, C, "f32")
+    x, g = torch.randn((R, C), device="cuda"), torch.randn(C, device="cuda")
+    one, zero = torch.ones(C, device="cuda"), torch.zeros(C, device="cuda")
+    for a, b in ((None, g), (g, None)):
+        y, y2 = empty((R, C), "f32"), empty((R, C), "f32")
+        ok(B.rmx_layer_norm(s, 1e-5, None, x, None, a, b, None, y, None, None))
+        ok(B.rmx_layer_norm(s, 1e-5, None, x, None, one if a is None else a, zero if b is None else b, None, y2, None, None))
+        ref, beta = f64(y2), 0.0 if b is None else np.abs(f64(b))
+        within(f64(y), ref, 2 * E32 * (3 * np.abs(ref) + 2 * beta) * (1 + 2.0 ** -20))
