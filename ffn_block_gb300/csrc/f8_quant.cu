@@ -270,11 +270,17 @@ template <typename T> __device__ __forceinline__ uint32_t half_bits(uint32_t h) 
   if (std::is_same<T, bf16>::value) return h << 16;
   return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
 }
-// 32 bytes to one sector.
-__device__ __forceinline__ void st_sector(uint8_t* p, const uint32_t (&o)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]),
-               "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-               : "memory");
+// 32 bytes to one sector, `whole` where p is on a boundary of 32 bytes (pointers are
+// only known to be on one of 16); else as two vectors.
+__device__ __forceinline__ void st_sector(uint8_t* p, const uint32_t (&o)[8], bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                 "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
 }
 
 // Resident CTAs an SM.
@@ -324,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, (quant_blocks<T, SUMS>))
   int ct = (int)at - cur.blk * ctiles;
   const int t = threadIdx.x, l = t & 7;
   const int cp = t & 63, quarter = t >> 6, r0 = quarter * 32;
+  const bool whole = (reinterpret_cast<uintptr_t>(a.qt) & 31) == 0;  // what is added to qt below is a multiple of 32
 
   Chunk<T> k[4][2];  // rows t / 8 + 32 i, columns 8 l and 64 + 8 l
   const size_t x_step = 32 * (size_t)a.row_stride, q_pitch = (size_t)ctiles * kTile;
@@ -471,11 +478,11 @@ __global__ void __launch_bounds__(kThreads, (quant_blocks<T, SUMS>))
       if (c >= a.C) continue;
       if (a.offsets) {
         // Block by block, [blocks][C][128], the exponents in fours, [blocks / 4][C][4].
-        st_sector(a.qt + ((size_t)blk * a.C + c) * kTile + r0, o);
+        st_sector(a.qt + ((size_t)blk * a.C + c) * kTile + r0, o, whole);
         if (quarter == 0) a.et[((size_t)(blk >> 2) * a.C + c) * 4 + (blk & 3)] = (uint8_t)e;
       } else {
         const size_t cr = (size_t)g * a.C + c;
-        st_sector(a.qt + cr * a.tp + (size_t)b * kTile + r0, o);
+        st_sector(a.qt + cr * a.tp + (size_t)b * kTile + r0, o, whole);
         if (quarter == 0) {
           uint8_t* ex = a.et + cr * a.tep;
           ex[b] = (uint8_t)e;
