@@ -19,6 +19,7 @@
 #include "launch.cuh"
 #include "q8_rows.cuh"
 #include "sparse.h"
+#include "tcgen05.cuh"
 
 namespace rmx {
 namespace {
@@ -156,7 +157,8 @@ template <typename T, int NCH, bool VEC> struct RowRing {
   uint32_t ph;
   bool failed;
 
-  // The bytes of a segment that copies bring, from its first vector on.
+  // The bytes of a segment that copies bring, from its first vector on; 0 where the
+  // segment lies in the tensor's last vector and that is not a whole one.
   __device__ __forceinline__ void range(long long row, size_t& from, uint32_t& bytes) const {
     const size_t b0 = ((size_t)row * C + seg0) * sizeof(T), b1 = b0 + (size_t)seg * sizeof(T);
     from = VEC ? b0 : b0 & ~(size_t)15;
@@ -169,6 +171,10 @@ template <typename T, int NCH, bool VEC> struct RowRing {
     size_t from;
     uint32_t bytes;
     range(row, from, bytes);
+    if (!VEC && bytes == 0) {  // a segment inside the tensor's last vector, where that is not a whole one
+      mbar_arrive(bar);
+      return;
+    }
     mbar_arrive_expect_tx(bar, bytes * (uint32_t)nt);
 #pragma unroll
     for (int i = 0; i < 3; ++i)
@@ -220,7 +226,8 @@ template <typename T, int NCH, bool VEC> struct RowRing {
     range(row, from, bytes);
     const size_t b0 = ((size_t)row * C + seg0) * sizeof(T);
     T* in = stage + (b0 - from) / sizeof(T);
-    const int there = (int)((from + bytes - b0) / sizeof(T)), lane = threadIdx.x & 31;
+    // The elements that copies have brought (none where bytes is 0: from is then at most b0).
+    const int there = bytes == 0 ? 0 : (int)((from + bytes - b0) / sizeof(T)), lane = threadIdx.x & 31;
     if (there < seg) {
       if (there + lane < seg) {
 #pragma unroll
