@@ -6,7 +6,10 @@
 //
 // Bound by HBM: one pass over the data each, the row in registers between its
 // moments and its output.  The moments are taken in two steps (mean, then the
-// squared deviations), so a row far from zero loses nothing.
+// squared deviations), and both directions subtract the mean before they multiply, so
+// a row far from zero loses nothing.  (Float32 rows of mean 1000 and deviation 1: with
+// h * rstd - mean * rstd in one operation xh was off by up to 6e-5, like this by 2e-7.)
+// The backward's outputs take two operations an element, with rstd in the row's means.
 //
 // Measured (GB300, 65,536 rows of 1280 bf16 columns, dropout and residual; a copy
 // moves 6.68 TB/s): forward 108 us (6.2 TB/s), backward 141 us with its column sums
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_layer_norm_bwd(co
   const int first_of_warp = L == 32 ? rib : (threadIdx.x >> 5) * (32 / L);
   for (long long row0 = (long long)blockIdx.x * rpb + rib; row0 - rib + first_of_warp < a.R; row0 += RB * step, slot ^= 1) {
     Chunk<T> cy[RB][NCH], ch[RB][NCH], cd[RB][NCH];
-    float rstd[RB], shift[RB];
+    float rstd[RB], mean[RB];
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       const long long row = row0 + r * step;
@@ -600,13 +603,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_layer_norm_bwd(co
         if (a.dh) cd[r][j] = load_chunk<T, L, VEC>(static_cast<const T*>(a.dh) + at, c_of(j), live ? a.C : 0);
       }
       rstd[r] = live ? a.rstd[row] : 0.f;
-      shift[r] = live ? -a.mean[row] * rstd[r] : 0.f;
+      mean[r] = live ? a.mean[row] : 0.f;
     }
     auto both = [&](int r, int j, float2 (&xh)[4], float2 (&t)[4]) {
       to_pairs(ch[r][j], xh);
       to_pairs(cy[r][j], t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xh[i] = fma2(xh[i], f2(rstd[r]), f2(shift[r]));
+      for (int i = 0; i < 4; ++i) xh[i] = mul2(add2(xh[i], f2(-mean[r])), f2(rstd[r]));
     };
     auto weigh = [&](int j, float2 (&t)[4]) {
       if (!a.gamma) return;
@@ -644,14 +647,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_layer_norm_bwd(co
       const long long row = row0 + r * step;
       const bool live = row < a.R;
       const size_t at = (size_t)(live ? row : 0) * a.C;
-      const float2 c1 = f2(-m[2 * r] * inv_n), c2 = f2(-m[2 * r + 1] * inv_n), rs = f2(rstd[r]);
+      const float2 rs = f2(rstd[r]), c1 = f2(-m[2 * r] * inv_n * rstd[r]), c2 = f2(-m[2 * r + 1] * inv_n * rstd[r]);
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         float2 xh[4], t[4];
         both(r, j, xh, t);
         weigh(j, t);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = mul2(fma2(xh[i], c2, add2(t[i], c1)), rs);
+        for (int i = 0; i < 4; ++i) t[i] = fma2(t[i], rs, fma2(xh[i], c2, c1));
         if (a.dh) {
           float2 d[4];
           to_pairs(cd[r][j], d);
@@ -752,7 +755,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
   int slot = 0;
   float next_rstd = row0 < a.R ? a.rstd[row0] : 0.f, next_mean = row0 < a.R ? a.mean[row0] : 0.f;
   for (long long row = row0; row < a.R; row += ring.step, slot ^= 1) {
-    const float rstd = next_rstd, shift = -next_mean * rstd;
+    const float rstd = next_rstd, mean = next_mean;
     if (row + ring.step < a.R) {
       next_rstd = a.rstd[row + ring.step];
       next_mean = a.mean[row + ring.step];
@@ -766,7 +769,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
       to_pairs(ring.load(in, 1, j), xh[j]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        xh[j][i] = fma2(xh[j][i], f2(rstd), f2(shift));
+        xh[j][i] = mul2(add2(xh[j][i], f2(-mean)), f2(rstd));
         ag[j][i] = fma2(t[j][i], xh[j][i], ag[j][i]);
         ab[j][i] = add2(t[j][i], ab[j][i]);
       }
@@ -784,13 +787,13 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1)
     }
     float m[2] = {m1.x + m1.y, m2.x + m2.y};
     row_sums<32, 2>(m, my_red, slot, w, W, 1 + rib);
-    const float2 c1 = f2(-m[0] * inv_n), c2 = f2(-m[1] * inv_n), rs = f2(rstd);
+    const float2 rs = f2(rstd), c1 = f2(-m[0] * inv_n * rstd), c2 = f2(-m[1] * inv_n * rstd);
     const size_t at = (size_t)row * a.C;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const int c0 = seg0 + col0<32, VEC>(j, lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t[j][i] = mul2(fma2(xh[j][i], c2, add2(t[j][i], c1)), rs);
+      for (int i = 0; i < 4; ++i) t[j][i] = fma2(t[j][i], rs, fma2(xh[j][i], c2, c1));
       if (a.dh) {
         float2 d[4];
         to_pairs(ring.load(in, 2, j), d);
