@@ -293,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, (quant_blocks<T, SUMS>))
   T* tile = reinterpret_cast<T*>(smem_q);  // [128][128]
   int* first = reinterpret_cast<int*>(tile + kTile * kTile);  // ragged: [G + 1] and [G + 1]
   int* before = first + a.G + 1;
-  __shared__ uint32_t ctop[4][kTile];
-  __shared__ float csum[4][kTile];
+  __shared__ __align__(8) uint32_t ctop[4][kTile];  // read and written in pairs
+  __shared__ __align__(8) float csum[4][kTile];
   uint32_t blocks = (uint32_t)a.blocks;
   if (a.offsets) {
     ragged_scan<kThreads>(a.offsets, a.G, a.M, kTile, first, before);
