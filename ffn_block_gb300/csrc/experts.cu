@@ -533,6 +533,20 @@ cudaError_t combine(const Routes& r, const int32_t* position, const float* weigh
   }
   return go(k_combine<T, 32, VEC>, units_of<32>(r.T, r.C), 8);
 }
+// Blocks of 256 columns that a warp of k_combine_bwd takes of a token's row of `blocks`
+// of them, more than one.  16-bit types: as few warps as five blocks each allow, the
+// blocks shared evenly (us, 240 MB of experts' rows, four a warp / like this: 512
+// columns 176 / 103, 600 166 / 109, 1536 148 / 98, 2560 133 / 106, 8192 129 / 122; 1280
+// as two warps of three 105, as one of five 103; 64 tokens 4 in all of them).  Float32:
+// four, but five where the row is then one warp's (1280 columns, 23,437 tokens 103 / 89;
+// 64 tokens 3.8 / 5.6).  Fewer blocks or five elsewhere win and lose there: two for
+// 512 columns 58,593 tokens 107 / 93, 2000 tokens 4.8 / 6.6; five for 2560 columns
+// 11,718 tokens 105 / 90, 64 tokens 3.9 / 5.8.
+template <typename T> int bwd_blocks(int blocks) {
+  if (sizeof(T) == 4) return blocks == 5 ? 5 : 4;
+  const int warps = (blocks + 4) / 5;
+  return (blocks + warps - 1) / warps;
+}
 template <typename T, bool VEC>
 cudaError_t combine_bwd(const Routes& r, const int32_t* position, const float* weight, const void* dout, const void* y,
                         void* dy, float* dweight, cudaStream_t st) {
@@ -547,8 +561,13 @@ cudaError_t combine_bwd(const Routes& r, const int32_t* position, const float* w
   if (r.C <= 64) return go(k_combine_bwd<T, 8, 1, VEC>, 8, 1);
   if (r.C <= 128) return go(k_combine_bwd<T, 16, 1, VEC>, 16, 1);
   if (blocks <= 1) return go(k_combine_bwd<T, 32, 1, VEC>, 32, 1);
-  if (blocks == 5) return go(k_combine_bwd<T, 32, 5, VEC>, 32, 5);
-  return go(k_combine_bwd<T, 32, 4, VEC>, 32, 4);
+  const int nch = bwd_blocks<T>(blocks);
+  if constexpr (sizeof(T) == 2) {
+    if (nch == 2) return go(k_combine_bwd<T, 32, 2, VEC>, 32, 2);
+    if (nch == 3) return go(k_combine_bwd<T, 32, 3, VEC>, 32, 3);
+  }
+  if (nch == 4) return go(k_combine_bwd<T, 32, 4, VEC>, 32, 4);
+  return go(k_combine_bwd<T, 32, 5, VEC>, 32, 5);
 }
 
 }  // namespace
