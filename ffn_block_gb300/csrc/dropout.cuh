@@ -31,28 +31,20 @@ __device__ __forceinline__ DropBits drop_bits(const Drop& d) {
 }
 
 // The eight columns 8 * grp .. 8 * grp + 7 of a row: 16 bits each, two to a word,
-// the lower half first.  N groups, round by round: they share the keys, and fill
-// one another's latency.
-template <int N>
-__device__ __forceinline__ void bits8(const DropBits& b, const long long (&row)[N], const int (&grp)[N], uint32_t (&c)[N][4]) {
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    c[n][0] = (uint32_t)grp[n] | (uint32_t)(row[n] >> 32) << 24;
-    c[n][1] = (uint32_t)row[n];
-    c[n][2] = b.o0;
-    c[n][3] = b.o1;
-  }
+// the lower half first.
+__device__ __forceinline__ void bits8(const DropBits& b, long long row, int grp, uint32_t (&c)[4]) {
+  c[0] = (uint32_t)grp | (uint32_t)(row >> 32) << 24;
+  c[1] = (uint32_t)row;
+  c[2] = b.o0;
+  c[3] = b.o1;
   uint32_t k0 = b.k0, k1 = b.k1;
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const uint64_t p0 = (uint64_t)c[n][0] * 0xD2511F53u, p1 = (uint64_t)c[n][2] * 0xCD9E8D57u;
-      c[n][0] = (uint32_t)(p1 >> 32) ^ c[n][1] ^ k0;
-      c[n][1] = (uint32_t)p1;
-      c[n][2] = (uint32_t)(p0 >> 32) ^ c[n][3] ^ k1;
-      c[n][3] = (uint32_t)p0;
-    }
+    const uint64_t p0 = (uint64_t)c[0] * 0xD2511F53u, p1 = (uint64_t)c[2] * 0xCD9E8D57u;
+    c[0] = (uint32_t)(p1 >> 32) ^ c[1] ^ k0;
+    c[1] = (uint32_t)p1;
+    c[2] = (uint32_t)(p0 >> 32) ^ c[3] ^ k1;
+    c[3] = (uint32_t)p0;
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
@@ -68,9 +60,9 @@ __device__ __forceinline__ uint32_t keep_mask(const DropBits& b, const uint32_t 
 }
 // Which of one group's are kept, a bit each.
 __device__ __forceinline__ uint32_t keep8(const DropBits& b, long long row, int grp) {
-  uint32_t w[1][4];
-  bits8<1>(b, {row}, {grp}, w);
-  return keep_mask(b, w[0]);
+  uint32_t w[4];
+  bits8(b, row, grp, w);
+  return keep_mask(b, w);
 }
 // v * scale where kept, exactly 0 elsewhere.
 __device__ __forceinline__ void drop_by_words(const DropBits& b, float scale, const uint32_t (&w)[4], float2 (&v)[4]) {
@@ -95,9 +87,9 @@ __device__ __forceinline__ void drop_values(const DropBits& b, float scale, long
     return;
   }
   if constexpr (VEC) {
-    uint32_t w[1][4];
-    bits8<1>(b, {row}, {c0 >> 3}, w);
-    drop_by_words(b, scale, w[0], v);
+    uint32_t w[4];
+    bits8(b, row, c0 >> 3, w);
+    drop_by_words(b, scale, w, v);
   } else {
     const int sub = threadIdx.x & 7;
     const uint32_t mine = keep8(b, row, (c0 + L * sub) >> 3);

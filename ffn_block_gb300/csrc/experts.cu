@@ -572,8 +572,7 @@ cudaError_t combine_bwd(const Routes& r, const int32_t* position, const float* w
 
 }  // namespace
 
-int sort_warps(int S, int E) {
-  (void)E;
+int sort_warps(int S) {
   if (S <= kClusterSlots) return 0;
   const int share = share_of(S);
   return (int)(((long long)S + share - 1) / share);
@@ -581,7 +580,7 @@ int sort_warps(int S, int E) {
 
 cudaError_t launch_expert_sort(const Routes& r, const int32_t* expert, int32_t* offsets, int32_t* position,
                                int32_t* source, int32_t* ws, int pass, cudaStream_t st) {
-  const int warps = sort_warps(r.S, r.E), E = r.E;
+  const int warps = sort_warps(r.S), E = r.E;
   if (warps == 0) {
     const bool one = r.S <= kOneSlots;
     // A warp to every 32 slots, up to what the CTAs have.

@@ -58,8 +58,9 @@ struct Routes {
   int T, k, E, C, dtype;
   int S;  // T * k
 };
-// Warps that share the counting of a large sort; 0: one CTA sorts by itself.
-int sort_warps(int S, int E);
+// Warps that share the counting of a sort of three launches; 0: one launch sorts, of a
+// CTA or a cluster.
+int sort_warps(int S);
 cudaError_t launch_expert_sort(const Routes& r, const int32_t* expert, int32_t* offsets, int32_t* position,
                                int32_t* source, int32_t* ws, int pass, cudaStream_t st);
 cudaError_t launch_expert_gather(const Routes& r, const int32_t* source, const void* x, void* out, cudaStream_t st);
@@ -99,7 +100,7 @@ struct QuantGroups {
   const void* x;
   uint8_t *q, *e, *qt, *et;
   long long q_row, q_group;            // rows of q between rows and groups
-  int tp, tep;                         // pitches of qt and et
+  int tp, tep;                         // pitches of qt and et (not with offsets)
   float* part;                         // column sums [blocks][C], may be null
   void* sums;
 };

@@ -149,7 +149,7 @@ rmx_status rmx_layer_norm_backward(const rmx_rows* shape, const rmx_drop* drop, 
 
 size_t rmx_expert_sort_workspace_bytes(const rmx_routes* routes) {
   if (!routes_ok(routes)) return 0;
-  const long long warps = sort_warps(routes->tokens * routes->k, routes->experts);
+  const long long warps = sort_warps(routes->tokens * routes->k);
   return up256((size_t)(warps + 1) * routes->experts * sizeof(int32_t));
 }
 
@@ -164,7 +164,7 @@ rmx_status rmx_expert_sort(const rmx_routes* routes, const int32_t* expert, int3
   if (ws_bytes < rmx_expert_sort_workspace_bytes(routes)) return RMX_ERR_WORKSPACE;
   const Routes r = routes_of(routes);
   static const char* const kNames[3] = {"expert_count", "expert_scan", "expert_place"};
-  const bool one = sort_warps(r.S, r.E) == 0;
+  const bool one = sort_warps(r.S) == 0;
   for (int pass = 0; pass < (one ? 1 : 3); ++pass) {
     Launch l(one ? "expert_sort" : kNames[pass], st);
     RMX_TRY(l.done(launch_expert_sort(r, expert, offsets, position, source, static_cast<int32_t*>(ws), pass, st)));
@@ -297,8 +297,10 @@ rmx_status rmx_quant_f8_groups(const rmx_groups* groups, int format, const int32
   a.q_group = tokens ? 1 : ragged ? 0 : g.M;
   a.row_stride = a.q_row * g.C;
   a.group_stride = a.q_group * g.C;
-  a.tp = ragged ? a.blocks * kF8Block : f8_pitch(g.M);
-  a.tep = ragged ? (a.blocks + 3) / 4 * 4 : f8_exps(g.M);
+  if (!ragged) {
+    a.tp = f8_pitch(g.M);
+    a.tep = f8_exps(g.M);
+  }
   {
     Launch l("quant_f8_groups", st);
     RMX_TRY(l.done(launch_quant_f8_groups(a, st)));
