@@ -549,8 +549,8 @@ cudaError_t dispatch(bool pair, int mode, const CUtensorMap& w, const CUtensorMa
 // most SMs idle; a step takes about 0.23 us, and sharing costs about 0.6 us and, for
 // each token, 0.035, 0.022 or 0.016 us with two, four or eight CTAs (two cluster
 // barriers, and the sums' way through distributed shared memory).  36 clusters of
-// four, 76 of two and 15 of eight fit the GPU at once.  us, one CTA / two / four /
-// eight to a tile:
+// four, 76 of two and 15 of eight fit the GPU at once; two are taken up to 72 tiles,
+// about what was measured.  us, one CTA / two / four / eight to a tile:
 //   15 tiles: 1 token 4096 -> 1920 11.4 / 9.2 / 7.5 / 6.2, 224 tokens 1024 -> 1920
 //   6.4 / 14.0 / 10.5 / 9.1, 4096 -> 1920 13.1 / 17.6 / 13.0 / 10.5
 //   32 tiles: 8 tokens 4096 -> 4096 11.3 / 9.3 / 7.8, 200 tokens 12.8 / 17.0 / 12.6

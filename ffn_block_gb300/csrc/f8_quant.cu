@@ -5,7 +5,8 @@
 // exact, so the only rounding is the conversion to 8 bits.  The exponent comes
 // from the largest magnitude's bits: 448 and 57344 are both 7/8 of a power of
 // two, so e follows from its exponent and from whether its mantissa passes 1.75.
-// Bound by HBM: 16-bit values in, bytes out.
+// Rows alone are bound by HBM (131,072 rows of 1280 bf16 columns 76 us, 99% of the copy
+// rate): 16-bit values in, bytes out.
 
 #include <float.h>
 
@@ -238,12 +239,15 @@ __global__ void __launch_bounds__(256) k_dequant_f8_odd(long long total, int bpr
 }
 
 // ---------------------------------------------------------------- rows and columns
-// A CTA takes tiles of 128 rows of a group by 128 columns through shared memory; the grid is what fits at once.  Row pass: eight lanes a
-// row, straight from the loads (the next tile's are issued before this one's
-// column pass).
+// A CTA takes tiles of 128 rows of a group by 128 columns through shared memory; the
+// grid is what fits at once.  Row pass: eight lanes a row, straight from the loads (the
+// next tile's are issued before this one's column pass).
 // Column pass: a thread two columns of 32 rows, held in registers between the
 // maximum and the conversion; its words in a row of shared memory are its
 // neighbours', without bank conflicts, and it writes whole 32-byte sectors.
+// 32,768 sorted rows of 1280 bf16 columns 42 us, of 2560 with sums 82 (60 to 74% of the
+// copy rate); neither DRAM nor issue is near its limit, so most likely a tile's two
+// block barriers bound it.
 constexpr int kTile = 128, kThreads = 256;
 
 template <typename T> struct Pair2;

@@ -7,13 +7,14 @@
 // Bound by HBM: one pass over the data each, the row in registers between its
 // moments and its output.  The moments are taken in two steps (mean, then the
 // squared deviations), and both directions subtract the mean before they multiply, so
-// a row far from zero loses nothing.  (Float32 rows of mean 1000 and deviation 1: with
-// h * rstd - mean * rstd in one operation xh was off by up to 6e-5, like this by 2e-7.)
+// a row far from zero loses no more than its mean's rounding.  (Float32 rows of mean 1000
+// and deviation 1: with h * rstd - mean * rstd in one operation the backward's xh was off
+// by up to 6e-5, like this by 2e-7.)
 // The backward's outputs take two operations an element, with rstd in the row's means.
 //
 // Measured (GB300, 65,536 rows of 1280 bf16 columns, dropout and residual; a copy
-// moves 6.68 TB/s): forward 108 us (6.2 TB/s), backward 141 us with its column sums
-// (6.0 TB/s), dropout alone 76 us with a residual (6.6 TB/s) and 63 without (5.3:
+// moves 6.68 TB/s): forward 108 us (6.2 TB/s), backward 142 us with its column sums
+// (5.9 TB/s), dropout alone 76 us with a residual (6.6 TB/s) and 63 without (5.3:
 // there the generator's integer operations bound it).
 
 #include "common.cuh"
@@ -303,7 +304,7 @@ RingSpread ring_spread(long long R, int C, int dtype, int nt, int threads, int s
 // 108 us for 65,536 x 1280, when the choice was made 117 (12 warps with them in
 // registers 124, 20 or 24 warps, which spill, 160 and 165; without a ring 130 to
 // 200).  Backward: 8 warps of 255 registers, a row's values kept from its sums to its
-// output: 141 us, then 145 (12 warps that work them out again 176, without a ring 350).
+// output: 142 us, then 145 (12 warps that work them out again 176, without a ring 350).
 constexpr int kFwdRingThreads = 512, kBwdRingThreads = 256;
 template <typename T, int NCH, bool VEC>
 __global__ void __launch_bounds__(kFwdRingThreads, 1)

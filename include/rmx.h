@@ -463,7 +463,8 @@ rmx_status rmx_dropout(const rmx_rows* shape, const rmx_drop* drop, const void* 
  * be null.  The sum, the statistics and y are float32; the norm is taken of the
  * unrounded sum.  Outputs: h and y in the storage type, mean, rstd [rows]
  * float32; h, mean and rstd may be null.  h may be x or r itself.  A constant
- * row with eps 0 has an infinite rstd and y NaN.  cols <= 16384. */
+ * row's deviations are what its mean's rounding leaves: with eps 0 and an exact
+ * mean rstd is infinite and y NaN.  cols <= 16384. */
 rmx_status rmx_layer_norm(const rmx_rows* shape, float eps, const rmx_drop* drop, const void* x, const void* r,
                           const void* gamma, const void* beta, void* h, void* y, float* mean, float* rstd,
                           rmx_stream stream);
@@ -473,8 +474,9 @@ rmx_status rmx_layer_norm(const rmx_rows* shape, float eps, const rmx_drop* drop
  *   dr = rstd * (t - mean(t) - xh * mean(t * xh)) + dh
  *   dx = drop(dr),  dgamma = sum over rows of dy * xh,  dbeta = sum of dy
  * dr is the gradient of the sum h and of r.  dh: the gradient that reaches h
- * from elsewhere (may be null).  dx, dgamma and dbeta may be null; drop, with the
- * forward's p and state, is only read where dx is given.  dr may be dy or dh.
+ * from elsewhere (may be null).  dx, dgamma and dbeta may be null.  drop has the
+ * forward's p and state: the state is only read where dx is given, a p outside
+ * [0, 1] is refused always.  dr may be dy or dh.
  * ws: rmx_layer_norm_backward_workspace_bytes.  rows == 0 writes zero dgamma
  * and dbeta.  cols <= 16384. */
 size_t rmx_layer_norm_backward_workspace_bytes(const rmx_rows* shape);
@@ -503,8 +505,8 @@ rmx_status rmx_expert_sort(const rmx_routes* routes, const int32_t* expert, int3
 
 /* The tokens' rows in sorted order: out[i] = x[source[i] / k], x [tokens, cols],
  * out [tokens * k, cols]; also or instead as 8-bit rows q, exps (see below) of
- * the given rmx_f8 format.  Rows without a source are left as they were.  out, or
- * q and exps, may be null. */
+ * the given rmx_f8 format (one of the two also where q is null).  Rows without a
+ * source are left as they were.  out, or q and exps, may be null. */
 rmx_status rmx_expert_gather(const rmx_routes* routes, const int32_t* source, const void* x, void* out, int format,
                              uint8_t* q, uint8_t* exps, rmx_stream stream);
 
